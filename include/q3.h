@@ -68,6 +68,13 @@ extern "C" {
 #define Q3_Q8_0_BYTES 34     /* bytes per canonical Q8_0 block */
 #define Q3_AFFINE4_GROUP 32  /* weights per AFFINE4_GS32 group */
 #define Q3_AFFINE4_BYTES 20  /* bytes per AFFINE4_GS32 group */
+#define Q3_KV4_TILE_BYTES 2560 /* 32 positions of K or V of one head in the 4-bit cache */
+#define Q3_LOGPROB_MAX_TOP 32  /* most alternatives q3_op_token_logprobs returns */
+
+/* Element types of the operators that take more than one. */
+#define Q3_TYPE_F32 0
+#define Q3_TYPE_F16 1
+#define Q3_TYPE_BF16 2
 
 /* Device status-word bits (q3_sync reports them as Q3_ERR_DEVICE_CHECK). */
 #define Q3_STATUS_TOKEN_RANGE 0x1   /* a token id outside [0, vocab) */
@@ -383,6 +390,113 @@ int q3_op_matvec_affine4(const void* groups_dev, const float* x_dev, int M, int 
 int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t* table_dev, int n_table,
                             int n_blocks, int pos0, int T, int n_q, int n_kv, void* out_dev, int use_tc,
                             void* stream);
+
+/* ---- Operators of the 4-bit K/V cache and of token scoring ----
+ * Unlike the gates above these serve callers that run their own layers: they
+ * allocate nothing, are asynchronous on stream, may be captured into a CUDA
+ * graph and keep no state between calls.  What a kernel finds wrong (a block
+ * id outside the pool, a value beyond the fp16 range) it reports by OR-ing
+ * Q3_STATUS_* bits into *status_dev, an int32 the caller owns, clears and
+ * reads when it likes, or NULL.  Arguments the host can see are refused with
+ * Q3_ERR_INVALID_ARG before anything is launched; zero rows are Q3_OK and
+ * launch nothing.  The caller's buffers are those of the current device.
+ * The Kipp pages have no counterpart beyond "Kipp Roadmap", status v0.0.4 (a
+ * quantized cache is opt-in) and "Kipp Model Support", section "Quantization
+ * (AFFINE4_GS32)", whose rule packs the rows.
+ *
+ * The cache.  kv_dev is [n_blocks][2][n_kv] tiles of Q3_KV4_TILE_BYTES (K,
+ * then V), 16-byte aligned: 32 positions of one KV head, each head row of 128
+ * packed by the AFFINE4_GS32 rule straight from FP32 (q3_quantize_affine4's,
+ * groups of 32 dimensions), 80 bytes a position and head.  A stored value is
+ * fp16(scale * code + bias), rounded once.
+ *   K tile: 16 code bytes [position][group], dimension i of a group in bits
+ *     4 i (low nibble first); from byte 2,048 fp16 (scale, bias)
+ *     [position][group].
+ *   V tile: 16-bit words [position / 2][g < 8][group][position % 2] holding
+ *     dimension 32 group + 4 g + i in bits 4 i; from byte 2,048 fp16
+ *     [position / 2][group][scale even, scale odd, bias even, bias odd].
+ * tables_dev: int32 [n_slots][max_blocks], the physical block of each 32
+ * positions of a slot.  Sizes: 1 <= n_kv, n_q a multiple of n_kv and at most
+ * 8 n_kv, 1 <= n_blocks, n_slots, max_blocks; max_blocks at most 2^20.
+ *
+ * q3_op_kv4_append: per row t of projections (n_q q heads, then n_kv k heads,
+ * then n_kv v heads of 128) at position row_pos_dev[t] of slot
+ * row_slot_dev[t]: q and k heads get the head RMSNorm (bf16 [128] gains) and
+ * rotate-half RoPE, q goes to q_out_dev (fp16 [T][n_q][128], or NULL), k and v
+ * are packed into the cache.  qkv_dev: qkv_type (f32, fp16 or bf16), rows
+ * qkv_stride elements apart (>= (n_q + 2 n_kv) * 128, a multiple of 4 for f32
+ * and of 8 otherwise; 16-byte aligned).  rope_dev: f32 [rope_len][64][2] (cos,
+ * sin) of position * theta^(-2i/128), 16-byte aligned.  kv_out_dev: fp16
+ * [T][2][n_kv][128] or NULL, receives the values the cache then holds.  A row
+ * with a negative position is padding: the cache is left alone and its output
+ * rows are zeros.  Two rows of a call must not name the same place.  Status:
+ * Q3_STATUS_BLOCK_RANGE (a slot, table entry or position outside its range;
+ * the row's K and V are then not stored), Q3_STATUS_F16_RANGE (|k| or |v|
+ * above 65,000 or |q| above 65,504, or not a number).
+ * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_kv4_append(const void* qkv_dev, int qkv_type, int64_t qkv_stride, const void* q_gain_dev,
+                     const void* k_gain_dev, float eps, const float* rope_dev, int rope_len,
+                     const int32_t* row_pos_dev, const int32_t* row_slot_dev, int T, int n_q, int n_kv,
+                     const int32_t* tables_dev, int n_slots, int max_blocks, void* kv_dev, int n_blocks,
+                     void* q_out_dev, void* kv_out_dev, int32_t* status_dev, void* stream);
+
+/* q3_op_kv4_decode_attention: GQA attention of rows that each stand at their
+ * own position of their own slot (the new tokens of a batch of sessions, or
+ * several rows of one): out[t][h] = sum_j softmax_j(q[t][h] . K[j] /
+ * sqrt(128)) V[j] over the slot's positions j <= row_pos_dev[t], which the
+ * cache must hold.  A negative position attends nothing: zeros.  q_dev: f32 or
+ * fp16, rows q_stride elements apart (>= n_q * 128, a multiple of 4 or 8;
+ * 16-byte aligned).  out_dev: f32 or fp16 [T][n_q][128].  max_ctx: the longest
+ * context the caller expects, 1 .. 32 max_blocks, or 0 for 32 max_blocks; it
+ * only chooses how contexts are split over the GPU, never the result's
+ * meaning.  Positions past a row's own are not read into the result, whatever
+ * their bytes hold.  Status: Q3_STATUS_BLOCK_RANGE (a slot, table entry or
+ * position outside its range: what it names is left out), Q3_STATUS_F16_RANGE.
+ * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, const int32_t* row_pos_dev,
+                               const int32_t* row_slot_dev, int T, int n_q, int n_kv, const int32_t* tables_dev,
+                               int n_slots, int max_blocks, int max_ctx, const void* kv_dev, int n_blocks,
+                               void* out_dev, int out_type, int32_t* status_dev, void* stream);
+
+/* q3_op_kv4_prefill_attention: causal GQA attention of ns sequences of rows.
+ * Sequence i is rows seq_rows_dev[i] .. seq_rows_dev[i + 1] - 1 (int32 [ns +
+ * 1], not decreasing, within [0, T]; a sequence may be empty) at positions
+ * seq_pos_dev[i] .. of slot seq_slot_dev[i] (NULL: slot i); each row attends
+ * the slot's positions up to its own, which the cache must hold (the round's
+ * rows are appended first).  Rows of no sequence keep their output; rows of
+ * negative position get zeros.  q_dev: fp16 rows q_stride elements apart (>=
+ * n_q * 128, a multiple of 8; 16-byte aligned); out_dev: fp16 [T][n_q][128],
+ * 16-byte aligned.  workspace_dev: q3_kv4_prefill_workspace bytes, 256-byte
+ * aligned, needing no preparation; calls that may overlap on the GPU take one
+ * each.  Status as q3_op_kv4_decode_attention, and Q3_STATUS_TIMEOUT.
+ * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32_t* seq_rows_dev,
+                                const int32_t* seq_pos_dev, const int32_t* seq_slot_dev, int ns, int T, int n_q,
+                                int n_kv, const int32_t* tables_dev, int n_slots, int max_blocks, const void* kv_dev,
+                                int n_blocks, void* out_dev, void* workspace_dev, int64_t workspace_bytes,
+                                int32_t* status_dev, void* stream);
+/* Bytes of workspace for these sizes.  Host only.  Errors: Q3_ERR_INVALID_ARG. */
+int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int n_blocks, int64_t* bytes);
+
+/* q3_op_token_logprobs: for each of N rows of V logits (f32, fp16 or bf16;
+ * rows stride elements apart, stride >= V, any alignment of the type):
+ *   logprob_dev[r] = x[target] - lse, lse = log sum_i exp(x_i); a target of -1
+ *     means none: 0;
+ *   entropy_dev[r] = -sum_i p_i log p_i in nats;
+ *   top_ids_dev[r][k], top_logprob_dev[r][k], k < top_k: the most probable
+ *     tokens in order (the lowest index first among equal logits) and their
+ *     log probabilities.
+ * Any output may be NULL; targets_dev (int32 [N]) may be NULL with
+ * logprob_dev.  A logit of -inf is a token of probability 0 and adds nothing
+ * to the entropy; a row of -inf alone gives log probabilities of -inf and
+ * entropy 0.  A row holding +inf or a NaN gives NaN log probabilities and
+ * entropy; NaN ranks after every number.  0 <= top_k <= min(V,
+ * Q3_LOGPROB_MAX_TOP).  Status: Q3_STATUS_TOKEN_RANGE (a target below -1 or
+ * past V: its log probability is NaN).
+ * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N, int V, const int32_t* targets_dev,
+                         int top_k, float* logprob_dev, float* entropy_dev, int32_t* top_ids_dev,
+                         float* top_logprob_dev, int32_t* status_dev, void* stream);
 
 /* Split-K matmul that allocates nothing (the Kipp pages have no counterpart;
  * this entry point serves callers that cannot call cudaMalloc where they need

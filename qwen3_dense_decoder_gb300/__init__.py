@@ -107,6 +107,12 @@ def lib():
         L.q3_op_kv_pack_q8_0.argtypes = [vp, i, vp, vp]
         L.q3_op_matvec_affine4.argtypes = [vp, vp, i, i, vp, vp]
         L.q3_model_prefill_tc.argtypes = [vp]
+        f = C.c_float
+        L.q3_op_kv4_append.argtypes = [vp, i, i64, vp, vp, f, vp, i, vp, vp, i, i, i, vp, i, i, vp, i, vp, vp, vp, vp]
+        L.q3_op_kv4_decode_attention.argtypes = [vp, i, i64, vp, vp, i, i, i, vp, i, i, i, vp, i, vp, i, vp, vp]
+        L.q3_kv4_prefill_workspace.argtypes = [i, i, i, i, i, C.POINTER(i64)]
+        L.q3_op_kv4_prefill_attention.argtypes = [vp, i64, vp, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, vp, i64, vp, vp]
+        L.q3_op_token_logprobs.argtypes = [vp, i, i64, i, i, vp, i, vp, vp, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -292,6 +298,213 @@ def op_prefill_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor,
                                          pos0, T, n_q, n_kv, _ptr(out), 1 if use_tc else 0,
                                          _stream_handle(stream)))
     return out
+
+
+# ---------------------------------------------------------------- 4-bit K/V cache, token scoring
+# These operators allocate nothing in the library and do not wait: outputs the
+# caller does not pass come from torch's allocator, everything runs on
+# `stream` (default: the current stream of the tensors' device), and what a
+# kernel finds wrong is OR-ed into `status` (int32 [1]; check_status raises).
+
+KV4_TILE = 2560
+LOGPROB_MAX_TOP = 32
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _need(ok: bool, msg: str) -> None:
+    if not ok:
+        raise ValueError(msg)
+
+
+class _On:
+    """The device of an operator's tensors made current, with the stream to
+    launch on; the tensors are kept from reuse until that stream is done."""
+
+    def __init__(self, name: str, stream, *tensors):
+        self.name = name
+        ts = [t for t in tensors if t is not None]
+        self.device = ts[0].device
+        for t in ts:
+            if t.device.type != "cuda" or t.device != self.device:
+                raise ValueError(f"{name}: tensors must be on one CUDA device")
+        self.index = self.device.index
+        self.tensors = ts
+        self.stream = stream
+
+    def call(self, fn, *args) -> None:
+        before = torch.cuda.current_device()
+        if before != self.index:
+            torch.cuda.set_device(self.index)
+        try:
+            current = torch.cuda.current_stream()
+            s = self.stream or current
+            if s.device.index != self.index:
+                raise ValueError(f"{self.name}: the stream is another device's")
+            rc = fn(*args, C.c_void_p(s.cuda_stream))
+            if s != current:
+                for t in self.tensors:
+                    t.record_stream(s)
+        finally:
+            if before != self.index:
+                torch.cuda.set_device(before)
+        _check(rc)
+
+
+def check_status(status: torch.Tensor) -> None:
+    """Read and clear an operator's status word; Q3Error if a kernel set it.  Synchronises."""
+    word = int(status.item())
+    if word:
+        status.zero_()
+        raise Q3Error(-7, f"device check failed (status 0x{word:x})")
+
+
+def _int32(name: str, what: str, t: torch.Tensor, shape: tuple) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be contiguous int32 {list(shape)}")
+
+
+def _kv4_pool(name: str, kv: torch.Tensor, tables: torch.Tensor, status) -> tuple[int, int]:
+    _need(kv.dtype == torch.uint8 and kv.dim() == 4 and kv.shape[1] == 2 and kv.shape[3] == KV4_TILE and kv.is_contiguous(),
+          f"{name}: kv must be contiguous uint8 [n_blocks, 2, n_kv, {KV4_TILE}]")
+    _need(tables.dtype == torch.int32 and tables.dim() == 2 and tables.is_contiguous(),
+          f"{name}: tables must be contiguous int32 [n_slots, max_blocks]")
+    if status is not None:
+        _int32(name, "status", status, (1,))
+    return kv.shape[0], kv.shape[2]
+
+
+def _out(name: str, out, shape: tuple, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(tuple(out.shape) == shape and out.dtype == dtype and out.is_contiguous(), f"{name}: outputs must be contiguous {dtype} {list(shape)}")
+    return out
+
+
+def rope_table(n: int, theta: float, device="cuda") -> torch.Tensor:
+    """(cos, sin) of position * theta^(-2i/128) for positions below n: f32 [n, 64, 2], the angles in 64 bits."""
+    inv = torch.pow(torch.tensor(theta, dtype=torch.float64), -torch.arange(0, 128, 2, dtype=torch.float64) / 128)
+    a = torch.arange(n, dtype=torch.float64).unsqueeze(1) * inv
+    return torch.stack((a.cos(), a.sin()), -1).float().to(device)
+
+
+def op_kv4_append(qkv: torch.Tensor, q_gain: torch.Tensor, k_gain: torch.Tensor, rope: torch.Tensor,
+                  row_pos: torch.Tensor, row_slot: torch.Tensor, tables: torch.Tensor, kv: torch.Tensor, n_q: int,
+                  eps: float = 1e-6, q_out: torch.Tensor | None = None, kv_out: torch.Tensor | None = None,
+                  status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Norm and rotate the q and k heads of projection rows qkv [T, (n_q + 2
+    n_kv) * 128] (f32, fp16 or bf16; rows may be strided), return q as fp16 [T,
+    n_q, 128] and pack k and v into the 4-bit cache kv (uint8 [n_blocks, 2,
+    n_kv, 2560]) at each row's position and slot.  rope: rope_table's; a row
+    of negative position is padding.  kv_out: fp16 [T, 2, n_kv, 128], if given,
+    receives the values the cache then holds."""
+    name = "op_kv4_append"
+    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
+    T = qkv.shape[0]
+    _need(qkv.dim() == 2 and qkv.dtype in _TYPES and qkv.shape[1] == (n_q + 2 * n_kv) * 128 and qkv.stride(1) == 1,
+          f"{name}: qkv must be f32, fp16 or bf16 [T, (n_q + 2 n_kv) * 128]")
+    _need(all(g.dtype == torch.bfloat16 and g.shape == (128,) and g.is_contiguous() for g in (q_gain, k_gain)),
+          f"{name}: gains must be bf16 [128]")
+    _need(rope.dtype == torch.float32 and rope.dim() == 3 and rope.shape[1:] == (64, 2) and rope.is_contiguous(),
+          f"{name}: rope must be f32 [n, 64, 2]")
+    _int32(name, "row_pos", row_pos, (T,))
+    _int32(name, "row_slot", row_slot, (T,))
+    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv.device)
+    if kv_out is not None:
+        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv.device)
+    on = _On(name, stream, qkv, q_gain, k_gain, rope, row_pos, row_slot, tables, kv, q_out, kv_out, status)
+    on.call(lib().q3_op_kv4_append, _ptr(qkv), _TYPES[qkv.dtype], qkv.stride(0) if T > 1 else qkv.shape[1], _ptr(q_gain),
+            _ptr(k_gain), eps, _ptr(rope), rope.shape[0], _ptr(row_pos), _ptr(row_slot), T, n_q, n_kv, _ptr(tables),
+            tables.shape[0], tables.shape[1], _ptr(kv), n_blocks, _ptr(q_out), _ptr(kv_out), _ptr(status))
+    return q_out
+
+
+def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: torch.Tensor, tables: torch.Tensor,
+                            kv: torch.Tensor, max_ctx: int = 0, out: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """GQA attention of rows q [T, n_q, 128] (f32 or fp16; rows may be strided)
+    over the 4-bit cache, each at its own position of its own slot: [T, n_q,
+    128], fp16 unless out is f32.  A row of negative position gives zeros.
+    max_ctx: the longest context expected (0: what the tables hold); it chooses
+    the split of the work only."""
+    name = "op_kv4_decode_attention"
+    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
+    _need(q.dim() == 3 and q.shape[2] == 128 and q.dtype in (torch.float32, torch.float16) and q.stride(2) == 1 and q.stride(1) == 128,
+          f"{name}: q must be f32 or fp16 [T, n_q, 128] with contiguous rows")
+    T, n_q, _ = q.shape
+    _int32(name, "row_pos", row_pos, (T,))
+    _int32(name, "row_slot", row_slot, (T,))
+    out = _out(name, out, (T, n_q, 128), torch.float16 if out is None or out.dtype != torch.float32 else torch.float32, q.device)
+    on = _On(name, stream, q, row_pos, row_slot, tables, kv, out, status)
+    on.call(lib().q3_op_kv4_decode_attention, _ptr(q), _TYPES[q.dtype], q.stride(0) if T > 1 else n_q * 128, _ptr(row_pos),
+            _ptr(row_slot), T, n_q, n_kv, _ptr(tables), tables.shape[0], tables.shape[1], max_ctx, _ptr(kv), n_blocks,
+            _ptr(out), _TYPES[out.dtype], _ptr(status))
+    return out
+
+
+def kv4_prefill_workspace(ns: int, T: int, n_q: int, n_kv: int, n_blocks: int) -> int:
+    """Bytes of workspace op_kv4_prefill_attention needs for these sizes.  Host only (no GPU)."""
+    n = C.c_int64()
+    _check(lib().q3_kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks, C.byref(n)))
+    return n.value
+
+
+def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: torch.Tensor, tables: torch.Tensor,
+                             kv: torch.Tensor, seq_slot: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Causal GQA attention over the 4-bit cache of sequences of rows q [T,
+    n_q, 128] fp16: sequence i is rows seq_rows[i] .. seq_rows[i + 1] at
+    positions seq_pos[i] .. of slot seq_slot[i] (default i), whose K and V the
+    cache already holds.  Returns fp16 [T, n_q, 128]; rows of no sequence keep
+    what out held.  workspace: uint8, kv4_prefill_workspace bytes (default:
+    allocated here)."""
+    name = "op_kv4_prefill_attention"
+    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
+    _need(q.dim() == 3 and q.shape[2] == 128 and q.dtype == torch.float16 and q.stride(2) == 1 and q.stride(1) == 128,
+          f"{name}: q must be fp16 [T, n_q, 128] with contiguous rows")
+    T, n_q, _ = q.shape
+    ns = seq_pos.shape[0]
+    _int32(name, "seq_rows", seq_rows, (ns + 1,))
+    _int32(name, "seq_pos", seq_pos, (ns,))
+    if seq_slot is not None:
+        _int32(name, "seq_slot", seq_slot, (ns,))
+    out = _out(name, out, (T, n_q, 128), torch.float16, q.device)
+    need = kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.numel() >= need,
+          f"{name}: workspace must be contiguous uint8, at least {need} bytes")
+    on = _On(name, stream, q, seq_rows, seq_pos, seq_slot, tables, kv, out, workspace, status)
+    on.call(lib().q3_op_kv4_prefill_attention, _ptr(q), q.stride(0) if T > 1 else n_q * 128, _ptr(seq_rows), _ptr(seq_pos),
+            _ptr(seq_slot), ns, T, n_q, n_kv, _ptr(tables), tables.shape[0], tables.shape[1], _ptr(kv), n_blocks, _ptr(out),
+            _ptr(workspace), workspace.numel(), _ptr(status))
+    return out
+
+
+def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0,
+                      status: torch.Tensor | None = None, stream=None):
+    """Of each logits row [N, V] (f32, fp16 or bf16; rows may be strided): the
+    target's log probability (f32 [N]; None without targets; a target of -1
+    gives 0), the entropy in nats (f32 [N]), and the top_k most probable tokens
+    in order, lowest index first among equals (int32 [N, top_k]), with their
+    log probabilities (f32 [N, top_k])."""
+    name = "op_token_logprobs"
+    _need(logits.dim() == 2 and logits.dtype in _TYPES and (logits.shape[1] <= 1 or logits.stride(1) == 1),
+          f"{name}: logits must be f32, fp16 or bf16 [N, V] with contiguous rows")
+    N, V = logits.shape
+    dev = logits.device
+    if targets is not None:
+        _int32(name, "targets", targets, (N,))
+    if status is not None:
+        _int32(name, "status", status, (1,))
+    logprob = None if targets is None else torch.empty(N, dtype=torch.float32, device=dev)
+    entropy = torch.empty(N, dtype=torch.float32, device=dev)
+    ids = torch.empty(N, max(0, top_k), dtype=torch.int32, device=dev)
+    values = torch.empty(N, max(0, top_k), dtype=torch.float32, device=dev)
+    on = _On(name, stream, logits, targets, logprob, entropy, ids, values, status)
+    on.call(lib().q3_op_token_logprobs, _ptr(logits), _TYPES[logits.dtype], logits.stride(0) if N > 1 else V, N, V, _ptr(targets),
+            top_k, _ptr(logprob), _ptr(entropy), _ptr(ids), _ptr(values), _ptr(status))
+    return logprob, entropy, ids, values
 
 
 class Model:

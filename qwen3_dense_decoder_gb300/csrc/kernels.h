@@ -21,6 +21,13 @@ namespace q3 {
 constexpr int KVQ_CODES = 32 * 128;
 constexpr int KVQ_TILE = KVQ_CODES + 32 * 4 * 2;
 
+// ---------------------------------------------------------------- 4-bit K/V cache layout
+// With the opt-in AFFINE4 cache a tile is KV4_TILE bytes: 4-bit codes, then
+// fp16 scales and biases, in the orders kv4.cuh states -- 80 bytes per
+// position and head.
+constexpr int KV4_CODES = 32 * 64;
+constexpr int KV4_TILE = KV4_CODES + 32 * 16;
+
 // ---------------------------------------------------------------- kernel attributes
 // A kernel that takes more than 48 KB of dynamic shared memory must be
 // allowed it on every device it launches on.  `done` keeps one bit per
@@ -299,6 +306,80 @@ cudaError_t launch_argmax(const Launch& L, const float* logits, int rows, int V,
 // Q8_0 K/V rows: n rows of 128 floats packed into canonical Q8_0 blocks (4 x
 // 34 bytes a row: fp16 scale, then 32 codes), by the cache writers' rule.
 cudaError_t launch_kv_pack_q8(cudaStream_t s, const float* rows, int n, uint8_t* out);
+
+// ---------------------------------------------------------------- 4-bit K/V cache
+// The writer: rows of projections (q, k, v heads of 128) -> fp16 q rows, and
+// K/V packed into the rows' places.  A row of negative position is padding:
+// nothing is written to the cache, its q_out and kv_out rows become zeros.
+struct Kv4AppendArgs {
+    const void* qkv;           // [T] rows, qkv_stride elements apart
+    int64_t qkv_stride;
+    const __nv_bfloat16* q_gain;
+    const __nv_bfloat16* k_gain;
+    float eps;
+    const float2* rope;        // [rope_len][64] (cos, sin)
+    int rope_len;
+    const int* row_pos;        // [T]
+    const int* row_slot;       // [T]
+    int T, n_q, n_kv;
+    const int* tables;         // [n_slots][max_blocks]
+    int n_slots, max_blocks;
+    uint8_t* kv;               // [n_blocks][2][n_kv] tiles
+    int n_blocks;
+    __half* q_out;             // [T][n_q][128] or null
+    __half* kv_out;            // [T][2][n_kv][128] the stored values, or null
+    int* status;               // or null
+};
+cudaError_t launch_kv4_append(const Launch& L, const Kv4AppendArgs& a, int type);
+
+// Attention of rows with a position and a slot each, over j <= position.
+struct Kv4DecodeArgs {
+    const void* q;             // [T] rows, q_stride elements apart
+    int64_t q_stride;
+    const int* row_pos;
+    const int* row_slot;
+    int T, n_q, n_kv;
+    const int* tables;
+    int n_slots, max_blocks;
+    int max_ctx;               // the longest context expected (chooses the splits only)
+    const uint8_t* kv;
+    int n_blocks;
+    void* out;                 // [T][n_q][128]
+    int* status;
+};
+cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type);
+
+// Causal attention of sequences of rows: sequence i is rows seq_rows[i] ..
+// seq_rows[i + 1] at positions seq_pos[i] .. of slot seq_slot[i].
+struct Kv4PrefillArgs {
+    const __half* q;
+    int64_t q_stride;
+    const int* seq_rows;       // [ns + 1]
+    const int* seq_pos;        // [ns]
+    const int* seq_slot;       // [ns], or null: i
+    int ns, T, n_q, n_kv;
+    const int* tables;
+    int n_slots, max_blocks;
+    const uint8_t* kv;
+    int n_blocks;
+    __half* out;               // [T][n_q][128]
+    int* status;
+};
+cudaError_t launch_kv4_prefill(const Launch& L, const Kv4PrefillArgs& a);
+
+// ---------------------------------------------------------------- token log probabilities
+struct LogprobArgs {
+    const void* logits;        // [N] rows, stride elements apart
+    int64_t stride;
+    int N, V, top;
+    const int32_t* targets;    // [N], -1: none
+    float* logprob;            // [N] or null
+    float* entropy;            // [N] or null
+    int32_t* top_ids;          // [N][top] or null
+    float* top_logprob;        // [N][top] or null
+    int* status;               // or null
+};
+cudaError_t launch_logprobs(const Launch& L, const LogprobArgs& a, int type);
 
 // Q8_0: canonical blocks -> (int8 plane, fp16 scale plane); planes -> fp16
 // tensor-core operand; bf16 -> canonical blocks.

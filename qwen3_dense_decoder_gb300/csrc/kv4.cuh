@@ -1,0 +1,92 @@
+// kv4.cuh -- the 4-bit K/V cache: its tiles and the packing of head rows.
+//
+// A head row (128 values) is packed by the weights' AFFINE4_GS32 rule ("Kipp
+// Model Support", section "Quantization (AFFINE4_GS32)": 32 values a group,
+// 4-bit codes, an fp16 scale and an fp16 bias) straight from FP32: bias =
+// fp16(min), scale = fp16((max - min) / 15), code = round-half-even((x - bias)
+// / scale) against the stored scale and bias, clamped to [0, 15]; a zero scale
+// gives zero codes.  80 bytes a row against 256 in BF16 and 136 in Q8_0.  A
+// stored value is fp16(scale * code + bias), rounded once.
+//
+// A pool tile is 32 positions of K or V of one KV head, KV4_TILE bytes: codes,
+// then parameters.  The orders are those in which the decode attention's
+// matrix fragments want them, so that every lane reads 16-byte words and one
+// mask of a word gives an fp16 pair:
+//  K  codes [position][group] 16 bytes: dimension i of a group in bits 4 i of
+//     its 128 (the canonical order); (scale, bias) pairs [position][group].
+//     A lane of K's fragment holds one group of a position.
+//  V  codes [position pair][g < 8][group] words: the four dimensions 32 group
+//     + 4 g + i of the even position in bits 4 i, of the odd one in bits
+//     16 + 4 i, so a mask pairs two positions of one dimension, the order of
+//     V's fragment; parameters [position pair][group] (scale even, scale odd,
+//     bias even, bias odd).  A row still owns whole 16-bit words, so appending
+//     a position is plain stores.
+#pragma once
+
+#include "common.cuh"
+
+namespace q3 {
+
+// |x| a packed row may hold: up to here no stored value passes the fp16 range
+constexpr float KV4_MAX = 65000.0f;
+
+// One head row held by a warp, lane l values [4l, 4l + 4): group b is lanes
+// 8b .. 8b + 7.  Returns the lane's four codes (value 4l + i in bits 4 i), its
+// group's scale and bias, and the values the cache then holds.  false in a
+// lane whose values leave the range (or are not numbers).
+Q3_DEV bool kv4_pack(const float (&y)[4], uint32_t& codes, __half& scale, __half& bias, __half (&val)[4]) {
+    float lo = fminf(fminf(y[0], y[1]), fminf(y[2], y[3]));
+    float hi = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    scale = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+    bias = __float2half_rn(lo);
+    const float s = __half2float(scale), b = __half2float(bias);
+    bool ok = true;
+    codes = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        ok = ok && fabsf(y[e]) <= KV4_MAX;
+        int q = 0;
+        if (s != 0.0f) q = (int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y[e], b), s)), 0.0f), 15.0f);
+        codes |= (uint32_t)q << (4 * e);
+        val[e] = __hfma(scale, __int2half_rn(q), bias);
+    }
+    return ok;
+}
+
+// Store a packed row at position r of a pool tile.
+Q3_DEV void kv4_store_k(uint8_t* tile, int r, uint32_t codes, __half scale, __half bias, int lane) {
+    *reinterpret_cast<uint16_t*>(tile + r * 64 + lane * 2) = (uint16_t)codes;
+    if ((lane & 7) == 0)
+        *reinterpret_cast<__half2*>(tile + KV4_CODES + r * 16 + (lane >> 3) * 4) = __halves2half2(scale, bias);
+}
+Q3_DEV void kv4_store_v(uint8_t* tile, int r, uint32_t codes, __half scale, __half bias, int lane) {
+    const int g = lane & 7, grp = lane >> 3;
+    *reinterpret_cast<uint16_t*>(tile + (r >> 1) * 128 + g * 16 + grp * 4 + (r & 1) * 2) = (uint16_t)codes;
+    if (g == 0) {
+        __half* par = reinterpret_cast<__half*>(tile + KV4_CODES + (r >> 1) * 32 + grp * 8);
+        par[r & 1] = scale;
+        par[2 + (r & 1)] = bias;
+    }
+}
+
+// Four dimensions [4 lane, 4 lane + 4) of position r of a tile.
+Q3_DEV void kv4_load_k(const uint8_t* tile, int r, int lane, __half (&v)[4]) {
+    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + r * 64 + lane * 2);
+    const __half2 sb = *reinterpret_cast<const __half2*>(tile + KV4_CODES + r * 16 + (lane >> 3) * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __hfma(__low2half(sb), __int2half_rn((c >> (4 * e)) & 15), __high2half(sb));
+}
+Q3_DEV void kv4_load_v(const uint8_t* tile, int r, int lane, __half (&v)[4]) {
+    const int g = lane & 7, grp = lane >> 3;
+    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + (r >> 1) * 128 + g * 16 + grp * 4 + (r & 1) * 2);
+    const __half* par = reinterpret_cast<const __half*>(tile + KV4_CODES + (r >> 1) * 32 + grp * 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __hfma(par[r & 1], __int2half_rn((c >> (4 * e)) & 15), par[2 + (r & 1)]);
+}
+
+}  // namespace q3

@@ -2101,4 +2101,149 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
     return Q3_OK;
 }
 
+// ---------------------------------------------------------------- 4-bit cache and scoring operators
+
+namespace {
+
+// what the three cache operators share: heads, tables, pool
+bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int max_blocks, const void* kv, int n_blocks)
+{
+    return T >= 0 && n_kv >= 1 && n_kv <= 4096 && n_q >= 1 && n_q <= 8 * n_kv && n_q % n_kv == 0 && tables && n_slots >= 1 &&
+           max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) && n_blocks >= 1;
+}
+
+bool row_stride_ok(int64_t stride, int type, int64_t width)
+{
+    return stride >= width && stride % (type == Q3_TYPE_F32 ? 4 : 8) == 0;
+}
+
+}  // namespace
+
+int q3_op_kv4_append(const void* qkv_dev, int qkv_type, int64_t qkv_stride, const void* q_gain_dev,
+                     const void* k_gain_dev, float eps, const float* rope_dev, int rope_len,
+                     const int32_t* row_pos_dev, const int32_t* row_slot_dev, int T, int n_q, int n_kv,
+                     const int32_t* tables_dev, int n_slots, int max_blocks, void* kv_dev, int n_blocks,
+                     void* q_out_dev, void* kv_out_dev, int32_t* status_dev, void* stream)
+{
+    if (!qkv_dev || !q_gain_dev || !k_gain_dev || !rope_dev || !row_pos_dev || !row_slot_dev || rope_len < 1 ||
+        !(eps >= 0.f) || !kv4_sizes_ok(T, n_q, n_kv, tables_dev, n_slots, max_blocks, kv_dev, n_blocks))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_append: bad argument");
+    if (qkv_type < Q3_TYPE_F32 || qkv_type > Q3_TYPE_BF16)
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_append: unknown type %d", qkv_type);
+    if (!row_stride_ok(qkv_stride, qkv_type, (int64_t)(n_q + 2 * n_kv) * 128))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_append: row stride too small or not a multiple of 16 bytes");
+    if (!aligned16(qkv_dev) || !aligned16(rope_dev) || !aligned16(q_gain_dev) || !aligned16(k_gain_dev) ||
+        !aligned16(q_out_dev) || !aligned16(kv_out_dev))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_append: pointers must be 16-byte aligned");
+    if (T == 0) return Q3_OK;
+    Kv4AppendArgs a{};
+    a.qkv = qkv_dev; a.qkv_stride = qkv_stride;
+    a.q_gain = static_cast<const bf16*>(q_gain_dev); a.k_gain = static_cast<const bf16*>(k_gain_dev);
+    a.eps = eps;
+    a.rope = reinterpret_cast<const float2*>(rope_dev); a.rope_len = rope_len;
+    a.row_pos = row_pos_dev; a.row_slot = row_slot_dev;
+    a.T = T; a.n_q = n_q; a.n_kv = n_kv;
+    a.tables = tables_dev; a.n_slots = n_slots; a.max_blocks = max_blocks;
+    a.kv = static_cast<uint8_t*>(kv_dev); a.n_blocks = n_blocks;
+    a.q_out = static_cast<f16*>(q_out_dev); a.kv_out = static_cast<f16*>(kv_out_dev);
+    a.status = status_dev;
+    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const cudaError_t e = launch_kv4_append(L, a, qkv_type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_append: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, const int32_t* row_pos_dev,
+                               const int32_t* row_slot_dev, int T, int n_q, int n_kv, const int32_t* tables_dev,
+                               int n_slots, int max_blocks, int max_ctx, const void* kv_dev, int n_blocks,
+                               void* out_dev, int out_type, int32_t* status_dev, void* stream)
+{
+    if (!q_dev || !row_pos_dev || !row_slot_dev || !out_dev || max_ctx < 0 ||
+        !kv4_sizes_ok(T, n_q, n_kv, tables_dev, n_slots, max_blocks, kv_dev, n_blocks) || max_ctx > 32 * max_blocks)
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_decode_attention: bad argument");
+    if ((q_type != Q3_TYPE_F32 && q_type != Q3_TYPE_F16) || (out_type != Q3_TYPE_F32 && out_type != Q3_TYPE_F16))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_decode_attention: q and out are f32 or fp16");
+    if (!row_stride_ok(q_stride, q_type, (int64_t)n_q * 128))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_decode_attention: row stride too small or not a multiple of 16 bytes");
+    if (!aligned16(q_dev) || !aligned16(out_dev))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_decode_attention: pointers must be 16-byte aligned");
+    if (T == 0) return Q3_OK;
+    Kv4DecodeArgs a{};
+    a.q = q_dev; a.q_stride = q_stride;
+    a.row_pos = row_pos_dev; a.row_slot = row_slot_dev;
+    a.T = T; a.n_q = n_q; a.n_kv = n_kv;
+    a.tables = tables_dev; a.n_slots = n_slots; a.max_blocks = max_blocks;
+    a.max_ctx = max_ctx ? max_ctx : 32 * max_blocks;
+    a.kv = static_cast<const uint8_t*>(kv_dev); a.n_blocks = n_blocks;
+    a.out = out_dev; a.status = status_dev;
+    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const cudaError_t e = launch_kv4_decode(L, a, q_type, out_type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_decode_attention: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int n_blocks, int64_t* bytes)
+{
+    if (!bytes || ns < 0 || T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv || n_blocks < 1)
+        return fail(Q3_ERR_INVALID_ARG, "kv4_prefill_workspace: bad argument");
+    *bytes = 0;
+    return Q3_OK;
+}
+
+int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32_t* seq_rows_dev,
+                                const int32_t* seq_pos_dev, const int32_t* seq_slot_dev, int ns, int T, int n_q,
+                                int n_kv, const int32_t* tables_dev, int n_slots, int max_blocks, const void* kv_dev,
+                                int n_blocks, void* out_dev, void* workspace_dev, int64_t workspace_bytes,
+                                int32_t* status_dev, void* stream)
+{
+    if (!q_dev || !seq_rows_dev || !seq_pos_dev || !out_dev || ns < 0 ||
+        !kv4_sizes_ok(T, n_q, n_kv, tables_dev, n_slots, max_blocks, kv_dev, n_blocks) || (!seq_slot_dev && ns > n_slots))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: bad argument");
+    if (!row_stride_ok(q_stride, Q3_TYPE_F16, (int64_t)n_q * 128))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: row stride too small or not a multiple of 16 bytes");
+    int64_t need = 0;
+    q3_kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks, &need);
+    if (need && (!workspace_dev || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: workspace of %lld bytes, 256-byte aligned", (long long)need);
+    if (!aligned16(q_dev) || !aligned16(out_dev))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: pointers must be 16-byte aligned");
+    if (T == 0 || ns == 0) return Q3_OK;
+    Kv4PrefillArgs a{};
+    a.q = static_cast<const f16*>(q_dev); a.q_stride = q_stride;
+    a.seq_rows = seq_rows_dev; a.seq_pos = seq_pos_dev; a.seq_slot = seq_slot_dev;
+    a.ns = ns; a.T = T; a.n_q = n_q; a.n_kv = n_kv;
+    a.tables = tables_dev; a.n_slots = n_slots; a.max_blocks = max_blocks;
+    a.kv = static_cast<const uint8_t*>(kv_dev); a.n_blocks = n_blocks;
+    a.out = static_cast<f16*>(out_dev); a.status = status_dev;
+    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const cudaError_t e = launch_kv4_prefill(L, a);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_prefill_attention: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N, int V, const int32_t* targets_dev,
+                         int top_k, float* logprob_dev, float* entropy_dev, int32_t* top_ids_dev,
+                         float* top_logprob_dev, int32_t* status_dev, void* stream)
+{
+    if (!logits_dev || N < 0 || V < 1 || stride < V || (logprob_dev && !targets_dev))
+        return fail(Q3_ERR_INVALID_ARG, "op_token_logprobs: bad argument");
+    if (type < Q3_TYPE_F32 || type > Q3_TYPE_BF16)
+        return fail(Q3_ERR_INVALID_ARG, "op_token_logprobs: unknown type %d", type);
+    if (reinterpret_cast<uintptr_t>(logits_dev) & (type == Q3_TYPE_F32 ? 3 : 1))
+        return fail(Q3_ERR_INVALID_ARG, "op_token_logprobs: logits not aligned to their type");
+    if (top_k < 0 || top_k > V || top_k > Q3_LOGPROB_MAX_TOP)
+        return fail(Q3_ERR_INVALID_ARG, "op_token_logprobs: top_k outside [0, min(V, %d)]", Q3_LOGPROB_MAX_TOP);
+    if (N == 0) return Q3_OK;
+    LogprobArgs a{};
+    a.logits = logits_dev; a.stride = stride; a.N = N; a.V = V;
+    a.top = top_ids_dev || top_logprob_dev ? top_k : 0;
+    a.targets = targets_dev; a.logprob = logprob_dev; a.entropy = entropy_dev;
+    a.top_ids = top_ids_dev; a.top_logprob = top_logprob_dev;
+    a.status = status_dev;
+    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const cudaError_t e = launch_logprobs(L, a, type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_token_logprobs: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
 }  // extern "C"

@@ -1,6 +1,8 @@
 // k_kv4.cu -- the 4-bit K/V cache's writer and attention ("Kipp Roadmap",
 // status v0.0.2: 32-position block tables; status v0.0.4: a quantized cache is
 // opt-in).  The tile format is in kv4.cuh.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -8,6 +10,8 @@
 namespace q3 {
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int D = 128;
 
@@ -101,41 +105,449 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
     else kv4_store_v(tile, pos % 32, codes, scale, bias, lane);
 }
 
-// ---------------------------------------------------------------- attention, a row and head at a time
-// Four warps take positions in turn, a lane four dimensions; each warp keeps
-// the running maximum, sum and output of its positions and they are merged in
-// warp order.
+// ---------------------------------------------------------------- decode attention
+// One CTA per (row, KV head, split of its context), four warps.  A warp takes
+// every fourth 32-position block of the split; lane 0 keeps the next blocks'
+// tiles (5,120 bytes of K and V, contiguous as stored) on their way with bulk
+// copies into the warp's own ring, so no barrier is shared between warps.
+//
+// Both products run on mma.sync m16n8k16 with the cache as the A operand, so
+// its 4-bit words become fragments in registers (kv4_pair; 1.6 instructions a
+// value) and never pass through shared memory again:
+//   S^T = K Q^T   rows positions, columns (head, part): column 2h is the fp16
+//                 high part of q_h, column 2h + 1 the remainder, so an FP32 q
+//                 keeps 22 bits and c0 + c1 is the score of one head in one
+//                 lane.  The order of the 16 dimensions of a step is free, so a
+//                 lane takes its own group's 32 dimensions in the order of their
+//                 nibbles.
+//   O^T += V^T P^T  rows dimensions (a lane's word pairs two positions), columns
+//                 (head, part) again: {high, low} of a weight lie side by side in
+//                 the score fragment and one 8 x 8 transpose makes them the B
+//                 fragment.
+// Softmax is online in base 2; O is rescaled only in blocks that raise a
+// maximum.  Four heads fill the eight columns; groups of five to eight take
+// two column tiles over the same fragments of K and V.
+//
+// Splits of a (row, KV head) are one cluster; warps merge in order through
+// shared memory, CTAs in order through distributed shared memory.
 constexpr int AW = 4;
+constexpr int KV4_STAGES = 2;
+constexpr int KV4_STAGE = 2 * KV4_TILE;
 
-template <typename Tq, typename To>
-Q3_DEV void attend_row(const Tq* q, To* out, int ctx, int kvh, const int* table, int n_kv, const uint8_t* kv,
-                       int n_blocks, int* status)
+Q3_DEV float fast_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+Q3_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+Q3_DEV uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+Q3_DEV __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+Q3_DEV uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+// wait_bar, bounded, with an optional status word
+Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (global_ns() - t0 > Q3_WAIT_LIMIT_NS) {
+            report(status, Q3_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// 32 values [32 tig, 32 tig + 32) of a head's q as the B fragments of one
+// column: registers 2 s, 2 s + 1 of step s; part 0 the high halves, 1 the rest
+template <typename Tq>
+Q3_DEV void load_q(const Tq* q, int part, uint32_t (&b)[16], bool& bad) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float f[8];
+        load4(q + 8 * j, 0, *reinterpret_cast<float (*)[4]>(f));
+        load4(q + 8 * j + 4, 0, *reinterpret_cast<float (*)[4]>(f + 4));
+        __half h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = to_f16(f[e], bad);
+            if (part) h[e] = __float2half_rn(f[e] - __half2float(h[e]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[4 * j + i] = as_u32(__halves2half2(h[i], h[i + 4]));
+    }
+}
+
+template <int NT>
+struct Attend {
+    float m[NT], l[NT];        // running maximum and this lane's part of the sum, head tig of each column tile
+    float o[NT][8][4];         // O^T: row tile 2 g + h holds dimensions 32 g + 4 (lane / 4) + 2 h, + 1
+};
+
+// One block: kt, vt its K and V tiles in shared memory, n_pos its positions
+// in use.
+template <int NT>
+Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&q)[NT][16], int n_pos, int lane, Attend<NT>& w)
+{
+    const int g = lane >> 2, tig = lane & 3;
+    const float scale = 1.4426950408889634f * 0.08838834764831845f;    // log2(e) / sqrt(128)
+    float s[NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        const int p = 16 * mt + g;
+        const uint4 ka = *reinterpret_cast<const uint4*>(kt + p * 64 + tig * 16);
+        const uint4 kb = *reinterpret_cast<const uint4*>(kt + (p + 8) * 64 + tig * 16);
+        const __half2 sa = *reinterpret_cast<const __half2*>(kt + KV4_CODES + p * 16 + tig * 4);
+        const __half2 sb = *reinterpret_cast<const __half2*>(kt + KV4_CODES + (p + 8) * 16 + tig * 4);
+        const __half2 sca = __low2half2(sa), bia = __high2half2(sa), scb = __low2half2(sb), bib = __high2half2(sb);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        float c[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a0[4] = {kv4_pair<0>(wa[j], sca, bia), kv4_pair<0>(wb[j], scb, bib),
+                                    kv4_pair<1>(wa[j], sca, bia), kv4_pair<1>(wb[j], scb, bib)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], a0, q[nt][4 * j], q[nt][4 * j + 1]);
+            const uint32_t a1[4] = {kv4_pair<2>(wa[j], sca, bia), kv4_pair<2>(wb[j], scb, bib),
+                                    kv4_pair<3>(wa[j], sca, bia), kv4_pair<3>(wb[j], scb, bib)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], a1, q[nt][4 * j + 2], q[nt][4 * j + 3]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            s[nt][2 * mt] = p < n_pos ? (c[nt][0] + c[nt][1]) * scale : -INFINITY;
+            s[nt][2 * mt + 1] = p + 8 < n_pos ? (c[nt][2] + c[nt][3]) * scale : -INFINITY;
+        }
+    }
+    uint32_t pt[NT][4];        // the weights' B fragments: 8 positions each
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float mx = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (__any_sync(0xffffffffu, mx > w.m[nt])) {
+            const float mn = fmaxf(w.m[nt], mx), alpha = fast_ex2(w.m[nt] - mn);     // 0 at first
+            w.m[nt] = mn;
+            w.l[nt] *= alpha;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w.o[nt][i][e] *= alpha;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float e = fast_ex2(s[nt][i] - w.m[nt]);
+            w.l[nt] += e;
+            const __half hi = __float2half_rn(e);
+            pt[nt][i] = transpose8x8(as_u32(__halves2half2(hi, __float2half_rn(e - __half2float(hi)))));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int pa = 8 * j + tig, pb = pa + 4;         // position pairs
+        const uint4 va = *reinterpret_cast<const uint4*>(vt + pa * 128 + g * 16);
+        const uint4 vb = *reinterpret_cast<const uint4*>(vt + pb * 128 + g * 16);
+        const uint4* para = reinterpret_cast<const uint4*>(vt + KV4_CODES + pa * 32);
+        const uint4* parb = reinterpret_cast<const uint4*>(vt + KV4_CODES + pb * 32);
+        const uint4 a01 = para[0], a23 = para[1], b01 = parb[0], b23 = parb[1];
+        uint32_t sba[8] = {a01.x, a01.y, a01.z, a01.w, a23.x, a23.y, a23.z, a23.w};
+        uint32_t sbb[8] = {b01.x, b01.y, b01.z, b01.w, b23.x, b23.y, b23.z, b23.w};
+        if (n_pos < 32) {      // positions past the end count as zeros, whatever is there
+            const uint32_t ma = (2 * pa < n_pos ? 0xffffu : 0u) | (2 * pa + 1 < n_pos ? 0xffff0000u : 0u);
+            const uint32_t mb = (2 * pb < n_pos ? 0xffffu : 0u) | (2 * pb + 1 < n_pos ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) { sba[e] &= ma; sbb[e] &= mb; }
+        }
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+            const __half2 sca = as_h2(sba[2 * gr]), bia = as_h2(sba[2 * gr + 1]);
+            const __half2 scb = as_h2(sbb[2 * gr]), bib = as_h2(sbb[2 * gr + 1]);
+            const uint32_t a0[4] = {kv4_pair<0>(wa[gr], sca, bia), kv4_pair<1>(wa[gr], sca, bia),
+                                    kv4_pair<0>(wb[gr], scb, bib), kv4_pair<1>(wb[gr], scb, bib)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[nt][2 * gr], a0, pt[nt][2 * j], pt[nt][2 * j + 1]);
+            const uint32_t a1[4] = {kv4_pair<2>(wa[gr], sca, bia), kv4_pair<3>(wa[gr], sca, bia),
+                                    kv4_pair<2>(wb[gr], scb, bib), kv4_pair<3>(wb[gr], scb, bib)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[nt][2 * gr + 1], a1, pt[nt][2 * j], pt[nt][2 * j + 1]);
+        }
+    }
+}
+
+struct DecodeShared {
+    union {
+        uint8_t ring[AW][KV4_STAGES][KV4_STAGE];
+        float o[AW][8][D];                 // per warp, then [0] the CTA's
+    };
+    uint64_t full[AW][KV4_STAGES];
+    float m[AW][8], l[AW][8];              // per warp, then [0] the CTA's
+};
+static_assert(sizeof(float) * AW * 8 * D <= (size_t)AW * KV4_STAGES * KV4_STAGE, "merge area");
+
+template <int NT, typename Tq, typename To>
+__global__ void __launch_bounds__(AW * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(const Kv4DecodeArgs a, int C)
+{
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    DecodeShared& sm = *reinterpret_cast<DecodeShared*>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, tig = lane & 3;
+    const int rank = blockIdx.x % C, unit = blockIdx.x / C;
+    const int kvh = unit % a.n_kv, t = unit / a.n_kv;
+    const int G = a.n_q / a.n_kv;
+    if (lane < KV4_STAGES) mbar_init(&sm.full[warp][lane], 1);
+    fence_barrier_init();
+    __syncwarp();
+    grid_dep_wait();
+
+    const int slot = a.row_slot[t];
+    int ctx = a.row_pos[t] + 1;
+    if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
+        if (rank == 0 && threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
+        ctx = 0;
+    }
+    const int nblk = max(ctx + 31, 0) / 32, per = (nblk + C - 1) / C;
+    const int b1 = min((rank + 1) * per, nblk);
+    const int* table = a.tables + (size_t)(ctx > 0 ? slot : 0) * a.max_blocks;
+    const uint8_t* kv = a.kv + (size_t)kvh * KV4_TILE;
+
+    // block b's tiles into stage st; false: its table entry is outside the pool
+    auto issue = [&](int phys, int st) -> bool {
+        if (phys < 0 || phys >= a.n_blocks) {
+            if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
+            return false;
+        }
+        if (lane == 0) {
+            const uint8_t* src = kv + (size_t)phys * 2 * a.n_kv * KV4_TILE;
+            uint8_t* dst = sm.ring[warp][st];
+            mbar_arrive_expect_tx(&sm.full[warp][st], KV4_STAGE);
+            bulk_load(dst, src, KV4_TILE, &sm.full[warp][st]);
+            bulk_load(dst + KV4_TILE, src + (size_t)a.n_kv * KV4_TILE, KV4_TILE, &sm.full[warp][st]);
+        }
+        return true;
+    };
+    uint32_t live = 0, phase = 0;          // per stage: a copy is on its way, the parity that ends it
+    const int first = rank * per + warp;
+#pragma unroll
+    for (int st = 0; st < KV4_STAGES; ++st) {
+        const int b = first + st * AW;
+        if (b < b1 && issue(table[b], st)) live |= 1u << st;
+    }
+
+    uint32_t q[NT][16];
+    bool bad = false;
+    const Tq* qrow = static_cast<const Tq*>(a.q) + (size_t)t * a.q_stride + (size_t)kvh * G * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 4 * nt + (g >> 1);
+        if (h < G) {
+            load_q(qrow + (size_t)h * D + 32 * tig, g & 1, q[nt], bad);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) q[nt][i] = 0u;
+        }
+    }
+    if (bad) report(a.status, Q3_STATUS_F16_RANGE);
+
+    Attend<NT> w;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        w.m[nt] = -INFINITY;
+        w.l[nt] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w.o[nt][i][0] = w.o[nt][i][1] = w.o[nt][i][2] = w.o[nt][i][3] = 0.f;
+    }
+
+    int st = 0;
+    bool ok = true;
+    for (int b = first; b < b1 && ok; b += AW) {
+        const int bn = b + KV4_STAGES * AW;
+        const int phys = bn < b1 ? table[bn] : 0;        // ahead of its use below
+        if (live >> st & 1) {
+            ok = wait_bar(&sm.full[warp][st], phase >> st & 1, a.status);
+            phase ^= 1u << st;
+            live &= ~(1u << st);
+            if (ok)
+                attend_block<NT>(sm.ring[warp][st], sm.ring[warp][st] + KV4_TILE, q, min(32, ctx - 32 * b), lane, w);
+        }
+        __syncwarp();                                    // every lane is done with the stage
+        if (ok && bn < b1 && issue(phys, st)) live |= 1u << st;
+        st = st + 1 == KV4_STAGES ? 0 : st + 1;
+    }
+    if (!ok)                                             // a wait ran out: leave no copy behind
+        for (int i = 0; i < KV4_STAGES; ++i)
+            if (live >> i & 1) wait_bar(&sm.full[warp][i], phase >> i & 1, a.status);
+    __syncthreads();                                     // the rings become the merge area
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = 4 * nt + tig;
+        float l = w.l[nt];
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (h >= G) continue;
+        if (g == 0) { sm.m[warp][h] = w.m[nt]; sm.l[warp][h] = l; }
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+            const float(&x)[4] = w.o[nt][2 * gr];
+            const float(&y)[4] = w.o[nt][2 * gr + 1];
+            *reinterpret_cast<float4*>(&sm.o[warp][h][32 * gr + 4 * g]) =
+                make_float4(x[0] + x[1], x[2] + x[3], y[0] + y[1], y[2] + y[3]);
+        }
+    }
+    __syncthreads();
+
+    // the warps in order; thread d owns dimension d
+    const int d = threadIdx.x;
+    To* out = static_cast<To*>(a.out) + ((size_t)t * a.n_q + (size_t)kvh * G) * D + d;
+    bad = false;
+    auto put = [&](int h, float O, float L) {
+        const float v = L > 0.f ? O / L : 0.f;           // nothing attended: zeros
+        if (sizeof(To) == 2) reinterpret_cast<__half*>(out)[(size_t)h * D] = to_f16(v, bad);
+        else reinterpret_cast<float*>(out)[(size_t)h * D] = v;
+    };
+    for (int h = 0; h < G; ++h) {
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int i = 0; i < AW; ++i) M = fmaxf(M, sm.m[i][h]);
+        if (M != -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < AW; ++i) {
+                const float e = fast_ex2(sm.m[i][h] - M);
+                L = fmaf(sm.l[i][h], e, L);
+                O = fmaf(sm.o[i][h][d], e, O);
+            }
+        }
+        if (C == 1) {
+            put(h, O, L);
+            continue;
+        }
+        __syncthreads();                                 // every thread has read head h's maxima
+        sm.o[0][h][d] = O;
+        if (d == 0) { sm.m[0][h] = M; sm.l[0][h] = L; }
+    }
+    if (C > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int h = rank; h < G; h += C) {
+            float M = -INFINITY, L = 0.f, O = 0.f;
+            for (int c = 0; c < C; ++c) M = fmaxf(M, *cluster.map_shared_rank(&sm.m[0][h], c));
+            if (M != -INFINITY)
+                for (int c = 0; c < C; ++c) {
+                    const float e = fast_ex2(*cluster.map_shared_rank(&sm.m[0][h], c) - M);
+                    L = fmaf(*cluster.map_shared_rank(&sm.l[0][h], c), e, L);
+                    O = fmaf(*cluster.map_shared_rank(&sm.o[0][h][d], c), e, O);
+                }
+            put(h, O, L);
+        }
+        cluster.sync();                                  // nobody's shared memory is read past here
+    }
+    if (bad) report(a.status, Q3_STATUS_F16_RANGE);
+}
+
+template <int NT, typename Tq, typename To>
+cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a, int C)
+{
+    static std::atomic<unsigned long long> attr_done{0}, wide_done{0};
+    if (cudaError_t e = allow_smem_per_device(kv4_decode_kernel<NT, Tq, To>, (int)sizeof(DecodeShared), attr_done)) return e;
+    if (C > 8)
+        if (cudaError_t e = allow_wide_clusters(kv4_decode_kernel<NT, Tq, To>, wide_done)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.T * a.n_kv * C);
+    cfg.blockDim = dim3(AW * 32);
+    cfg.dynamicSmemBytes = sizeof(DecodeShared);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = L.pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (L.counter) ++*L.counter;
+    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<NT, Tq, To>, a, C);
+}
+
+// CTAs of a (row, KV head): as many of 1, 2, 4, 8, 16 as it takes to fill the
+// SMs (four CTAs each) while every warp has a block.
+int decode_splits(const Kv4DecodeArgs& a)
+{
+    const int64_t units = (int64_t)a.T * a.n_kv;
+    const int blocks = (a.max_ctx + 31) / 32;
+    int C = 1;
+    while (C < 16 && units * C < 4 * 152 && AW * C < blocks) C *= 2;
+    return C;
+}
+
+template <int NT>
+cudaError_t launch_decode_nt(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type)
+{
+    const int C = decode_splits(a);
+    if (q_type == Q3_TYPE_F32)
+        return out_type == Q3_TYPE_F32 ? launch_decode<NT, float, float>(L, a, C) : launch_decode<NT, float, __half>(L, a, C);
+    return out_type == Q3_TYPE_F32 ? launch_decode<NT, __half, float>(L, a, C) : launch_decode<NT, __half, __half>(L, a, C);
+}
+
+// ---------------------------------------------------------------- prefill attention, a row and head at a time
+Q3_DEV __half kv4_value(const uint8_t* tile, bool v, int r, int d) {
+    const int grp = d / 32, i = d % 32, g = i / 4;
+    const int at = v ? (r / 2) * 128 + g * 16 + grp * 4 + (r & 1) * 2 + (i & 3) / 2 : r * 64 + d / 2;
+    const int c = tile[at] >> (4 * (d & 1)) & 15;
+    const __half* par = reinterpret_cast<const __half*>(tile + KV4_CODES);
+    const __half s = v ? par[(r / 2) * 16 + grp * 4 + (r & 1)] : par[r * 8 + grp * 2];
+    const __half b = v ? par[(r / 2) * 16 + grp * 4 + 2 + (r & 1)] : par[r * 8 + grp * 2 + 1];
+    return __hfma(s, __int2half_rn(c), b);
+}
+
+__global__ void __launch_bounds__(AW * 32) kv4_prefill_kernel(const Kv4PrefillArgs a)
 {
     __shared__ float s_m[AW], s_l[AW], s_o[AW][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int t = blockIdx.y, h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int i = 0;
+    while (i < a.ns && !(a.seq_rows[i] <= t && t < a.seq_rows[i + 1])) ++i;
+    if (i == a.ns) return;                               // a row of no sequence
+    const int slot = a.seq_slot ? a.seq_slot[i] : i;
+    int ctx = a.seq_pos[i] + t - a.seq_rows[i] + 1;
+    if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
+        if (threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
+        ctx = 0;
+    }
+    const int kvh = h / (a.n_q / a.n_kv);
+    const int* table = a.tables + (size_t)max(slot, 0) * a.max_blocks;
     float qv[4];
-    load4(q, lane, qv);
+    load4(a.q + (size_t)t * a.q_stride + h * D, lane, qv);
     float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     const float scale = 1.4426950408889634f * 0.08838834764831845f;
     for (int p = warp; p < ctx; p += AW) {
         const int blk = table[p / 32];
-        if (blk < 0 || blk >= n_blocks) {
-            if (lane == 0) report(status, Q3_STATUS_BLOCK_RANGE);
+        if (blk < 0 || blk >= a.n_blocks) {
+            if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
             continue;
         }
-        const uint8_t* kt = kv + ((size_t)blk * 2 * n_kv + kvh) * KV4_TILE;
-        __half k[4], v[4];
-        kv4_load_k(kt, p % 32, lane, k);
-        kv4_load_v(kt + (size_t)n_kv * KV4_TILE, p % 32, lane, v);
+        const uint8_t* kt = a.kv + ((size_t)blk * 2 * a.n_kv + kvh) * KV4_TILE;
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __half2float(k[e]), s);
+        for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __half2float(kv4_value(kt, false, p % 32, lane * 4 + e)), s);
         s = warp_allsum(s) * scale;
         const float mn = fmaxf(m, s), alpha = exp2f(m - mn), w = exp2f(s - mn);
         m = mn;
         l = l * alpha + w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * alpha + w * __half2float(v[e]);
+        for (int e = 0; e < 4; ++e)
+            o[e] = o[e] * alpha + w * __half2float(kv4_value(kt + (size_t)a.n_kv * KV4_TILE, true, p % 32, lane * 4 + e));
     }
     if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
 #pragma unroll
@@ -150,43 +562,9 @@ Q3_DEV void attend_row(const Tq* q, To* out, int ctx, int kvh, const int* table,
             L = fmaf(s_l[w], e, L);
             O = fmaf(s_o[w][d], e, O);
         }
-    const float v = L > 0.f ? O / L : 0.f;
     bool bad = false;
-    if (sizeof(To) == 2) reinterpret_cast<__half*>(out)[d] = to_f16(v, bad);
-    else reinterpret_cast<float*>(out)[d] = v;
-    if (bad) report(status, Q3_STATUS_F16_RANGE);
-}
-
-template <typename Tq, typename To>
-__global__ void __launch_bounds__(AW * 32) kv4_decode_kernel(const Kv4DecodeArgs a)
-{
-    grid_dep_wait();
-    const int t = blockIdx.y, h = blockIdx.x;
-    const int slot = a.row_slot[t];
-    int ctx = a.row_pos[t] + 1;
-    if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
-        if (threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        ctx = 0;
-    }
-    attend_row(static_cast<const Tq*>(a.q) + (size_t)t * a.q_stride + h * D, static_cast<To*>(a.out) + ((size_t)t * a.n_q + h) * D,
-               ctx, h / (a.n_q / a.n_kv), a.tables + (size_t)max(slot, 0) * a.max_blocks, a.n_kv, a.kv, a.n_blocks, a.status);
-}
-
-__global__ void __launch_bounds__(AW * 32) kv4_prefill_kernel(const Kv4PrefillArgs a)
-{
-    grid_dep_wait();
-    const int t = blockIdx.y, h = blockIdx.x;
-    int i = 0;
-    while (i < a.ns && !(a.seq_rows[i] <= t && t < a.seq_rows[i + 1])) ++i;
-    if (i == a.ns) return;                               // a row of no sequence
-    const int slot = a.seq_slot ? a.seq_slot[i] : i;
-    int ctx = a.seq_pos[i] + t - a.seq_rows[i] + 1;
-    if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
-        if (threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        ctx = 0;
-    }
-    attend_row(a.q + (size_t)t * a.q_stride + h * D, a.out + ((size_t)t * a.n_q + h) * D, ctx, h / (a.n_q / a.n_kv),
-               a.tables + (size_t)max(slot, 0) * a.max_blocks, a.n_kv, a.kv, a.n_blocks, a.status);
+    a.out[((size_t)t * a.n_q + h) * D + d] = to_f16(L > 0.f ? O / L : 0.f, bad);
+    if (bad) report(a.status, Q3_STATUS_F16_RANGE);
 }
 
 }  // namespace
@@ -203,12 +581,7 @@ cudaError_t launch_kv4_append(const Launch& L, const Kv4AppendArgs& a, int type)
 
 cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type)
 {
-    const dim3 grid(a.n_q, a.T), block(AW * 32);
-    if (q_type == Q3_TYPE_F32)
-        return out_type == Q3_TYPE_F32 ? launch_ex(L, kv4_decode_kernel<float, float>, grid, block, a)
-                                       : launch_ex(L, kv4_decode_kernel<float, __half>, grid, block, a);
-    return out_type == Q3_TYPE_F32 ? launch_ex(L, kv4_decode_kernel<__half, float>, grid, block, a)
-                                   : launch_ex(L, kv4_decode_kernel<__half, __half>, grid, block, a);
+    return a.n_q / a.n_kv <= 4 ? launch_decode_nt<1>(L, a, q_type, out_type) : launch_decode_nt<2>(L, a, q_type, out_type);
 }
 
 cudaError_t launch_kv4_prefill(const Launch& L, const Kv4PrefillArgs& a)

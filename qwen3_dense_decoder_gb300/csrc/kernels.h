@@ -46,6 +46,20 @@ cudaError_t allow_smem_per_device(Kernel* kernel, int bytes, std::atomic<unsigne
     return e;
 }
 
+// Likewise for clusters of more than eight CTAs.
+template <typename Kernel>
+cudaError_t allow_wide_clusters(Kernel* kernel, std::atomic<unsigned long long>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = (dev >= 0 && dev < 64) ? 1ull << dev : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
 // ---------------------------------------------------------------- launch
 // How a kernel is launched: stream, and whether it may start early under
 // programmatic dependent launch.

@@ -74,19 +74,23 @@ Q3_DEV void kv4_store_v(uint8_t* tile, int r, uint32_t codes, __half scale, __ha
     }
 }
 
-// Four dimensions [4 lane, 4 lane + 4) of position r of a tile.
-Q3_DEV void kv4_load_k(const uint8_t* tile, int r, int lane, __half (&v)[4]) {
-    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + r * 64 + lane * 2);
-    const __half2 sb = *reinterpret_cast<const __half2*>(tile + KV4_CODES + r * 16 + (lane >> 3) * 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __hfma(__low2half(sb), __int2half_rn((c >> (4 * e)) & 15), __high2half(sb));
-}
-Q3_DEV void kv4_load_v(const uint8_t* tile, int r, int lane, __half (&v)[4]) {
-    const int g = lane & 7, grp = lane >> 3;
-    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + (r >> 1) * 128 + g * 16 + grp * 4 + (r & 1) * 2);
-    const __half* par = reinterpret_cast<const __half*>(tile + KV4_CODES + (r >> 1) * 32 + grp * 8);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __hfma(par[r & 1], __int2half_rn((c >> (4 * e)) & 15), par[2 + (r & 1)]);
+// Nibble pair i of a code word (bits 4 i and 16 + 4 i) as fp16(scale * code +
+// bias): an odd i keeps its place as 1024 + 16 code, so a word needs one shift.
+// 1024 + code is exact in fp16, so are the code left by one exact operation and
+// the fused multiply-add's argument; the last rounds once.
+template <int I>
+Q3_DEV uint32_t kv4_pair(uint32_t w, __half2 scale, __half2 bias) {
+    const uint32_t x = I >= 2 ? w >> 8 : w;
+    __half2 c;
+    if (I & 1) {
+        const uint32_t v = (x & 0x00f000f0u) | 0x64006400u;
+        c = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f), __float2half2_rn(-64.0f));
+    } else {
+        const uint32_t v = (x & 0x000f000fu) | 0x64006400u;
+        c = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1024.0f));
+    }
+    const __half2 r = __hfma2(c, scale, bias);
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 }  // namespace q3

@@ -311,42 +311,26 @@ LOGPROB_MAX_TOP = 32
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-def _need(ok: bool, msg: str) -> None:
-    if not ok:
-        raise ValueError(msg)
-
-
-class _On:
-    """The device of an operator's tensors made current, with the stream to
-    launch on; the tensors are kept from reuse until that stream is done."""
-
-    def __init__(self, name: str, stream, *tensors):
-        self.name = name
-        ts = [t for t in tensors if t is not None]
-        self.device = ts[0].device
-        for t in ts:
-            if t.device.type != "cuda" or t.device != self.device:
-                raise ValueError(f"{name}: tensors must be on one CUDA device")
-        self.index = self.device.index
-        self.tensors = ts
-        self.stream = stream
-
-    def call(self, fn, *args) -> None:
-        before = torch.cuda.current_device()
-        if before != self.index:
-            torch.cuda.set_device(self.index)
-        try:
-            current = torch.cuda.current_stream()
-            s = self.stream or current
-            if s.device.index != self.index:
-                raise ValueError(f"{self.name}: the stream is another device's")
-            rc = fn(*args, C.c_void_p(s.cuda_stream))
-            if s != current:
-                for t in self.tensors:
-                    t.record_stream(s)
-        finally:
-            if before != self.index:
-                torch.cuda.set_device(before)
+def _launch(name: str, fn, stream, tensors, *args) -> None:
+    """fn(*args, stream) with the tensors' device current.  On a stream other
+    than the current one the tensors are kept from reuse until it is done."""
+    i = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != i or i < 0):
+            raise ValueError(f"{name}: tensors must be on one CUDA device")
+    if torch.cuda.current_device() != i:
+        with torch.cuda.device(i):
+            return _launch(name, fn, stream, tensors, *args)
+    raw = torch._C._cuda_getCurrentRawStream(i)
+    if stream is not None and stream.cuda_stream != raw:
+        if stream.device_index != i:
+            raise ValueError(f"{name}: the stream is another device's")
+        raw = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    rc = fn(*args, raw)
+    if rc:
         _check(rc)
 
 
@@ -359,25 +343,34 @@ def check_status(status: torch.Tensor) -> None:
 
 
 def _int32(name: str, what: str, t: torch.Tensor, shape: tuple) -> None:
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: {what} must be contiguous int32 {list(shape)}")
 
 
-def _kv4_pool(name: str, kv: torch.Tensor, tables: torch.Tensor, status) -> tuple[int, int]:
-    _need(kv.dtype == torch.uint8 and kv.dim() == 4 and kv.shape[1] == 2 and kv.shape[3] == KV4_TILE and kv.is_contiguous(),
-          f"{name}: kv must be contiguous uint8 [n_blocks, 2, n_kv, {KV4_TILE}]")
-    _need(tables.dtype == torch.int32 and tables.dim() == 2 and tables.is_contiguous(),
-          f"{name}: tables must be contiguous int32 [n_slots, max_blocks]")
+def _kv4_pool(name: str, kv: torch.Tensor, tables: torch.Tensor, status) -> None:
+    if kv.dtype != torch.uint8 or kv.dim() != 4 or kv.shape[1] != 2 or kv.shape[3] != KV4_TILE or not kv.is_contiguous():
+        raise ValueError(f"{name}: kv must be contiguous uint8 [n_blocks, 2, n_kv, {KV4_TILE}]")
+    if tables.dtype != torch.int32 or tables.dim() != 2 or not tables.is_contiguous():
+        raise ValueError(f"{name}: tables must be contiguous int32 [n_slots, max_blocks]")
     if status is not None:
         _int32(name, "status", status, (1,))
-    return kv.shape[0], kv.shape[2]
 
 
-def _out(name: str, out, shape: tuple, dtype, device):
+def _rows(name: str, q: torch.Tensor, types: tuple) -> None:
+    if q.dtype not in types or q.dim() != 3 or q.shape[2] != 128 or q.stride(2) != 1 or (q.stride(1) != 128 and q.shape[1] > 1):
+        raise ValueError(f"{name}: q must be [T, n_q, 128] of {types} with contiguous rows")
+
+
+def _out(name: str, out, shape: tuple, dtype, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(tuple(out.shape) == shape and out.dtype == dtype and out.is_contiguous(), f"{name}: outputs must be contiguous {dtype} {list(shape)}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"{name}: outputs must be contiguous {dtype} {list(shape)}")
     return out
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def rope_table(n: int, theta: float, device="cuda") -> torch.Tensor:
@@ -398,23 +391,29 @@ def op_kv4_append(qkv: torch.Tensor, q_gain: torch.Tensor, k_gain: torch.Tensor,
     of negative position is padding.  kv_out: fp16 [T, 2, n_kv, 128], if given,
     receives the values the cache then holds."""
     name = "op_kv4_append"
-    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
+    _kv4_pool(name, kv, tables, status)
+    n_blocks, _, n_kv, _ = kv.shape
+    width = (n_q + 2 * n_kv) * 128
+    if qkv.dtype not in _TYPES or qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
+        raise ValueError(f"{name}: qkv must be f32, fp16 or bf16 [T, (n_q + 2 n_kv) * 128]")
     T = qkv.shape[0]
-    _need(qkv.dim() == 2 and qkv.dtype in _TYPES and qkv.shape[1] == (n_q + 2 * n_kv) * 128 and qkv.stride(1) == 1,
-          f"{name}: qkv must be f32, fp16 or bf16 [T, (n_q + 2 n_kv) * 128]")
-    _need(all(g.dtype == torch.bfloat16 and g.shape == (128,) and g.is_contiguous() for g in (q_gain, k_gain)),
-          f"{name}: gains must be bf16 [128]")
-    _need(rope.dtype == torch.float32 and rope.dim() == 3 and rope.shape[1:] == (64, 2) and rope.is_contiguous(),
-          f"{name}: rope must be f32 [n, 64, 2]")
+    for g in (q_gain, k_gain):
+        if g.dtype != torch.bfloat16 or g.shape != (128,) or not g.is_contiguous():
+            raise ValueError(f"{name}: gains must be bf16 [128]")
+    if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[1:] != (64, 2) or not rope.is_contiguous():
+        raise ValueError(f"{name}: rope must be f32 [n, 64, 2]")
     _int32(name, "row_pos", row_pos, (T,))
     _int32(name, "row_slot", row_slot, (T,))
-    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv.device)
+    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv)
     if kv_out is not None:
-        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv.device)
-    on = _On(name, stream, qkv, q_gain, k_gain, rope, row_pos, row_slot, tables, kv, q_out, kv_out, status)
-    on.call(lib().q3_op_kv4_append, _ptr(qkv), _TYPES[qkv.dtype], qkv.stride(0) if T > 1 else qkv.shape[1], _ptr(q_gain),
-            _ptr(k_gain), eps, _ptr(rope), rope.shape[0], _ptr(row_pos), _ptr(row_slot), T, n_q, n_kv, _ptr(tables),
-            tables.shape[0], tables.shape[1], _ptr(kv), n_blocks, _ptr(q_out), _ptr(kv_out), _ptr(status))
+        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv)
+    if T == 0:
+        return q_out
+    _launch(name, lib().q3_op_kv4_append, stream,
+            (qkv, q_gain, k_gain, rope, row_pos, row_slot, tables, kv, q_out, kv_out, status),
+            qkv.data_ptr(), _TYPES[qkv.dtype], qkv.stride(0) if T > 1 else width, q_gain.data_ptr(), k_gain.data_ptr(), eps,
+            rope.data_ptr(), rope.shape[0], row_pos.data_ptr(), row_slot.data_ptr(), T, n_q, n_kv, tables.data_ptr(),
+            tables.shape[0], tables.shape[1], kv.data_ptr(), n_blocks, q_out.data_ptr(), _p(kv_out), _p(status))
     return q_out
 
 
@@ -427,17 +426,18 @@ def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: to
     max_ctx: the longest context expected (0: what the tables hold); it chooses
     the split of the work only."""
     name = "op_kv4_decode_attention"
-    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
-    _need(q.dim() == 3 and q.shape[2] == 128 and q.dtype in (torch.float32, torch.float16) and q.stride(2) == 1 and q.stride(1) == 128,
-          f"{name}: q must be f32 or fp16 [T, n_q, 128] with contiguous rows")
+    _kv4_pool(name, kv, tables, status)
+    _rows(name, q, (torch.float32, torch.float16))
     T, n_q, _ = q.shape
     _int32(name, "row_pos", row_pos, (T,))
     _int32(name, "row_slot", row_slot, (T,))
-    out = _out(name, out, (T, n_q, 128), torch.float16 if out is None or out.dtype != torch.float32 else torch.float32, q.device)
-    on = _On(name, stream, q, row_pos, row_slot, tables, kv, out, status)
-    on.call(lib().q3_op_kv4_decode_attention, _ptr(q), _TYPES[q.dtype], q.stride(0) if T > 1 else n_q * 128, _ptr(row_pos),
-            _ptr(row_slot), T, n_q, n_kv, _ptr(tables), tables.shape[0], tables.shape[1], max_ctx, _ptr(kv), n_blocks,
-            _ptr(out), _TYPES[out.dtype], _ptr(status))
+    out = _out(name, out, (T, n_q, 128), torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16, q)
+    if T == 0:
+        return out
+    _launch(name, lib().q3_op_kv4_decode_attention, stream, (q, row_pos, row_slot, tables, kv, out, status),
+            q.data_ptr(), _TYPES[q.dtype], q.stride(0) if T > 1 else n_q * 128, row_pos.data_ptr(), row_slot.data_ptr(), T, n_q,
+            kv.shape[2], tables.data_ptr(), tables.shape[0], tables.shape[1], max_ctx, kv.data_ptr(), kv.shape[0], out.data_ptr(),
+            _TYPES[out.dtype], _p(status))
     return out
 
 
@@ -459,25 +459,27 @@ def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: t
     what out held.  workspace: uint8, kv4_prefill_workspace bytes (default:
     allocated here)."""
     name = "op_kv4_prefill_attention"
-    n_blocks, n_kv = _kv4_pool(name, kv, tables, status)
-    _need(q.dim() == 3 and q.shape[2] == 128 and q.dtype == torch.float16 and q.stride(2) == 1 and q.stride(1) == 128,
-          f"{name}: q must be fp16 [T, n_q, 128] with contiguous rows")
+    _kv4_pool(name, kv, tables, status)
+    _rows(name, q, (torch.float16,))
+    n_blocks, _, n_kv, _ = kv.shape
     T, n_q, _ = q.shape
     ns = seq_pos.shape[0]
     _int32(name, "seq_rows", seq_rows, (ns + 1,))
     _int32(name, "seq_pos", seq_pos, (ns,))
     if seq_slot is not None:
         _int32(name, "seq_slot", seq_slot, (ns,))
-    out = _out(name, out, (T, n_q, 128), torch.float16, q.device)
+    out = _out(name, out, (T, n_q, 128), torch.float16, q)
+    if T == 0 or ns == 0:
+        return out
     need = kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.numel() >= need,
-          f"{name}: workspace must be contiguous uint8, at least {need} bytes")
-    on = _On(name, stream, q, seq_rows, seq_pos, seq_slot, tables, kv, out, workspace, status)
-    on.call(lib().q3_op_kv4_prefill_attention, _ptr(q), q.stride(0) if T > 1 else n_q * 128, _ptr(seq_rows), _ptr(seq_pos),
-            _ptr(seq_slot), ns, T, n_q, n_kv, _ptr(tables), tables.shape[0], tables.shape[1], _ptr(kv), n_blocks, _ptr(out),
-            _ptr(workspace), workspace.numel(), _ptr(status))
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"{name}: workspace must be contiguous uint8, at least {need} bytes")
+    _launch(name, lib().q3_op_kv4_prefill_attention, stream, (q, seq_rows, seq_pos, seq_slot, tables, kv, out, workspace, status),
+            q.data_ptr(), q.stride(0) if T > 1 else n_q * 128, seq_rows.data_ptr(), seq_pos.data_ptr(), _p(seq_slot), ns, T, n_q,
+            n_kv, tables.data_ptr(), tables.shape[0], tables.shape[1], kv.data_ptr(), n_blocks, out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _p(status))
     return out
 
 
@@ -489,21 +491,25 @@ def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None,
     in order, lowest index first among equals (int32 [N, top_k]), with their
     log probabilities (f32 [N, top_k])."""
     name = "op_token_logprobs"
-    _need(logits.dim() == 2 and logits.dtype in _TYPES and (logits.shape[1] <= 1 or logits.stride(1) == 1),
-          f"{name}: logits must be f32, fp16 or bf16 [N, V] with contiguous rows")
+    if logits.dtype not in _TYPES or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"{name}: logits must be f32, fp16 or bf16 [N, V] with contiguous rows")
     N, V = logits.shape
-    dev = logits.device
     if targets is not None:
         _int32(name, "targets", targets, (N,))
     if status is not None:
         _int32(name, "status", status, (1,))
-    logprob = None if targets is None else torch.empty(N, dtype=torch.float32, device=dev)
-    entropy = torch.empty(N, dtype=torch.float32, device=dev)
-    ids = torch.empty(N, max(0, top_k), dtype=torch.int32, device=dev)
-    values = torch.empty(N, max(0, top_k), dtype=torch.float32, device=dev)
-    on = _On(name, stream, logits, targets, logprob, entropy, ids, values, status)
-    on.call(lib().q3_op_token_logprobs, _ptr(logits), _TYPES[logits.dtype], logits.stride(0) if N > 1 else V, N, V, _ptr(targets),
-            top_k, _ptr(logprob), _ptr(entropy), _ptr(ids), _ptr(values), _ptr(status))
+    if top_k < 0:
+        raise ValueError(f"{name}: top_k must not be negative")
+    f32, dev = torch.float32, logits.device
+    logprob = None if targets is None else torch.empty(N, dtype=f32, device=dev)
+    entropy = torch.empty(N, dtype=f32, device=dev)
+    ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
+    values = torch.empty((N, top_k), dtype=f32, device=dev)
+    if N == 0:
+        return logprob, entropy, ids, values
+    _launch(name, lib().q3_op_token_logprobs, stream, (logits, targets, logprob, entropy, ids, values, status),
+            logits.data_ptr(), _TYPES[logits.dtype], logits.stride(0) if N > 1 else V, N, V, _p(targets), top_k, _p(logprob),
+            entropy.data_ptr(), ids.data_ptr(), values.data_ptr(), _p(status))
     return logprob, entropy, ids, values
 
 

@@ -468,15 +468,19 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
  * n_q * 128, a multiple of 8; 16-byte aligned); out_dev: fp16 [T][n_q][128],
  * 16-byte aligned.  workspace_dev: q3_kv4_prefill_workspace bytes, 256-byte
  * aligned, needing no preparation; calls that may overlap on the GPU take one
- * each.  Status as q3_op_kv4_decode_attention, and Q3_STATUS_TIMEOUT.
+ * each.  Status: Q3_STATUS_BLOCK_RANGE (a table entry outside the pool: its
+ * positions count as zeros; a slot, or a sequence longer than its table: the
+ * sequence's rows are zeros), Q3_STATUS_F16_RANGE, Q3_STATUS_TIMEOUT.
  * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32_t* seq_rows_dev,
                                 const int32_t* seq_pos_dev, const int32_t* seq_slot_dev, int ns, int T, int n_q,
                                 int n_kv, const int32_t* tables_dev, int n_slots, int max_blocks, const void* kv_dev,
                                 int n_blocks, void* out_dev, void* workspace_dev, int64_t workspace_bytes,
                                 int32_t* status_dev, void* stream);
-/* Bytes of workspace for these sizes.  Host only.  Errors: Q3_ERR_INVALID_ARG. */
-int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int n_blocks, int64_t* bytes);
+/* Bytes of workspace for these sizes: mostly an fp16 copy of the blocks a call
+ * may read, min(n_blocks, ns * max_blocks) blocks of n_kv * 16 KB.  Host only.
+ * Errors: Q3_ERR_INVALID_ARG. */
+int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks, int64_t* bytes);
 
 /* q3_op_token_logprobs: for each of N rows of V logits (f32, fp16 or bf16;
  * rows stride elements apart, stride >= V, any alignment of the type):

@@ -110,7 +110,7 @@ def lib():
         f = C.c_float
         L.q3_op_kv4_append.argtypes = [vp, i, i64, vp, vp, f, vp, i, vp, vp, i, i, i, vp, i, i, vp, i, vp, vp, vp, vp]
         L.q3_op_kv4_decode_attention.argtypes = [vp, i, i64, vp, vp, i, i, i, vp, i, i, i, vp, i, vp, i, vp, vp]
-        L.q3_kv4_prefill_workspace.argtypes = [i, i, i, i, i, C.POINTER(i64)]
+        L.q3_kv4_prefill_workspace.argtypes = [i, i, i, i, i, i, C.POINTER(i64)]
         L.q3_op_kv4_prefill_attention.argtypes = [vp, i64, vp, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, vp, i64, vp, vp]
         L.q3_op_token_logprobs.argtypes = [vp, i, i64, i, i, vp, i, vp, vp, vp, vp, vp, vp]
         _lib = L
@@ -441,10 +441,10 @@ def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: to
     return out
 
 
-def kv4_prefill_workspace(ns: int, T: int, n_q: int, n_kv: int, n_blocks: int) -> int:
+def kv4_prefill_workspace(ns: int, T: int, n_q: int, n_kv: int, max_blocks: int, n_blocks: int) -> int:
     """Bytes of workspace op_kv4_prefill_attention needs for these sizes.  Host only (no GPU)."""
     n = C.c_int64()
-    _check(lib().q3_kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks, C.byref(n)))
+    _check(lib().q3_kv4_prefill_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks, C.byref(n)))
     return n.value
 
 
@@ -471,7 +471,7 @@ def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: t
     out = _out(name, out, (T, n_q, 128), torch.float16, q)
     if T == 0 or ns == 0:
         return out
-    need = kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks)
+    need = kv4_prefill_workspace(ns, T, n_q, n_kv, tables.shape[1], n_blocks)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:

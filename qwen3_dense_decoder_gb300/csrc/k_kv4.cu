@@ -500,71 +500,161 @@ cudaError_t launch_decode_nt(const Launch& L, const Kv4DecodeArgs& a, int q_type
     return out_type == Q3_TYPE_F32 ? launch_decode<NT, __half, float>(L, a, C) : launch_decode<NT, __half, __half>(L, a, C);
 }
 
-// ---------------------------------------------------------------- prefill attention, a row and head at a time
-Q3_DEV __half kv4_value(const uint8_t* tile, bool v, int r, int d) {
-    const int grp = d / 32, i = d % 32, g = i / 4;
-    const int at = v ? (r / 2) * 128 + g * 16 + grp * 4 + (r & 1) * 2 + (i & 3) / 2 : r * 64 + d / 2;
-    const int c = tile[at] >> (4 * (d & 1)) & 15;
-    const __half* par = reinterpret_cast<const __half*>(tile + KV4_CODES);
-    const __half s = v ? par[(r / 2) * 16 + grp * 4 + (r & 1)] : par[r * 8 + grp * 2];
-    const __half b = v ? par[(r / 2) * 16 + grp * 4 + 2 + (r & 1)] : par[r * 8 + grp * 2 + 1];
-    return __hfma(s, __int2half_rn(c), b);
+// ---------------------------------------------------------------- prefill: tile list and fp16 copy
+// A prompt's attention reads every block once per query tile, so its blocks
+// are expanded once, into an fp16 copy that the tcgen05 kernel (k_attn_tc.cu)
+// fetches with TMA: 80 + 256 bytes a position and head against 512 flop a row
+// and position.  A warp expands one tile: 4-byte code words in, 16-byte words
+// out, both coalesced.  Places at or past the sequence's end hold whatever
+// the pool holds, made finite (their weights are zero).
+//
+// CTA 0 first lists the query tiles, longest context first: a counting sort by
+// context in 1,024 classes (order within a class does not matter).
+constexpr int XT = 256;
+constexpr int CLASSES = 1024;
+
+struct Seq {
+    int row0, rows, skip, pos0, slot;      // rows without the skipped ones (negative positions), the first one's position
+};
+// Sequence i; rows 0 where it cannot be attended (then skip covers its rows)
+Q3_DEV Seq seq_of(const Kv4PrefillArgs& a, int i, bool& bad) {
+    Seq s;
+    const int r0 = max(a.seq_rows[i], 0), n = max(min(a.seq_rows[i + 1], a.T) - r0, 0);
+    const int pos = a.seq_pos[i];
+    s.slot = a.seq_slot ? a.seq_slot[i] : i;
+    s.skip = pos < 0 ? (int)min((int64_t)n, -(int64_t)pos) : 0;
+    s.pos0 = max(pos, 0);
+    bad = n > s.skip && (s.slot < 0 || s.slot >= a.n_slots || (int64_t)s.pos0 + (n - s.skip) > (int64_t)a.max_blocks * 32);
+    if (bad) s.skip = n;
+    s.rows = n - s.skip;
+    s.row0 = r0 + s.skip;
+    return s;
 }
 
-__global__ void __launch_bounds__(AW * 32) kv4_prefill_kernel(const Kv4PrefillArgs a)
-{
-    __shared__ float s_m[AW], s_l[AW], s_o[AW][D];
-    grid_dep_wait();
-    const int t = blockIdx.y, h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int i = 0;
-    while (i < a.ns && !(a.seq_rows[i] <= t && t < a.seq_rows[i + 1])) ++i;
-    if (i == a.ns) return;                               // a row of no sequence
-    const int slot = a.seq_slot ? a.seq_slot[i] : i;
-    int ctx = a.seq_pos[i] + t - a.seq_rows[i] + 1;
-    if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
-        if (threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        ctx = 0;
-    }
-    const int kvh = h / (a.n_q / a.n_kv);
-    const int* table = a.tables + (size_t)max(slot, 0) * a.max_blocks;
-    float qv[4];
-    load4(a.q + (size_t)t * a.q_stride + h * D, lane, qv);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const float scale = 1.4426950408889634f * 0.08838834764831845f;
-    for (int p = warp; p < ctx; p += AW) {
-        const int blk = table[p / 32];
-        if (blk < 0 || blk >= a.n_blocks) {
-            if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-            continue;
-        }
-        const uint8_t* kt = a.kv + ((size_t)blk * 2 * a.n_kv + kvh) * KV4_TILE;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = fmaf(qv[e], __half2float(kv4_value(kt, false, p % 32, lane * 4 + e)), s);
-        s = warp_allsum(s) * scale;
-        const float mn = fmaxf(m, s), alpha = exp2f(m - mn), w = exp2f(s - mn);
-        m = mn;
-        l = l * alpha + w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] = o[e] * alpha + w * __half2float(kv4_value(kt + (size_t)a.n_kv * KV4_TILE, true, p % 32, lane * 4 + e));
-    }
-    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s_o[warp][lane * 4 + e] = o[e];
+Q3_DEV void plan_tiles(const Kv4PrefillArgs& a) {
+    __shared__ int s_most, s_at[CLASSES];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) s_most = 0;
+    for (int i = threadIdx.x; i < CLASSES; i += XT) s_at[i] = 0;
     __syncthreads();
-    const int d = threadIdx.x;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int w = 0; w < AW; ++w) M = fmaxf(M, s_m[w]);
-    if (M != -INFINITY)
-        for (int w = 0; w < AW; ++w) {
-            const float e = exp2f(s_m[w] - M);
-            L = fmaf(s_l[w], e, L);
-            O = fmaf(s_o[w][d], e, O);
+    bool bad;
+    for (int i = threadIdx.x; i < a.ns; i += XT) {
+        const Seq s = seq_of(a, i, bad);
+        if (bad) report(a.status, Q3_STATUS_BLOCK_RANGE);
+        if (s.rows) atomicMax(&s_most, s.pos0 + s.rows);
+    }
+    __syncthreads();
+    const float per = (float)CLASSES / (float)(s_most + 1);
+    auto each = [&](auto&& f) {                          // a warp a sequence, a lane a tile
+        for (int i = warp; i < a.ns; i += XT / 32) {
+            bool b;
+            const Seq s = seq_of(a, i, b);
+            for (int k = lane * a.rows_per_tile; k < s.rows; k += 32 * a.rows_per_tile) {
+                const int rows = min(a.rows_per_tile, s.rows - k);
+                const int last = s.pos0 + k + rows - 1;
+                f(CLASSES - 1 - min((int)((float)last * per), CLASSES - 1), make_int4(s.row0 + k, rows, s.pos0 + k, i));
+            }
         }
-    bool bad = false;
-    a.out[((size_t)t * a.n_q + h) * D + d] = to_f16(L > 0.f ? O / L : 0.f, bad);
-    if (bad) report(a.status, Q3_STATUS_F16_RANGE);
+    };
+    each([&](int c, const int4&) { atomicAdd(&s_at[c], 1); });
+    __syncthreads();
+    if (warp == 0) {                                     // counts to first places
+        int base = 0;
+        for (int i = lane; i < CLASSES; i += 32) {
+            const int n = s_at[i];
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            s_at[i] = base + x - n;
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) *a.n_tiles = base;
+    }
+    __syncthreads();
+    each([&](int c, const int4& t) { a.tiles[atomicAdd(&s_at[c], 1)] = t; });
+    // rows that attend nothing
+    for (int i = 0; i < a.ns; ++i) {
+        const Seq s = seq_of(a, i, bad);
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)(s.row0 - s.skip) * a.n_q * D);
+        for (int64_t k = threadIdx.x; k < (int64_t)s.skip * a.n_q * (D / 8); k += XT) dst[k] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// infinities and NaN of an fp16 pair become zeros
+Q3_DEV uint32_t finite_pair(uint32_t v) {
+    if ((v & 0x7c00u) == 0x7c00u) v &= 0xffff0000u;
+    if ((v & 0x7c000000u) == 0x7c000000u) v &= 0xffffu;
+    return v;
+}
+
+__global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
+{
+    grid_dep_launch();
+    grid_dep_wait();
+    if (blockIdx.x == 0) plan_tiles(a);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (XT / 32);
+    int64_t u = (int64_t)blockIdx.x * (XT / 32) + warp;      // unit: (block, K or V, KV head) of the sequences in turn
+    int64_t base = 0;
+    for (int i = 0; i < a.ns; ++i) {
+        bool bad;
+        const Seq s = seq_of(a, i, bad);
+        if (!s.rows) continue;
+        const int end = s.pos0 + s.rows, units = 2 * a.n_kv;
+        const int64_t n = (int64_t)((end + 31) / 32) * units;
+        for (; u < base + n; u += step) {
+            const int j = (int)((u - base) / units), part = (int)((u - base) % units);
+            const int phys = a.tables[(size_t)s.slot * a.max_blocks + j];
+            if (phys < 0 || phys >= a.n_blocks) {            // the attention kernel leaves its places zero
+                if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
+                continue;
+            }
+            const uint8_t* src = a.kv + ((size_t)phys * units + part) * KV4_TILE;
+            __half* dst = a.copy + ((size_t)(a.by_seq ? i * a.max_blocks + j : phys) * units + part) * (32 * D);
+            const int n_pos = min(32, end - 32 * j);
+            if (part < a.n_kv) {
+#pragma unroll 4
+                for (int k = 0; k < 16; ++k) {               // two positions a step, eight dimensions a lane
+                    const int p = 2 * k + (lane >> 4), c = lane & 15;
+                    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src + p * 64) + c);
+                    const __half2 sb = *reinterpret_cast<const __half2*>(src + KV4_CODES + p * 16 + (c >> 2) * 4);
+                    const __half2 sc = __low2half2(sb), bi = __high2half2(sb);
+                    const uint32_t p0 = kv4_pair<0>(w, sc, bi), p1 = kv4_pair<1>(w, sc, bi), p2 = kv4_pair<2>(w, sc, bi),
+                                   p3 = kv4_pair<3>(w, sc, bi);
+                    uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
+                                         __byte_perm(p2, p3, 0x7632));
+                    if (p >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+                    *reinterpret_cast<uint4*>(dst + p * D + c * 8) = o;
+                }
+            } else {
+#pragma unroll 4
+                for (int k = 0; k < 8; ++k) {                // two position pairs a step
+                    const int pr = 2 * k + (lane >> 4), gr = (lane & 15) >> 2, m = lane & 3;
+                    const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(src + pr * 128 + 2 * m * 16) + gr);
+                    const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(src + pr * 128 + (2 * m + 1) * 16) + gr);
+                    const uint2 sb = *reinterpret_cast<const uint2*>(src + KV4_CODES + pr * 32 + gr * 8);
+                    const __half2 sc = as_h2(sb.x), bi = as_h2(sb.y);
+                    const uint32_t p0 = kv4_pair<0>(w0, sc, bi), p1 = kv4_pair<1>(w0, sc, bi), p2 = kv4_pair<2>(w0, sc, bi),
+                                   p3 = kv4_pair<3>(w0, sc, bi);
+                    const uint32_t r0 = kv4_pair<0>(w1, sc, bi), r1 = kv4_pair<1>(w1, sc, bi), r2 = kv4_pair<2>(w1, sc, bi),
+                                   r3 = kv4_pair<3>(w1, sc, bi);
+                    uint4 e = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(r0, r1, 0x5410),
+                                         __byte_perm(r2, r3, 0x5410));
+                    uint4 o = make_uint4(__byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632), __byte_perm(r0, r1, 0x7632),
+                                         __byte_perm(r2, r3, 0x7632));
+                    if (2 * pr >= n_pos) e = make_uint4(finite_pair(e.x), finite_pair(e.y), finite_pair(e.z), finite_pair(e.w));
+                    if (2 * pr + 1 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+                    uint4* to = reinterpret_cast<uint4*>(dst + 2 * pr * D + 32 * gr + 8 * m);
+                    to[0] = e;
+                    to[D / 8] = o;
+                }
+            }
+        }
+        base += n;
+    }
 }
 
 }  // namespace
@@ -584,9 +674,9 @@ cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_typ
     return a.n_q / a.n_kv <= 4 ? launch_decode_nt<1>(L, a, q_type, out_type) : launch_decode_nt<2>(L, a, q_type, out_type);
 }
 
-cudaError_t launch_kv4_prefill(const Launch& L, const Kv4PrefillArgs& a)
+cudaError_t launch_kv4_expand(const Launch& L, const Kv4PrefillArgs& a)
 {
-    return launch_ex(L, kv4_prefill_kernel, dim3(a.n_q, a.T), dim3(AW * 32), a);
+    return launch_ex(L, kv4_expand_kernel, dim3(4 * 152), dim3(XT), a);
 }
 
 }  // namespace q3

@@ -96,6 +96,20 @@ bool tmap_kv(CUtensorMap* m, const void* ptr, uint64_t rows)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The fp16 copy of the 4-bit cache, in the same boxes.
+bool tmap_kv16(CUtensorMap* m, const void* ptr, uint64_t rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {128, rows};
+    cuuint64_t strides[1] = {256};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t elem[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 struct Q8Planes {
@@ -2112,6 +2126,50 @@ bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int
            max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) && n_blocks >= 1;
 }
 
+// The prefill attention's workspace: a tile count and a spare status word, the
+// tile list, the fp16 copy of the blocks (numbered as in the pool, or by
+// sequence where that is fewer).
+struct Kv4Workspace {
+    size_t tiles, copy, bytes;
+    int64_t blocks;
+    bool by_seq;
+};
+Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks)
+{
+    Kv4Workspace w;
+    w.by_seq = (int64_t)ns * max_blocks < n_blocks;
+    w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
+    w.tiles = 256;
+    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
+    w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
+    return w;
+}
+
+// expansion, then attention over the copy, on the workspace at ws
+cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int n_sm)
+{
+    const Kv4Workspace w = kv4_workspace(a.ns, a.T, a.n_q, a.n_kv, a.max_blocks, a.n_blocks);
+    int* head = reinterpret_cast<int*>(ws);
+    a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
+    a.n_tiles = head;
+    a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
+    a.copy = reinterpret_cast<f16*>(ws + w.copy);
+    a.by_seq = w.by_seq;
+    CUtensorMap map;
+    if (!tmap_kv16(&map, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32)) return cudaErrorInvalidValue;
+    if (cudaError_t e = launch_kv4_expand(L, a)) return e;
+    PrefillAttnArgs p{};
+    p.q = a.q; p.q_stride = a.q_stride;
+    p.T = a.T; p.n_q = a.n_q; p.n_kv = a.n_kv;
+    p.tables = a.tables; p.max_blocks = a.max_blocks; p.n_blocks = a.n_blocks;
+    p.seq_slot = a.seq_slot; p.by_seq = a.by_seq;
+    p.tiles = a.tiles; p.n_tiles_dev = a.n_tiles;
+    p.out = a.out;
+    p.status = a.status ? a.status : head + 1;       // a spare word nobody reads
+    const Launch after{L.stream, true, L.counter};   // its setup overlaps the expansion
+    return launch_prefill_attention_kv4(after, map, p, n_sm);
+}
+
 bool row_stride_ok(int64_t stride, int type, int64_t width)
 {
     return stride >= width && stride % (type == Q3_TYPE_F32 ? 4 : 8) == 0;
@@ -2182,11 +2240,12 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
     return Q3_OK;
 }
 
-int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int n_blocks, int64_t* bytes)
+int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks, int64_t* bytes)
 {
-    if (!bytes || ns < 0 || T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv || n_blocks < 1)
+    if (!bytes || ns < 0 || T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv || n_q > 8 * n_kv || max_blocks < 1 ||
+        max_blocks > (1 << 20) || n_blocks < 1)
         return fail(Q3_ERR_INVALID_ARG, "kv4_prefill_workspace: bad argument");
-    *bytes = 0;
+    *bytes = (int64_t)kv4_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks).bytes;
     return Q3_OK;
 }
 
@@ -2201,10 +2260,11 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: bad argument");
     if (!row_stride_ok(q_stride, Q3_TYPE_F16, (int64_t)n_q * 128))
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: row stride too small or not a multiple of 16 bytes");
-    int64_t need = 0;
-    q3_kv4_prefill_workspace(ns, T, n_q, n_kv, n_blocks, &need);
-    if (need && (!workspace_dev || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
-        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: workspace of %lld bytes, 256-byte aligned", (long long)need);
+    const Kv4Workspace w = kv4_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks);
+    if (T > 0 && ns > 0 && (!workspace_dev || workspace_bytes < (int64_t)w.bytes || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: workspace of %lld bytes, 256-byte aligned", (long long)w.bytes);
+    if (w.blocks * 2 * n_kv * 32 > 0x7fffffffll)
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: more than 2^31 cache rows in one call");
     if (!aligned16(q_dev) || !aligned16(out_dev))
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: pointers must be 16-byte aligned");
     if (T == 0 || ns == 0) return Q3_OK;
@@ -2215,8 +2275,11 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
     a.tables = tables_dev; a.n_slots = n_slots; a.max_blocks = max_blocks;
     a.kv = static_cast<const uint8_t*>(kv_dev); a.n_blocks = n_blocks;
     a.out = static_cast<f16*>(out_dev); a.status = status_dev;
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return fail(Q3_ERR_CUDA, "op_kv4_prefill_attention: no CUDA device");
     const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
-    const cudaError_t e = launch_kv4_prefill(L, a);
+    const cudaError_t e = run_kv4_prefill(L, a, static_cast<uint8_t*>(workspace_dev), n_sm);
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_prefill_attention: %s", cudaGetErrorString(e));
     return Q3_OK;
 }

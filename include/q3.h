@@ -99,7 +99,14 @@ typedef struct q3_session q3_session;
  * clamped to [-127, 127] -- 136 bytes per head row against 256, about 1.9x
  * smaller.  Attention reads fp16(fp16 d * code) (each product rounded once);
  * a Q8_0-cache model runs prefill attention on the mma.sync kernel and
- * one-session decode on the per-operation path. */
+ * one-session decode on the per-operation path.  Q3_AFFINE4 is the 4-bit
+ * cache, opt-in as well: head rows packed by the AFFINE4_GS32 rule straight
+ * from FP32, 80 bytes a row, about 3.2x smaller than BF16 (the operators'
+ * section below states the tiles); a stored value is fp16(scale * code +
+ * bias).  Its prefill rounds attend an fp16 copy of the round's blocks on the
+ * tcgen05 kernel (a pool holds that copy's room for one layer: n_blocks *
+ * n_kv * 16 KB), its decode rounds the 4-bit tiles; one-session decode takes
+ * the per-operation path. */
 typedef struct q3_config {
     int n_layers, hidden, n_q_heads, n_kv_heads, head_dim, ffn, vocab, max_ctx;
     float rope_theta, rms_eps;
@@ -162,8 +169,8 @@ void q3_model_destroy(q3_model* m);
  * library; up to max_sessions sessions draw from it.  One block holds, per
  * layer, K and V of every KV head: 32 * head_dim bf16 values each, or with
  * the Q8_0 cache a tile of 4,096 int8 codes ([32 positions][128]) followed
- * by 128 fp16 scales ([32 positions][4]).  Errors: Q3_ERR_INVALID_ARG,
- * Q3_ERR_OOM. */
+ * by 128 fp16 scales ([32 positions][4]), or with the 4-bit cache a tile of
+ * Q3_KV4_TILE_BYTES.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_OOM. */
 int q3_pool_create(q3_model* m, int n_blocks, int max_sessions, q3_pool** out);
 void q3_pool_destroy(q3_pool* p);
 
@@ -201,6 +208,20 @@ int q3_session_eval(q3_session* s, const int32_t* tokens_dev, int n,
  * Q3_ERR_POOL_EXHAUSTED, Q3_ERR_CUDA, Q3_ERR_POISONED. */
 int q3_session_eval_n(q3_session* s, const int32_t* tokens_dev, int n, int n_logits, float* logits_dev,
                       int32_t* argmax_dev);
+
+/* One round of n tokens appended to the session, as q3_session_eval_n, whose
+ * last n_score rows are scored instead of returned whole: row i (of the
+ * n_score) gives the log probability of targets_dev[i] after its token
+ * (targets_dev: int32 [n_score], -1: none; to score a text, the text itself
+ * moved by one), the entropy of its distribution and its top_k most probable
+ * tokens with their log probabilities, as q3_op_token_logprobs returns them.
+ * Outputs: float [n_score], float [n_score], int32 and float [n_score][top_k];
+ * each may be NULL, targets_dev with logprob_dev.  The logits stay in the
+ * model's scratch, 512 rows at a time (made by the first call: 2 KB * vocab;
+ * Q3_ERR_OOM if it cannot be).  A target outside [-1, vocab) is reported by
+ * q3_sync as Q3_ERR_DEVICE_CHECK.  Errors as q3_session_eval_n. */
+int q3_session_score(q3_session* s, const int32_t* tokens_dev, int n, int n_score, const int32_t* targets_dev, int top_k,
+                     float* logprob_dev, float* entropy_dev, int32_t* top_ids_dev, float* top_logprob_dev);
 
 /* One round over ns distinct sessions of one pool ("Kipp Roadmap", status
  * v0.0.2, kipp_eval_batch): session i appends n[i] tokens.  tokens_dev:
@@ -563,7 +584,8 @@ int q3_model_set_prefill_tc(q3_model* m, int on);
 int q3_model_prefill_tc(const q3_model* m);
 
 /* Bytes one position's K and V take in one layer of the cache: 2 * n_kv *
- * 256 (BF16) or 2 * n_kv * 136 (Q8_0); -1 for a NULL model. */
+ * 256 (BF16), 2 * n_kv * 136 (Q8_0) or 2 * n_kv * 80 (AFFINE4); -1 for a NULL
+ * model. */
 int q3_model_kv_bytes_per_position(const q3_model* m);
 
 /* q3_op_kv_pack_q8_0: the Q8_0 cache writers' packing on caller rows

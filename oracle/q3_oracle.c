@@ -417,8 +417,8 @@ orc_model* orc_model_create(const orc_cfg* cfg, const uint16_t* embed,
                             const orc_layer* layers, int n_threads)
 {
     if (cfg->n_q_heads % cfg->n_kv_heads || cfg->head_dim % 2 ||
-        (cfg->kv_quant != ORC_BF16 && cfg->kv_quant != ORC_Q8_0) ||
-        (cfg->kv_quant == ORC_Q8_0 && cfg->head_dim % ORC_BLOCK) ||
+        (cfg->kv_quant != ORC_BF16 && cfg->kv_quant != ORC_Q8_0 && cfg->kv_quant != ORC_AFFINE4) ||
+        (cfg->kv_quant != ORC_BF16 && cfg->head_dim % ORC_BLOCK) ||
         (cfg->scheme != ORC_BF16 && cfg->scheme != ORC_Q8_0 && cfg->scheme != ORC_AFFINE4) ||
         (cfg->scheme != ORC_BF16 && (cfg->hidden % ORC_BLOCK || cfg->ffn % ORC_BLOCK ||
                                      (cfg->n_q_heads * cfg->head_dim) % ORC_BLOCK)))
@@ -443,10 +443,11 @@ void orc_model_free(orc_model* m)
 
 static long kv_row(const orc_cfg* c) { return (long)c->n_kv_heads * c->head_dim; }
 
-/* Bytes of one position's K (or V) row: bf16 values, or Q8_0 blocks of 32
- * consecutive values (a head row of d values is d/32 whole blocks). */
+/* Bytes of one position's K (or V) row: bf16 values, or Q8_0 blocks or
+ * AFFINE4 groups of 32 consecutive values (a head row of d values is d/32 whole blocks). */
 static long kv_row_bytes(const orc_cfg* c)
 {
+    if (c->kv_quant == ORC_AFFINE4) return kv_row(c) / ORC_BLOCK * ORC_AFFINE4_BYTES;
     return c->kv_quant == ORC_Q8_0 ? kv_row(c) / ORC_BLOCK * ORC_Q8_0_BYTES : kv_row(c) * 2;
 }
 
@@ -756,9 +757,14 @@ static uint8_t* kv_slot(orc_session* s, int l, int p, int is_v)
 }
 
 /* store one position's K (or V) row: rounded to bf16, or packed to Q8_0
- * blocks straight from FP32 (reading: the quantizer of the weights) */
+ * blocks or AFFINE4 groups straight from FP32 (reading: the quantizer of the
+ * weights) */
 static void kv_store(const orc_cfg* c, const float* row, uint8_t* slot)
 {
+    if (c->kv_quant == ORC_AFFINE4) {
+        orc_affine4_pack(row, kv_row(c), slot);
+        return;
+    }
     if (c->kv_quant == ORC_Q8_0) {
         orc_q8_0_pack(row, kv_row(c), slot);
         return;
@@ -770,9 +776,15 @@ static void kv_store(const orc_cfg* c, const float* row, uint8_t* slot)
     }
 }
 
-/* read it back as FP32 values (exact: bf16 widening, or fp16 scale times quant) */
+/* read it back as FP32 values (exact: bf16 widening, or fp16 scale times
+ * quant; a 4-bit value is scale * code + bias rounded to fp16) */
 static void kv_load(const orc_cfg* c, const uint8_t* slot, float* row)
 {
+    if (c->kv_quant == ORC_AFFINE4) {
+        orc_affine4_unpack(slot, kv_row(c), row);
+        for (long i = 0; i < kv_row(c); i++) row[i] = orc_f16_to_f32(orc_f32_to_f16(row[i]));
+        return;
+    }
     if (c->kv_quant == ORC_Q8_0) {
         orc_q8_0_unpack(slot, kv_row(c), row);
         return;

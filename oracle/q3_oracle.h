@@ -53,7 +53,7 @@ typedef struct orc_cfg {
     int tied;     /* 1: lm_head is the token embedding */
     int scheme;   /* ORC_BF16, ORC_Q8_0 or ORC_AFFINE4 (the seven projections only) */
     double rope_theta, rms_eps;
-    int kv_quant; /* ORC_BF16: K/V stored as bf16; ORC_Q8_0: as Q8_0 blocks */
+    int kv_quant; /* ORC_BF16: K/V stored as bf16; ORC_Q8_0: as Q8_0 blocks; ORC_AFFINE4: as AFFINE4 groups */
 } orc_cfg;
 
 /* Per-layer weights, host memory, row-major [out][in].  BF16 tensors are
@@ -100,7 +100,7 @@ void  orc_gqa_attend(const float* q, const uint16_t* K, const uint16_t* V,
                      int ctx, int n_q, int n_kv, int d, float* o);
 
 /* Bytes one position's K and V take in one layer's cache: 2 n_kv d (bf16)
- * or 2 n_kv (d/32) 34 (Q8_0 blocks). */
+ * or 2 n_kv (d/32) 34 (Q8_0 blocks) or 2 n_kv (d/32) 20 (AFFINE4 groups). */
 long  orc_kv_bytes_per_position(const orc_cfg* c);
 
 /* ---- model / KV / sessions ---- */

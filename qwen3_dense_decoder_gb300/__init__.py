@@ -112,6 +112,7 @@ def lib():
         L.q3_op_kv4_decode_attention.argtypes = [vp, i, i64, vp, vp, i, i, i, vp, i, i, i, vp, i, vp, i, vp, vp]
         L.q3_kv4_prefill_workspace.argtypes = [i, i, i, i, i, i, C.POINTER(i64)]
         L.q3_op_kv4_prefill_attention.argtypes = [vp, i64, vp, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, vp, i64, vp, vp]
+        L.q3_session_score.argtypes = [vp, vp, i, i, vp, i, vp, vp, vp, vp]
         L.q3_op_token_logprobs.argtypes = [vp, i, i64, i, i, vp, i, vp, vp, vp, vp, vp, vp]
         _lib = L
     return _lib
@@ -361,9 +362,17 @@ def _rows(name: str, q: torch.Tensor, types: tuple) -> None:
         raise ValueError(f"{name}: q must be [T, n_q, 128] of {types} with contiguous rows")
 
 
-def _out(name: str, out, shape: tuple, dtype, like: torch.Tensor) -> torch.Tensor:
-    if out is None:
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory of the stream that writes it: none of its earlier uses can still be running."""
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(name: str, out, shape: tuple, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    if out is None:
+        return _new(shape, dtype, like, stream)
     if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError(f"{name}: outputs must be contiguous {dtype} {list(shape)}")
     return out
@@ -404,9 +413,9 @@ def op_kv4_append(qkv: torch.Tensor, q_gain: torch.Tensor, k_gain: torch.Tensor,
         raise ValueError(f"{name}: rope must be f32 [n, 64, 2]")
     _int32(name, "row_pos", row_pos, (T,))
     _int32(name, "row_slot", row_slot, (T,))
-    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv)
+    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv, stream)
     if kv_out is not None:
-        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv)
+        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv, stream)
     if T == 0:
         return q_out
     _launch(name, lib().q3_op_kv4_append, stream,
@@ -431,7 +440,7 @@ def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: to
     T, n_q, _ = q.shape
     _int32(name, "row_pos", row_pos, (T,))
     _int32(name, "row_slot", row_slot, (T,))
-    out = _out(name, out, (T, n_q, 128), torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16, q)
+    out = _out(name, out, (T, n_q, 128), torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16, q, stream)
     if T == 0:
         return out
     _launch(name, lib().q3_op_kv4_decode_attention, stream, (q, row_pos, row_slot, tables, kv, out, status),
@@ -468,12 +477,12 @@ def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: t
     _int32(name, "seq_pos", seq_pos, (ns,))
     if seq_slot is not None:
         _int32(name, "seq_slot", seq_slot, (ns,))
-    out = _out(name, out, (T, n_q, 128), torch.float16, q)
+    out = _out(name, out, (T, n_q, 128), torch.float16, q, stream)
     if T == 0 or ns == 0:
         return out
     need = kv4_prefill_workspace(ns, T, n_q, n_kv, tables.shape[1], n_blocks)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(need, torch.uint8, q, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"{name}: workspace must be contiguous uint8, at least {need} bytes")
     _launch(name, lib().q3_op_kv4_prefill_attention, stream, (q, seq_rows, seq_pos, seq_slot, tables, kv, out, workspace, status),
@@ -500,11 +509,10 @@ def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None,
         _int32(name, "status", status, (1,))
     if top_k < 0:
         raise ValueError(f"{name}: top_k must not be negative")
-    f32, dev = torch.float32, logits.device
-    logprob = None if targets is None else torch.empty(N, dtype=f32, device=dev)
-    entropy = torch.empty(N, dtype=f32, device=dev)
-    ids = torch.empty((N, top_k), dtype=torch.int32, device=dev)
-    values = torch.empty((N, top_k), dtype=f32, device=dev)
+    logprob = None if targets is None else _new(N, torch.float32, logits, stream)
+    entropy = _new(N, torch.float32, logits, stream)
+    ids = _new((N, top_k), torch.int32, logits, stream)
+    values = _new((N, top_k), torch.float32, logits, stream)
     if N == 0:
         return logprob, entropy, ids, values
     _launch(name, lib().q3_op_token_logprobs, stream, (logits, targets, logprob, entropy, ids, values, status),
@@ -526,7 +534,7 @@ class Model:
     def __init__(self, shape, weights: dict, max_ctx: int, max_round_tokens: int = 2048,
                  stream=None):
         kv_scheme = getattr(shape, "kv_quant", BF16)
-        if kv_scheme not in (BF16, Q8_0):
+        if kv_scheme not in (BF16, Q8_0, AFFINE4):
             raise ValueError(f"unknown K/V cache scheme {kv_scheme}")
         self.shape = shape
         self.stream = stream or torch.cuda.current_stream()
@@ -700,6 +708,32 @@ class Session:
         assert logits.is_contiguous() and logits.numel() >= n_logits * logits.shape[-1]
         _check(lib().q3_session_eval_n(self.h, _ptr(tokens), tokens.numel(), n_logits, _ptr(logits),
                                        _ptr(argmax)))
+
+    def score(self, tokens: torch.Tensor, targets: torch.Tensor | None = None, n_score: int | None = None,
+              top_k: int = 0):
+        """Append a round of tokens and score its last n_score rows (default:
+        as many as there are targets, or all): the log probability of each
+        row's target (int32, -1: none; None without targets), the entropy, and
+        the top_k most probable tokens with their log probabilities, as
+        op_token_logprobs returns them.  On the model's stream."""
+        n = tokens.numel()
+        if n_score is None:
+            n_score = n if targets is None else targets.numel()
+        if tokens.dtype != torch.int32 or not tokens.is_cuda or not tokens.is_contiguous():
+            raise ValueError("score: tokens must be contiguous int32 on the model's device")
+        if targets is not None:
+            if targets.get_device() != tokens.get_device():
+                raise ValueError("score: targets must be on the tokens' device")
+            _int32("score", "targets", targets, (n_score,))
+        if n_score < 1 or n_score > n or top_k < 0:
+            raise ValueError("score: n_score must be in [1, tokens] and top_k not negative")
+        stream = self.pool.model.stream
+        logprob = None if targets is None else _new(n_score, torch.float32, tokens, stream)
+        entropy, ids = _new(n_score, torch.float32, tokens, stream), _new((n_score, top_k), torch.int32, tokens, stream)
+        values = _new((n_score, top_k), torch.float32, tokens, stream)
+        _check(lib().q3_session_score(self.h, tokens.data_ptr(), n, n_score, _p(targets), top_k, _p(logprob), entropy.data_ptr(),
+                                      ids.data_ptr() or None, values.data_ptr() or None))
+        return logprob, entropy, ids, values
 
     def eval(self, tokens: torch.Tensor, logits: torch.Tensor,
              argmax: torch.Tensor | None = None) -> None:

@@ -79,7 +79,18 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
         return;
     }
     float y[4];
-    load4(static_cast<const Tin*>(a.qkv) + (size_t)t * a.qkv_stride + (size_t)hh * D, lane, y);
+    const size_t at = (size_t)t * a.qkv_stride + (size_t)hh * D;
+    if (sizeof(Tin) == 4 && a.n_parts > 1) {
+        y[0] = y[1] = y[2] = y[3] = 0.f;
+        for (int i = 0; i < a.n_parts; ++i) {
+            float z[4];
+            load4(a.parts + (size_t)i * a.T * a.qkv_stride + at, lane, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += z[e];
+        }
+    } else {
+        load4(static_cast<const Tin*>(a.qkv) + at, lane, y);
+    }
     if (is_q || is_k)
         head_norm_rope(y, is_q ? a.q_gain : a.k_gain, a.rope + (size_t)pos * (D / 2), a.eps, lane);
     if (is_q) {
@@ -94,8 +105,8 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
     __half scale, bias, val[4];
     if (!kv4_pack(y, codes, scale, bias, val)) report(a.status, Q3_STATUS_F16_RANGE);
     if (dst) store4(dst, lane, val);
-    const int slot = a.row_slot[t], at = pos / 32;
-    const int blk = slot >= 0 && slot < a.n_slots && at < a.max_blocks ? a.tables[(size_t)slot * a.max_blocks + at] : -1;
+    const int slot = a.row_slot[t], j = pos / 32;
+    const int blk = slot >= 0 && slot < a.n_slots && j < a.max_blocks ? a.tables[(size_t)slot * a.max_blocks + j] : -1;
     if (blk < 0 || blk >= a.n_blocks) {
         if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
         return;

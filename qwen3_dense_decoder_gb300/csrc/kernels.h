@@ -335,6 +335,8 @@ cudaError_t launch_kv_pack_q8(cudaStream_t s, const float* rows, int n, uint8_t*
 struct Kv4AppendArgs {
     const void* qkv;           // [T] rows, qkv_stride elements apart
     int64_t qkv_stride;
+    const float* parts;        // f32, with n_parts > 1: a split-K GEMM's partials instead, [part][T][row], summed
+    int n_parts;               // here in order
     const __nv_bfloat16* q_gain;
     const __nv_bfloat16* k_gain;
     float eps;

@@ -188,6 +188,8 @@ struct q3_model {
     int* pre_counter = nullptr;     // work queue of the prefill attention, zero between launches
     int n_sm = 0;
     bool kv_q8 = false;             // the opt-in Q8_0 K/V cache
+    bool kv4 = false;               // the opt-in 4-bit K/V cache
+    float* score_logits = nullptr;  // [SCORE_ROWS][vocab], made by the first scoring round
     bool prefill_tc_ok = false;     // the tcgen05 prefill attention supports these shapes
     bool prefill_tc = true;         // use it when prefill_tc_ok
 
@@ -307,6 +309,7 @@ struct q3_pool {
     size_t block_bytes = 0;      // one block of one layer: K and V of every KV head
     CUtensorMap kv_map;          // kv as rows of 128 (tcgen05 prefill attention)
     int* tables = nullptr;       // [max_sessions][max_blocks]
+    uint8_t* kv4_ws = nullptr;   // 4-bit cache: the prefill attention's tile list and fp16 copy of one layer's blocks
 #ifdef Q3_TEST_FAULTS
     int* fault_tables = nullptr; // faults 1, 3 (readers) and 4 (writers): the perturbed tables
 #endif
@@ -430,7 +433,7 @@ int validate_config(const q3_config* c)
         return fail(Q3_ERR_INVALID_ARG, "config: hidden, ffn and vocab must be multiples of 128");
     if (c->scheme != Q3_BF16 && c->scheme != Q3_Q8_0 && c->scheme != Q3_AFFINE4)
         return fail(Q3_ERR_INVALID_ARG, "config: unknown weight scheme %d", c->scheme);
-    if (c->kv_scheme != Q3_BF16 && c->kv_scheme != Q3_Q8_0)
+    if (c->kv_scheme != Q3_BF16 && c->kv_scheme != Q3_Q8_0 && c->kv_scheme != Q3_AFFINE4)
         return fail(Q3_ERR_INVALID_ARG, "config: unknown K/V cache scheme %d", c->kv_scheme);
     if (!(c->rms_eps > 0.f) || !(c->rope_theta > 0.f))
         return fail(Q3_ERR_INVALID_ARG, "config: rms_eps and rope_theta must be positive");
@@ -442,10 +445,70 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // bytes of one 32-position block of one layer: K and V of every KV head
 size_t kv_block_bytes(const q3_model* m)
 {
-    return (size_t)2 * m->c.n_kv_heads * (m->kv_q8 ? KVQ_TILE : 32 * 128 * 2);
+    return (size_t)2 * m->c.n_kv_heads * (m->kv4 ? KV4_TILE : m->kv_q8 ? KVQ_TILE : 32 * 128 * 2);
+}
+
+// ---------------------------------------------------------------- 4-bit cache prefill
+
+// The prefill attention's workspace: a tile count and a spare status word, the
+// tile list, the fp16 copy of the blocks (numbered as in the pool, or by
+// sequence where that is fewer).
+struct Kv4Workspace {
+    size_t tiles, copy, bytes;
+    int64_t blocks;
+    bool by_seq;
+};
+Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks)
+{
+    Kv4Workspace w;
+    w.by_seq = (int64_t)ns * max_blocks < n_blocks;
+    w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
+    w.tiles = 256;
+    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
+    w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
+    return w;
+}
+
+// expansion, then attention over the copy, on the workspace at ws
+cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int n_sm)
+{
+    const Kv4Workspace w = kv4_workspace(a.ns, a.T, a.n_q, a.n_kv, a.max_blocks, a.n_blocks);
+    int* head = reinterpret_cast<int*>(ws);
+    a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
+    a.n_tiles = head;
+    a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
+    a.copy = reinterpret_cast<f16*>(ws + w.copy);
+    a.by_seq = w.by_seq;
+    CUtensorMap map;
+    if (!tmap_kv16(&map, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32)) return cudaErrorInvalidValue;
+    if (cudaError_t e = launch_kv4_expand(L, a)) return e;
+    PrefillAttnArgs p{};
+    p.q = a.q; p.q_stride = a.q_stride;
+    p.T = a.T; p.n_q = a.n_q; p.n_kv = a.n_kv;
+    p.tables = a.tables; p.max_blocks = a.max_blocks; p.n_blocks = a.n_blocks;
+    p.seq_slot = a.seq_slot; p.by_seq = a.by_seq;
+    p.tiles = a.tiles; p.n_tiles_dev = a.n_tiles;
+    p.out = a.out;
+    p.status = a.status ? a.status : head + 1;       // a spare word nobody reads
+    const Launch after{L.stream, true, L.counter};   // its setup overlaps the expansion
+    return launch_prefill_attention_kv4(after, map, p, n_sm);
 }
 
 // ---------------------------------------------------------------- the round
+
+// Rows of logits a scoring round holds at a time: the lm_head is read once per
+// chunk (0.8 GB at 151,936 x 2,560), which 512 rows of products cover.
+constexpr int SCORE_ROWS = 512;
+
+// What a scoring round returns of its last n_out rows instead of their logits.
+struct Score {
+    const int32_t* targets;
+    int top;
+    float* logprob;
+    float* entropy;
+    int32_t* top_ids;
+    float* top_logprob;
+};
 
 struct Round {
     int T = 0, ns = 0;
@@ -461,6 +524,7 @@ struct Round {
     int n_tiles = 0;                 // query tiles (prefill attention)
     bool attn_tc = false;            // the tiles and schedule are the tcgen05 kernel's
     int attn_grid = 0;               // its CTAs
+    const Score* score = nullptr;    // scores of the logit rows, which then stay in the model's scratch
 };
 
 #ifndef Q3_ATTN_BATCH_BPW
@@ -676,7 +740,7 @@ int setup_decode_step(q3_model* m, int n_sm)
 {
     const q3_config& c = m->c;
     if (c.scheme == Q3_AFFINE4) return Q3_OK;   // no AFFINE4 consumer in the step
-    if (m->kv_q8) return Q3_OK;                 // the step reads the BF16 cache only
+    if (m->kv_q8 || m->kv4) return Q3_OK;       // the step reads the BF16 cache only
 #ifdef Q3_TEST_FAULTS
     if (m->fault) return Q3_OK;                 // planted faults reach the per-operation kernels only
 #endif
@@ -770,6 +834,27 @@ int run_decode_step(q3_model* m, const Round& r)
     return rc;
 }
 
+// The scores of n rows, from row `first` of the scored ones, whose logits are
+// in the model's scratch.
+int score_rows(q3_model* m, const Round& r, int first, int n)
+{
+    const Score& s = *r.score;
+    LogprobArgs a{};
+    a.logits = m->score_logits; a.stride = m->c.vocab;
+    a.N = n; a.V = m->c.vocab; a.top = s.top;
+    a.targets = s.targets ? s.targets + first : nullptr;
+    a.logprob = s.logprob ? s.logprob + first : nullptr;
+    a.entropy = s.entropy ? s.entropy + first : nullptr;
+    a.top_ids = s.top_ids ? s.top_ids + (size_t)first * s.top : nullptr;
+    a.top_logprob = s.top_logprob ? s.top_logprob + (size_t)first * s.top : nullptr;
+    a.status = m->status;
+    const Launch L{m->stream, m->pdl && !m->prof_on, &m->launches};
+    m->prof_begin(Q3_K_OTHER);
+    const int rc = m->check(launch_logprobs(L, a, Q3_TYPE_F32), "token log probabilities");
+    m->prof_end();
+    return rc;
+}
+
 int run_round(q3_model* m, const Round& r)
 {
     const q3_config& c = m->c;
@@ -796,7 +881,10 @@ int run_round(q3_model* m, const Round& r)
         m->prof_end();
         return e;
     };
-    if (one && r.ns == 1 && m->step_ok && m->fused_decode) return run_decode_step(m, r);
+    if (one && r.ns == 1 && m->step_ok && m->fused_decode) {
+        const int rc = run_decode_step(m, r);
+        return rc || !r.score ? rc : score_rows(m, r, 0, 1);
+    }
     const size_t layer_kv = (size_t)r.pool->n_blocks * 2 * c.n_kv_heads * 32 * 128;   // bf16 cache
     const size_t layer_bytes = (size_t)r.pool->n_blocks * r.pool->block_bytes;
     const int n_splits = attention_splits(m, T, r.max_ctx);
@@ -820,7 +908,7 @@ int run_round(q3_model* m, const Round& r)
         // (BF16 cache, no K split) or in their own kernel; decode rounds: the
         // attention sums the QKV partials and does all three itself
         RopeArgs ra{};
-        if (!r.decode) {
+        if (!r.decode || m->kv4) {
             ra.qkv = m->qkv; ra.T = T; ra.n_q = c.n_q_heads; ra.n_kv = c.n_kv_heads;
             ra.q_gain = static_cast<const bf16*>(W.q_norm);
             ra.k_gain = static_cast<const bf16*>(W.k_norm);
@@ -853,19 +941,57 @@ int run_round(q3_model* m, const Round& r)
                                "rmsnorm")))
                 return rc;
             ha_ready = false;
-            const bool head_epi_ok = !r.decode && !m->kv_q8 && c.head_dim == 128;
+            const bool head_epi_ok = !r.decode && !m->kv_q8 && !m->kv4 && c.head_dim == 128;
             rc = gemm(m, &Mp.m[P_Q], &Mp.m[P_K], &Mp.m[P_V], m->qw / 128, (m->qw + m->kvw) / 128, 0,
                       m->qkvw, T, H, m->ha, EPI_STORE_F32, m->qkv, m->qkvw, nullptr, nullptr, nullptr,
                       r.decode ? &qkv_splits : nullptr, head_epi_ok ? &ra : nullptr, &roped);
             if (rc) return rc;
         }
-        if (!r.decode && !roped &&
+        if (m->kv4) {
+            Kv4AppendArgs ka{};
+            ka.qkv = m->qkv; ka.qkv_stride = m->qkvw;
+            if (!one && qkv_splits > 1) { ka.parts = m->ws; ka.n_parts = qkv_splits; }
+            ka.q_gain = ra.q_gain; ka.k_gain = ra.k_gain; ka.eps = ra.eps;
+            ka.rope = m->rope; ka.rope_len = c.max_ctx;
+            ka.row_pos = ra.row_pos; ka.row_slot = ra.row_slot;
+            ka.T = T; ka.n_q = c.n_q_heads; ka.n_kv = c.n_kv_heads;
+            ka.tables = ra.tables; ka.n_slots = r.pool->max_sessions; ka.max_blocks = r.pool->max_blocks;
+            ka.kv = reinterpret_cast<uint8_t*>(r.pool->kv) + (size_t)l * layer_bytes; ka.n_blocks = r.pool->n_blocks;
+            ka.q_out = m->q16; ka.status = m->status;
+            if ((rc = m->check(run(Q3_K_ROPE, [&] { return launch_kv4_append(L, ka, Q3_TYPE_F32); }), "4-bit append")))
+                return rc;
+        } else if (!r.decode && !roped &&
             (rc = m->check(run(Q3_K_ROPE, [&] { return launch_qk_norm_rope_append(L, ra); }),
                            "qk-norm/rope/append")))
             return rc;
 
         // ---- attention
-        if (r.decode) {
+        if (m->kv4 && r.decode) {
+            Kv4DecodeArgs da{};
+            da.q = m->q16; da.q_stride = m->qw;
+            da.row_pos = row_pos; da.row_slot = row_slot;
+            da.T = T; da.n_q = c.n_q_heads; da.n_kv = c.n_kv_heads;
+            da.tables = r.pool->tables; da.n_slots = r.pool->max_sessions; da.max_blocks = r.pool->max_blocks;
+            da.max_ctx = r.max_ctx;
+            da.kv = reinterpret_cast<uint8_t*>(r.pool->kv) + (size_t)l * layer_bytes; da.n_blocks = r.pool->n_blocks;
+            da.out = one ? (void*)m->attf : (void*)m->att;
+            da.status = m->status;
+            if ((rc = m->check(run(Q3_K_ATTN, [&] {
+                     return launch_kv4_decode(L, da, Q3_TYPE_F16, one ? Q3_TYPE_F32 : Q3_TYPE_F16);
+                 }), "4-bit attention")))
+                return rc;
+        } else if (m->kv4) {
+            Kv4PrefillArgs pa{};
+            pa.q = m->q16; pa.q_stride = m->qw;
+            pa.seq_rows = m->meta + 3 * m->max_rows; pa.seq_pos = m->meta + 4 * m->max_rows;
+            pa.seq_slot = m->meta + 6 * m->max_rows;
+            pa.ns = r.ns; pa.T = T; pa.n_q = c.n_q_heads; pa.n_kv = c.n_kv_heads;
+            pa.tables = r.pool->tables; pa.n_slots = r.pool->max_sessions; pa.max_blocks = r.pool->max_blocks;
+            pa.kv = reinterpret_cast<uint8_t*>(r.pool->kv) + (size_t)l * layer_bytes; pa.n_blocks = r.pool->n_blocks;
+            pa.out = m->att; pa.status = m->status;
+            if ((rc = m->check(run(Q3_K_ATTN, [&] { return run_kv4_prefill(L, pa, r.pool->kv4_ws, m->n_sm); }), "4-bit prefill attention")))
+                return rc;
+        } else if (r.decode) {
             AttnArgs aa{};
             aa.q = m->q; aa.qkv = m->qkv;
             aa.qkv_ws = m->ws; aa.qkv_splits = one ? 0 : qkv_splits;
@@ -963,20 +1089,28 @@ int run_round(q3_model* m, const Round& r)
     // ---- final norm + lm_head (+ argmax): the last row of each session, or
     // the last n_out rows of a one-session round
     const int n_out = r.ns == 1 ? r.n_out : r.ns;
-    if (n_out == 1) {
-        const void* w[1] = {m->lm_head};
-        const int rows[1] = {c.vocab};
-        if ((rc = gemv(m, 1, w, nullptr, rows, 0, H, m->x + (size_t)r.last_row * H, m->final_norm,
-                       EPI_STORE_F32, r.logits, r.argmax)))
-            return rc;
-    } else {
-        if ((rc = m->check(run(Q3_K_NORM, [&] { return launch_rmsnorm_f16(L, m->x, last_rows, n_out, H, m->final_norm, c.rms_eps,
-                                              m->hfin, m->status); }), "final norm")))
-            return rc;
-        if ((rc = gemm(m, &m->lm_map, nullptr, nullptr, c.vocab / 128, c.vocab / 128, 0, c.vocab, n_out, H,
-                       m->hfin, EPI_STORE_F32, r.logits, c.vocab)))
-            return rc;
+    // logits of the n rows listed from `first` on
+    auto logit_rows = [&](int first, int n, float* logits, int32_t* argmax) -> int {
+        if (n == 1) {
+            const void* w[1] = {m->lm_head};
+            const int rows[1] = {c.vocab};
+            return gemv(m, 1, w, nullptr, rows, 0, H, m->x + (size_t)(r.last_row - n_out + 1 + first) * H, m->final_norm, EPI_STORE_F32,
+                        logits, argmax);
+        }
+        int e = m->check(run(Q3_K_NORM, [&] { return launch_rmsnorm_f16(L, m->x, last_rows + first, n, H, m->final_norm, c.rms_eps,
+                                                                        m->hfin, m->status); }), "final norm");
+        return e ? e : gemm(m, &m->lm_map, nullptr, nullptr, c.vocab / 128, c.vocab / 128, 0, c.vocab, n, H, m->hfin,
+                            EPI_STORE_F32, logits, c.vocab);
+    };
+    if (r.score) {
+        for (int i = 0; i < n_out; i += SCORE_ROWS) {
+            const int n = std::min(SCORE_ROWS, n_out - i);
+            if ((rc = logit_rows(i, n, m->score_logits, nullptr))) return rc;
+            if ((rc = score_rows(m, r, i, n))) return rc;
+        }
+        return Q3_OK;
     }
+    if ((rc = logit_rows(0, n_out, r.logits, n_out == 1 ? r.argmax : nullptr))) return rc;
     if (n_out > 1 && r.argmax &&
         (rc = m->check(run(Q3_K_OTHER, [&] { return launch_argmax(L, r.logits, n_out, c.vocab, r.argmax); }), "argmax")))
         return rc;
@@ -1035,7 +1169,7 @@ int upload_table(q3_session* s)
 }
 
 int eval_round(q3_session* const* S, int ns, const int32_t* tokens, const int* n, float* logits,
-               int32_t* argmax, int n_out = 1)
+               int32_t* argmax, int n_out = 1, const Score* score = nullptr)
 {
     q3_pool* pool = S[0]->pool;
     q3_model* m = pool->m;
@@ -1047,6 +1181,7 @@ int eval_round(q3_session* const* S, int ns, const int32_t* tokens, const int* n
     r.logits = logits;
     r.argmax = argmax;
     r.n_out = n_out;
+    r.score = score;
     if (n_out < 1 || (ns > 1 && n_out != 1) || (ns == 1 && n_out > n[0]))
         return fail(Q3_ERR_INVALID_ARG, "logit rows %d outside [1, round rows]", n_out);
     for (int i = 0; i < ns; ++i) {
@@ -1093,8 +1228,23 @@ int eval_round(q3_session* const* S, int ns, const int32_t* tokens, const int* n
     // longest-processing-time-first assignment (an item is one tile for one
     // KV head; its cost is the number of 128-position K/V tiles it walks).
     size_t meta_ints = 6 * (size_t)m->max_rows;
-    r.attn_tc = m->prefill_tc && m->prefill_tc_ok;
-    {
+    if (m->kv4) {
+        // the 4-bit cache lists its tiles on the device from the sessions' rows,
+        // positions and slots (a round with more rows than sessions has room)
+        if (r.T > ns) {
+            int row = 0;
+            for (int i = 0; i < ns; ++i) {
+                h[3 * m->max_rows + i] = row;
+                h[4 * m->max_rows + i] = S[i]->pos;
+                h[6 * m->max_rows + i] = S[i]->slot;
+                row += n[i];
+            }
+            h[3 * m->max_rows + ns] = row;
+            meta_ints += ns;
+        }
+    }
+    r.attn_tc = !m->kv4 && m->prefill_tc && m->prefill_tc_ok;
+    if (!m->kv4) {
         const int R = r.attn_tc ? prefill_tc_rows(m->c.n_q_heads, m->c.n_kv_heads) : 64;
         struct Tile { int row0, rows, last_pos; };
         std::vector<Tile> tiles;
@@ -1188,6 +1338,7 @@ void pool_release(q3_pool* p)
     cudaStreamSynchronize(p->m->stream);
     cudaFree(p->kv);
     cudaFree(p->tables);
+    cudaFree(p->kv4_ws);
 #ifdef Q3_TEST_FAULTS
     cudaFree(p->fault_tables);
 #endif
@@ -1222,6 +1373,7 @@ int q3_model_set_prefill_tc(q3_model* m, int on)
 {
     if (!m) return fail(Q3_ERR_INVALID_ARG, "model is NULL");
     if (on && !m->prefill_tc_ok) return fail(Q3_ERR_INVALID_ARG, "tcgen05 prefill attention unsupported here");
+    if (!on && m->kv4) return fail(Q3_ERR_INVALID_ARG, "the 4-bit cache has no mma.sync prefill attention");
     m->prefill_tc = on != 0;
     return Q3_OK;
 }
@@ -1264,10 +1416,15 @@ int q3_model_create(const q3_config* cfg, const q3_weights* w, int max_round_tok
     m->pdl = true;
     m->n_sm = std::min(prop.multiProcessorCount, SCHED_GRID);
     m->kv_q8 = c.kv_scheme == Q3_Q8_0;
-    // the tcgen05 prefill attention reads the BF16 cache through a tensor map;
-    // the Q8_0 cache takes the mma.sync kernel
+    m->kv4 = c.kv_scheme == Q3_AFFINE4;
+    // the tcgen05 prefill attention reads the BF16 cache, or the fp16 copy of the
+    // 4-bit cache, through a tensor map; the Q8_0 cache takes the mma.sync kernel
     m->prefill_tc_ok = !m->kv_q8 && prefill_tc_rows(c.n_q_heads, c.n_kv_heads) > 0 &&
                        prefill_tc_smem() <= (size_t)prop.sharedMemPerBlockOptin;
+    if (m->kv4 && !m->prefill_tc_ok) {
+        delete m;
+        return fail(Q3_ERR_INVALID_ARG, "config: the 4-bit cache needs the tcgen05 prefill attention");
+    }
 
     auto bad = [&](int code, const char* msg) {
         free_model(m);
@@ -1503,7 +1660,7 @@ int q3_pool_create(q3_model* m, int n_blocks, int max_sessions, q3_pool** out)
         delete p;
         return fail(Q3_ERR_OOM, "pool: cannot allocate %zu bytes of KV", kv_bytes);
     }
-    if (!m->kv_q8 && !tmap_kv(&p->kv_map, p->kv, kv_bytes / 256)) {
+    if (!m->kv_q8 && !m->kv4 && !tmap_kv(&p->kv_map, p->kv, kv_bytes / 256)) {
         cudaFree(p->kv);
         delete p;
         return fail(Q3_ERR_CUDA, "pool: tensor map encoding failed");
@@ -1527,6 +1684,16 @@ int q3_pool_create(q3_model* m, int n_blocks, int max_sessions, q3_pool** out)
         delete p;
         return fail(Q3_ERR_CUDA, "pool: memset failed");
     }
+    if (m->kv4) {
+        const size_t wb = kv4_workspace(std::min(max_sessions, m->max_rows), m->max_rows, m->c.n_q_heads, m->c.n_kv_heads,
+                                        p->max_blocks, n_blocks).bytes;
+        if (cudaMalloc(&p->kv4_ws, wb) != cudaSuccess) {
+            cudaFree(p->kv);
+            cudaFree(p->tables);
+            delete p;
+            return fail(Q3_ERR_OOM, "pool: cannot allocate %zu bytes of prefill workspace", wb);
+        }
+    }
 #ifdef Q3_TEST_FAULTS
     if (m->fault == 1 || m->fault == 3 || m->fault == 4) {
         const size_t tb = sizeof(int) * (size_t)max_sessions * p->max_blocks;
@@ -1535,6 +1702,7 @@ int q3_pool_create(q3_model* m, int n_blocks, int max_sessions, q3_pool** out)
             cudaFree(p->fault_tables);
             cudaFree(p->kv);
             cudaFree(p->tables);
+            cudaFree(p->kv4_ws);
             delete p;
             return fail(Q3_ERR_OOM, "pool: fault tables");
         }
@@ -1644,6 +1812,46 @@ int q3_session_eval_n(q3_session* s, const int32_t* tokens_dev, int n, int n_log
                             argmax_dev ? argmax_dev + (lo - first) : nullptr, rows);
         else
             rc = eval_round(&s, 1, tokens_dev + off, &k, logits_dev, nullptr, 1);   // overwritten later
+        if (rc) return rc;
+    }
+    return Q3_OK;
+}
+
+int q3_session_score(q3_session* s, const int32_t* tokens_dev, int n, int n_score, const int32_t* targets_dev, int top_k,
+                     float* logprob_dev, float* entropy_dev, int32_t* top_ids_dev, float* top_logprob_dev)
+{
+    if (!s || !tokens_dev || n < 1 || n_score < 1 || n_score > n || (logprob_dev && !targets_dev))
+        return fail(Q3_ERR_INVALID_ARG, "score: bad argument");
+    q3_model* m = s->pool->m;
+    if (top_k < 0 || top_k > m->c.vocab || top_k > Q3_LOGPROB_MAX_TOP)
+        return fail(Q3_ERR_INVALID_ARG, "score: top_k outside [0, %d]", Q3_LOGPROB_MAX_TOP);
+    if (s->pos + n > m->c.max_ctx)
+        return fail(Q3_ERR_CTX_OVERFLOW, "position %d + %d exceeds max_ctx %d", s->pos, n, m->c.max_ctx);
+    if (m->poisoned) return fail(Q3_ERR_POISONED, "model poisoned by an earlier error");
+    if (!m->score_logits) {
+        const size_t rows = std::min(SCORE_ROWS, m->max_rows);
+        m->score_logits = static_cast<float*>(m->dalloc(sizeof(float) * rows * m->c.vocab));
+        if (!m->score_logits) {
+            cudaGetLastError();
+            return fail(Q3_ERR_OOM, "score: cannot allocate the logits of %zu rows", rows);
+        }
+    }
+    const int first = n - n_score;
+    for (int off = 0; off < n; off += m->max_rows) {
+        const int k = std::min(m->max_rows, n - off);
+        const int lo = std::max(off, first);
+        const int rows = off + k - lo;                          // this round's scored rows (a suffix)
+        int rc;
+        if (rows >= 1) {
+            const size_t at = lo - first;
+            const Score sc{targets_dev ? targets_dev + at : nullptr, top_ids_dev || top_logprob_dev ? top_k : 0,
+                           logprob_dev ? logprob_dev + at : nullptr, entropy_dev ? entropy_dev + at : nullptr,
+                           top_ids_dev ? top_ids_dev + at * top_k : nullptr,
+                           top_logprob_dev ? top_logprob_dev + at * top_k : nullptr};
+            rc = eval_round(&s, 1, tokens_dev + off, &k, m->score_logits, nullptr, rows, &sc);
+        } else {
+            rc = eval_round(&s, 1, tokens_dev + off, &k, m->score_logits, nullptr, 1);   // overwritten later
+        }
         if (rc) return rc;
     }
     return Q3_OK;
@@ -2124,50 +2332,6 @@ bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int
 {
     return T >= 0 && n_kv >= 1 && n_kv <= 4096 && n_q >= 1 && n_q <= 8 * n_kv && n_q % n_kv == 0 && tables && n_slots >= 1 &&
            max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) && n_blocks >= 1;
-}
-
-// The prefill attention's workspace: a tile count and a spare status word, the
-// tile list, the fp16 copy of the blocks (numbered as in the pool, or by
-// sequence where that is fewer).
-struct Kv4Workspace {
-    size_t tiles, copy, bytes;
-    int64_t blocks;
-    bool by_seq;
-};
-Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks)
-{
-    Kv4Workspace w;
-    w.by_seq = (int64_t)ns * max_blocks < n_blocks;
-    w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
-    w.tiles = 256;
-    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
-    w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
-    return w;
-}
-
-// expansion, then attention over the copy, on the workspace at ws
-cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int n_sm)
-{
-    const Kv4Workspace w = kv4_workspace(a.ns, a.T, a.n_q, a.n_kv, a.max_blocks, a.n_blocks);
-    int* head = reinterpret_cast<int*>(ws);
-    a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
-    a.n_tiles = head;
-    a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
-    a.copy = reinterpret_cast<f16*>(ws + w.copy);
-    a.by_seq = w.by_seq;
-    CUtensorMap map;
-    if (!tmap_kv16(&map, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32)) return cudaErrorInvalidValue;
-    if (cudaError_t e = launch_kv4_expand(L, a)) return e;
-    PrefillAttnArgs p{};
-    p.q = a.q; p.q_stride = a.q_stride;
-    p.T = a.T; p.n_q = a.n_q; p.n_kv = a.n_kv;
-    p.tables = a.tables; p.max_blocks = a.max_blocks; p.n_blocks = a.n_blocks;
-    p.seq_slot = a.seq_slot; p.by_seq = a.by_seq;
-    p.tiles = a.tiles; p.n_tiles_dev = a.n_tiles;
-    p.out = a.out;
-    p.status = a.status ? a.status : head + 1;       // a spare word nobody reads
-    const Launch after{L.stream, true, L.counter};   // its setup overlaps the expansion
-    return launch_prefill_attention_kv4(after, map, p, n_sm);
 }
 
 bool row_stride_ok(int64_t stride, int type, int64_t width)

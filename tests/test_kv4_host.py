@@ -121,3 +121,40 @@ def test_binding_refuses_before_the_library():
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was taken")
+
+
+def test_prefill_workspace_is_planned_on_the_host(L):
+    import qwen3_dense_decoder_gb300 as q3
+    copy = 8 * 16384                                    # one block of eight KV heads in fp16, K and V
+    # the pool's blocks, or the sequences' tables where those are fewer
+    assert q3.kv4_prefill_workspace(1, 2048, 32, 8, 64, 40) - 40 * copy < 1 << 16
+    assert q3.kv4_prefill_workspace(2, 100, 32, 8, 4, 100000) - 8 * copy < 1 << 16
+    sizes = [q3.kv4_prefill_workspace(n, 300, 32, 8, 16, 64) for n in (0, 1, 2, 4, 5, 9)]
+    assert sizes == sorted(sizes)
+    for bad in ((-1, 1, 32, 8, 4, 4), (1, -1, 32, 8, 4, 4), (1, 1, 31, 8, 4, 4), (1, 1, 72, 8, 4, 4), (1, 1, 32, 0, 4, 4), (1, 1, 32, 8, 0, 4),
+                (1, 1, 32, 8, 4, 0)):
+        with pytest.raises(q3.Q3Error):
+            q3.kv4_prefill_workspace(*bad)
+    assert _prefill(L, ws=None) == -1 and _prefill(L, ws=P + 16) == -1 and _prefill(L, ws_bytes=2 * copy) == -1
+
+
+def test_score_refuses_without_a_session(L):
+    assert L.q3_session_score(None, None, 1, 1, None, 0, None, None, None, None) == -1
+
+
+def test_oracle_cache_scheme(orc):
+    """The oracle's 4-bit cache: its size, and a forward near the BF16 one without equalling it."""
+    import numpy as np
+    import synthetic
+    s = synthetic.SHAPES["4b"]
+    assert orc.kv_bytes_per_position(s.replace(kv_quant=synthetic.AFFINE4)) == 2 * 8 * 80
+    small = synthetic.Shape("kv4-small", 2, 128, 4, 2, 32, 128, 256, True)
+    w = synthetic.make_weights(small, seed=3)
+    toks = synthetic.make_tokens(40, small.vocab, seed=4)
+    bf, q4 = (orc.Model(small.replace(kv_quant=k), w, n_threads=2).session(max_ctx=64).eval(toks, all_rows=True)
+              for k in (synthetic.BF16, synthetic.AFFINE4))
+    e = float(((q4 - bf) ** 2).sum() / (bf ** 2).sum())
+    assert 0 < e < 0.05, e
+    assert np.isfinite(q4).all()
+    with pytest.raises(ValueError):                     # whole groups of 32 values a head row
+        orc.Model(small.replace(head_dim=16, kv_quant=synthetic.AFFINE4), w, n_threads=1)

@@ -125,25 +125,26 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 // Both products run on mma.sync m16n8k16 with the cache as the A operand, so
 // its 4-bit words become fragments in registers (kv4_pair; 1.6 instructions a
 // value) and never pass through shared memory again:
-//   S^T = K Q^T   rows positions, columns (head, part): column 2h is the fp16
-//                 high part of q_h, column 2h + 1 the remainder, so an FP32 q
-//                 keeps 22 bits and c0 + c1 is the score of one head in one
-//                 lane.  The order of the 16 dimensions of a step is free, so a
-//                 lane takes its own group's 32 dimensions in the order of their
-//                 nibbles.
+//   S^T = K Q^T   rows positions, columns heads.  The order of the 16
+//                 dimensions of a step is free, so a lane takes its own group's
+//                 32 dimensions in the order of their nibbles.
 //   O^T += V^T P^T  rows dimensions (a lane's word pairs two positions), columns
-//                 (head, part) again: {high, low} of a weight lie side by side in
-//                 the score fragment and one 8 x 8 transpose makes them the B
-//                 fragment.
-// Softmax is online in base 2; O is rescaled only in blocks that raise a
-// maximum.  Four heads fill the eight columns; groups of five to eight take
-// two column tiles over the same fragments of K and V.
+//                 heads; the weights turn from the score fragment's layout into
+//                 B fragments by 8 x 8 transposes.
+// q and the weights enter as fp16 high and low parts (22 bits).  Up to four
+// heads the two parts are columns 2h and 2h + 1 of one tile (c0 + c1 is the
+// result of one head in one lane); from five on the columns are eight heads and
+// the parts two products into the same accumulators.  An fp16 q has no low
+// part, so the wide form leaves its product out.
+// Softmax is online in base 2; O and the sums are rescaled only when a maximum
+// grows by more than 2^8 (the weights then reach 2^8, far inside fp16).
 //
 // Splits of a (row, KV head) are one cluster; warps merge in order through
 // shared memory, CTAs in order through distributed shared memory.
 constexpr int AW = 4;
-constexpr int KV4_STAGES = 2;
+constexpr int STAGES = 2;
 constexpr int KV4_STAGE = 2 * KV4_TILE;
+constexpr float LAZY = 8.0f;
 
 Q3_DEV float fast_ex2(float x) {
     float y;
@@ -151,10 +152,10 @@ Q3_DEV float fast_ex2(float x) {
     return y;
 }
 Q3_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 Q3_DEV uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -164,7 +165,7 @@ Q3_DEV uint32_t transpose8x8(uint32_t v) {
 Q3_DEV __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 Q3_DEV uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
-// wait_bar, bounded, with an optional status word
+// mbar_wait with an optional status word
 Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
@@ -179,9 +180,9 @@ Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
 }
 
 // 32 values [32 tig, 32 tig + 32) of a head's q as the B fragments of one
-// column: registers 2 s, 2 s + 1 of step s; part 0 the high halves, 1 the rest
+// column: registers 2 s, 2 s + 1 of step s; the high halves, or the rest
 template <typename Tq>
-Q3_DEV void load_q(const Tq* q, int part, uint32_t (&b)[16], bool& bad) {
+Q3_DEV void load_q(const Tq* q, bool low, uint32_t (&b)[16], bool& bad) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float f[8];
@@ -191,27 +192,31 @@ Q3_DEV void load_q(const Tq* q, int part, uint32_t (&b)[16], bool& bad) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             h[e] = to_f16(f[e], bad);
-            if (part) h[e] = __float2half_rn(f[e] - __half2float(h[e]));
+            if (low) h[e] = __float2half_rn(f[e] - __half2float(h[e]));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[4 * j + i] = as_u32(__halves2half2(h[i], h[i + 4]));
     }
 }
 
-template <int NT>
+// WIDE: a lane's score columns are heads 2 tig and 2 tig + 1; else head tig.
+template <bool WIDE>
 struct Attend {
-    float m[NT], l[NT];        // running maximum and this lane's part of the sum, head tig of each column tile
-    float o[NT][8][4];         // O^T: row tile 2 g + h holds dimensions 32 g + 4 (lane / 4) + 2 h, + 1
+    static constexpr int NH = WIDE ? 2 : 1;
+    float m[NH], l[NH];        // running maximum and this lane's part of the sum
+    float o[8][4];             // O^T: row tile 2 g + h holds dimensions 32 g + 4 (lane / 4) + 2 h, + 1
 };
 
 // One block: kt, vt its K and V tiles in shared memory, n_pos its positions
-// in use.
-template <int NT>
-Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&q)[NT][16], int n_pos, int lane, Attend<NT>& w)
+// in use (TAIL: fewer than 32).  QP parts of q.
+template <bool WIDE, int QP, bool TAIL>
+Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&q)[QP][16], int n_pos, uint32_t magic, int lane,
+                         Attend<WIDE>& w)
 {
+    constexpr int NH = Attend<WIDE>::NH;
     const int g = lane >> 2, tig = lane & 3;
     const float scale = 1.4426950408889634f * 0.08838834764831845f;    // log2(e) / sqrt(128)
-    float s[NT][4];
+    float s[NH][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
         const int p = 16 * mt + g;
@@ -221,47 +226,75 @@ Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&
         const __half2 sb = *reinterpret_cast<const __half2*>(kt + KV4_CODES + (p + 8) * 16 + tig * 4);
         const __half2 sca = __low2half2(sa), bia = __high2half2(sa), scb = __low2half2(sb), bib = __high2half2(sb);
         const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        float c[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t a0[4] = {kv4_pair<0>(wa[j], sca, bia), kv4_pair<0>(wb[j], scb, bib),
-                                    kv4_pair<1>(wa[j], sca, bia), kv4_pair<1>(wb[j], scb, bib)};
+            const uint32_t a0[4] = {kv4_pair<0>(wa[j], sca, bia, magic), kv4_pair<0>(wb[j], scb, bib, magic),
+                                    kv4_pair<1>(wa[j], sca, bia, magic), kv4_pair<1>(wb[j], scb, bib, magic)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], a0, q[nt][4 * j], q[nt][4 * j + 1]);
-            const uint32_t a1[4] = {kv4_pair<2>(wa[j], sca, bia), kv4_pair<2>(wb[j], scb, bib),
-                                    kv4_pair<3>(wa[j], sca, bia), kv4_pair<3>(wb[j], scb, bib)};
+            for (int i = 0; i < QP; ++i) mma_f16(c, a0, q[i][4 * j], q[i][4 * j + 1]);
+            const uint32_t a1[4] = {kv4_pair<2>(wa[j], sca, bia, magic), kv4_pair<2>(wb[j], scb, bib, magic),
+                                    kv4_pair<3>(wa[j], sca, bia, magic), kv4_pair<3>(wb[j], scb, bib, magic)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(c[nt], a1, q[nt][4 * j + 2], q[nt][4 * j + 3]);
+            for (int i = 0; i < QP; ++i) mma_f16(c, a1, q[i][4 * j + 2], q[i][4 * j + 3]);
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            s[nt][2 * mt] = p < n_pos ? (c[nt][0] + c[nt][1]) * scale : -INFINITY;
-            s[nt][2 * mt + 1] = p + 8 < n_pos ? (c[nt][2] + c[nt][3]) * scale : -INFINITY;
+        if (WIDE) {
+            s[0][2 * mt] = c[0] * scale; s[NH - 1][2 * mt] = c[1] * scale;
+            s[0][2 * mt + 1] = c[2] * scale; s[NH - 1][2 * mt + 1] = c[3] * scale;
+        } else {
+            s[0][2 * mt] = (c[0] + c[1]) * scale;
+            s[0][2 * mt + 1] = (c[2] + c[3]) * scale;
         }
     }
-    uint32_t pt[NT][4];        // the weights' B fragments: 8 positions each
+    if (TAIL) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float mx = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
+        for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (__any_sync(0xffffffffu, mx > w.m[nt])) {
-            const float mn = fmaxf(w.m[nt], mx), alpha = fast_ex2(w.m[nt] - mn);     // 0 at first
-            w.m[nt] = mn;
-            w.l[nt] *= alpha;
+            for (int i = 0; i < 4; ++i)
+                if (8 * i + g >= n_pos) s[h][i] = -INFINITY;
+    }
+    float mx[NH];
+    bool grow = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+    for (int h = 0; h < NH; ++h) {
+        mx[h] = fmaxf(fmaxf(s[h][0], s[h][1]), fmaxf(s[h][2], s[h][3]));
+        grow = grow || mx[h] > w.m[h] + LAZY;
+    }
+    if (__any_sync(0xffffffffu, grow)) {                 // every lane of a head takes the head's maximum
+        float alpha[NH];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w.o[nt][i][e] *= alpha;
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
+            const float mn = fmaxf(w.m[h], mx[h]);
+            alpha[h] = fast_ex2(w.m[h] - mn);            // 0 at first
+            w.m[h] = mn;
+            w.l[h] *= alpha[h];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float e = fast_ex2(s[nt][i] - w.m[nt]);
-            w.l[nt] += e;
-            const __half hi = __float2half_rn(e);
-            pt[nt][i] = transpose8x8(as_u32(__halves2half2(hi, __float2half_rn(e - __half2float(hi)))));
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w.o[i][e] *= alpha[WIDE ? (e & (NH - 1)) : 0];
+    }
+    // the weights' B fragments, 8 positions each: (high, low) of one head side
+    // by side, or the high and the low parts of two heads
+    uint32_t pt[NH][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float e[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            e[h] = fast_ex2(s[h][i] - w.m[h]);
+            w.l[h] += e[h];
+        }
+        if (WIDE) {
+            const __half2 hi = __floats2half2_rn(e[0], e[NH - 1]);
+            const float2 f = __half22float2(hi);
+            pt[0][i] = transpose8x8(as_u32(hi));
+            pt[NH - 1][i] = transpose8x8(as_u32(__floats2half2_rn(e[0] - f.x, e[NH - 1] - f.y)));
+        } else {
+            const __half hi = __float2half_rn(e[0]);
+            pt[0][i] = transpose8x8(as_u32(__halves2half2(hi, __float2half_rn(e[0] - __half2float(hi)))));
         }
     }
 #pragma unroll
@@ -274,7 +307,7 @@ Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&
         const uint4 a01 = para[0], a23 = para[1], b01 = parb[0], b23 = parb[1];
         uint32_t sba[8] = {a01.x, a01.y, a01.z, a01.w, a23.x, a23.y, a23.z, a23.w};
         uint32_t sbb[8] = {b01.x, b01.y, b01.z, b01.w, b23.x, b23.y, b23.z, b23.w};
-        if (n_pos < 32) {      // positions past the end count as zeros, whatever is there
+        if (TAIL) {            // positions past the end count as zeros, whatever is there
             const uint32_t ma = (2 * pa < n_pos ? 0xffffu : 0u) | (2 * pa + 1 < n_pos ? 0xffff0000u : 0u);
             const uint32_t mb = (2 * pb < n_pos ? 0xffffu : 0u) | (2 * pb + 1 < n_pos ? 0xffff0000u : 0u);
 #pragma unroll
@@ -285,31 +318,37 @@ Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&
         for (int gr = 0; gr < 4; ++gr) {
             const __half2 sca = as_h2(sba[2 * gr]), bia = as_h2(sba[2 * gr + 1]);
             const __half2 scb = as_h2(sbb[2 * gr]), bib = as_h2(sbb[2 * gr + 1]);
-            const uint32_t a0[4] = {kv4_pair<0>(wa[gr], sca, bia), kv4_pair<1>(wa[gr], sca, bia),
-                                    kv4_pair<0>(wb[gr], scb, bib), kv4_pair<1>(wb[gr], scb, bib)};
+            const uint32_t a0[4] = {kv4_pair<0>(wa[gr], sca, bia, magic), kv4_pair<1>(wa[gr], sca, bia, magic),
+                                    kv4_pair<0>(wb[gr], scb, bib, magic), kv4_pair<1>(wb[gr], scb, bib, magic)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[nt][2 * gr], a0, pt[nt][2 * j], pt[nt][2 * j + 1]);
-            const uint32_t a1[4] = {kv4_pair<2>(wa[gr], sca, bia), kv4_pair<3>(wa[gr], sca, bia),
-                                    kv4_pair<2>(wb[gr], scb, bib), kv4_pair<3>(wb[gr], scb, bib)};
+            for (int h = 0; h < NH; ++h) mma_f16(w.o[2 * gr], a0, pt[h][2 * j], pt[h][2 * j + 1]);
+            const uint32_t a1[4] = {kv4_pair<2>(wa[gr], sca, bia, magic), kv4_pair<3>(wa[gr], sca, bia, magic),
+                                    kv4_pair<2>(wb[gr], scb, bib, magic), kv4_pair<3>(wb[gr], scb, bib, magic)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[nt][2 * gr + 1], a1, pt[nt][2 * j], pt[nt][2 * j + 1]);
+            for (int h = 0; h < NH; ++h) mma_f16(w.o[2 * gr + 1], a1, pt[h][2 * j], pt[h][2 * j + 1]);
         }
     }
 }
 
+constexpr int MAX_SPLITS = 16;
 struct DecodeShared {
     union {
-        uint8_t ring[AW][KV4_STAGES][KV4_STAGE];
-        float o[AW][8][D];                 // per warp, then [0] the CTA's
+        uint8_t ring[AW][STAGES][KV4_STAGE];
+        float o[AW][8][D];                 // per warp
     };
-    uint64_t full[AW][KV4_STAGES];
-    float m[AW][8], l[AW][8];              // per warp, then [0] the CTA's
+    uint64_t full[AW][STAGES];
+    float m[AW][8], l[AW][8];              // per warp
+    // what the cluster's CTAs leave here of the heads this one finishes: CTA c's
+    // part of its n-th head in row n C + c; ceil(8 / C) C rows at most
+    float in_o[MAX_SPLITS][D], in_m[MAX_SPLITS], in_l[MAX_SPLITS];
 };
-static_assert(sizeof(float) * AW * 8 * D <= (size_t)AW * KV4_STAGES * KV4_STAGE, "merge area");
+static_assert(sizeof(float) * 8 * D <= (size_t)STAGES * KV4_STAGE, "merge area");
 
-template <int NT, typename Tq, typename To>
-__global__ void __launch_bounds__(AW * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(const Kv4DecodeArgs a, int C)
+template <bool WIDE, typename Tq>
+__global__ void __launch_bounds__(AW * 32, 4) kv4_decode_kernel(const Kv4DecodeArgs a, int C)
 {
+    constexpr int NH = Attend<WIDE>::NH;
+    constexpr int QP = WIDE && sizeof(Tq) == 4 ? 2 : 1;      // narrow: the parts are columns
     extern __shared__ __align__(128) uint8_t smem_raw[];
     DecodeShared& sm = *reinterpret_cast<DecodeShared*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,9 +356,10 @@ __global__ void __launch_bounds__(AW * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(co
     const int rank = blockIdx.x % C, unit = blockIdx.x / C;
     const int kvh = unit % a.n_kv, t = unit / a.n_kv;
     const int G = a.n_q / a.n_kv;
-    if (lane < KV4_STAGES) mbar_init(&sm.full[warp][lane], 1);
+    if (lane < STAGES) mbar_init(&sm.full[warp][lane], 1);
     fence_barrier_init();
     __syncwarp();
+    if (C > 1) cg::this_cluster().barrier_arrive();
     grid_dep_wait();
 
     const int slot = a.row_slot[t];
@@ -335,99 +375,103 @@ __global__ void __launch_bounds__(AW * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(co
 
     // block b's tiles into stage st; false: its table entry is outside the pool
     auto issue = [&](int phys, int st) -> bool {
-        if (phys < 0 || phys >= a.n_blocks) {
-            if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-            return false;
-        }
-        if (lane == 0) {
+        const bool in_pool = (unsigned)phys < (unsigned)a.n_blocks;
+        if (lane == 0 && !in_pool) {
+            report(a.status, Q3_STATUS_BLOCK_RANGE);
+            mbar_arrive(&sm.full[warp][st]);
+        } else if (lane == 0) {
             const uint8_t* src = kv + (size_t)phys * 2 * a.n_kv * KV4_TILE;
             uint8_t* dst = sm.ring[warp][st];
             mbar_arrive_expect_tx(&sm.full[warp][st], KV4_STAGE);
             bulk_load(dst, src, KV4_TILE, &sm.full[warp][st]);
             bulk_load(dst + KV4_TILE, src + (size_t)a.n_kv * KV4_TILE, KV4_TILE, &sm.full[warp][st]);
         }
-        return true;
+        return in_pool;
     };
-    uint32_t live = 0, phase = 0;          // per stage: a copy is on its way, the parity that ends it
+    // the blocks of this warp, first, first + AW, ...: block n's tiles pass
+    // through stage n % STAGES; one outside the pool leaves its stage as it
+    // is and only ends the stage's phase
     const int first = rank * per + warp;
+    uint32_t held = 0;                     // bit st: stage st's block is in the pool
 #pragma unroll
-    for (int st = 0; st < KV4_STAGES; ++st) {
+    for (int st = 0; st < STAGES; ++st) {
         const int b = first + st * AW;
-        if (b < b1 && issue(table[b], st)) live |= 1u << st;
+        if (b < b1 && issue(table[b], st)) held |= 1u << st;
     }
 
-    uint32_t q[NT][16];
+    uint32_t q[QP][16];
     bool bad = false;
-    const Tq* qrow = static_cast<const Tq*>(a.q) + (size_t)t * a.q_stride + (size_t)kvh * G * D;
+    const Tq* qrow = static_cast<const Tq*>(a.q) + (size_t)t * a.q_stride + (size_t)kvh * G * D + 32 * tig;
+    const int qh = WIDE ? g : g >> 1;                        // the head of this lane's column
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 4 * nt + (g >> 1);
-        if (h < G) {
-            load_q(qrow + (size_t)h * D + 32 * tig, g & 1, q[nt], bad);
+    for (int i = 0; i < QP; ++i) {
+        if (qh < G) {
+            load_q(qrow + (size_t)qh * D, WIDE ? i == 1 : (g & 1) != 0, q[i], bad);
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) q[nt][i] = 0u;
+            for (int e = 0; e < 16; ++e) q[i][e] = 0u;
         }
     }
     if (bad) report(a.status, Q3_STATUS_F16_RANGE);
 
-    Attend<NT> w;
+    Attend<WIDE> w;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        w.m[nt] = -INFINITY;
-        w.l[nt] = 0.f;
+    for (int h = 0; h < NH; ++h) { w.m[h] = -INFINITY; w.l[h] = 0.f; }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w.o[nt][i][0] = w.o[nt][i][1] = w.o[nt][i][2] = w.o[nt][i][3] = 0.f;
-    }
+    for (int i = 0; i < 8; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.f;
 
-    int st = 0;
     bool ok = true;
-    for (int b = first; b < b1 && ok; b += AW) {
-        const int bn = b + KV4_STAGES * AW;
+    uint32_t parity = 0;
+    int b = first;
+    for (int st = 0; b < b1; b += AW) {
+        const int bn = b + STAGES * AW;
         const int phys = bn < b1 ? table[bn] : 0;        // ahead of its use below
-        if (live >> st & 1) {
-            ok = wait_bar(&sm.full[warp][st], phase >> st & 1, a.status);
-            phase ^= 1u << st;
-            live &= ~(1u << st);
-            if (ok)
-                attend_block<NT>(sm.ring[warp][st], sm.ring[warp][st] + KV4_TILE, q, min(32, ctx - 32 * b), lane, w);
+        ok = wait_bar(&sm.full[warp][st], parity, a.status);
+        if (!ok) break;
+        if (held >> st & 1) {
+            const uint8_t* kt = sm.ring[warp][st];
+            const int n_pos = ctx - 32 * b;
+            if (n_pos >= 32) attend_block<WIDE, QP, false>(kt, kt + KV4_TILE, q, 32, a.magic, lane, w);
+            else attend_block<WIDE, QP, true>(kt, kt + KV4_TILE, q, n_pos, a.magic, lane, w);
         }
         __syncwarp();                                    // every lane is done with the stage
-        if (ok && bn < b1 && issue(phys, st)) live |= 1u << st;
-        st = st + 1 == KV4_STAGES ? 0 : st + 1;
+        if (bn < b1) held = (held & ~(1u << st)) | (uint32_t)issue(phys, st) << st;
+        if (++st == STAGES) { st = 0; parity ^= 1; }
     }
     if (!ok)                                             // a wait ran out: leave no copy behind
-        for (int i = 0; i < KV4_STAGES; ++i)
-            if (live >> i & 1) wait_bar(&sm.full[warp][i], phase >> i & 1, a.status);
+        for (int n = (b - first) / AW; first + n * AW < min(b + STAGES * AW, b1); ++n)
+            wait_bar(&sm.full[warp][n % STAGES], n / STAGES & 1, a.status);
     __syncthreads();                                     // the rings become the merge area
 
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 4 * nt + tig;
-        float l = w.l[nt];
+    for (int i = 0; i < NH; ++i) {
+        const int h = WIDE ? 2 * tig + i : tig;
+        float l = w.l[i];
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         if (h >= G) continue;
-        if (g == 0) { sm.m[warp][h] = w.m[nt]; sm.l[warp][h] = l; }
+        if (g == 0) { sm.m[warp][h] = w.m[i]; sm.l[warp][h] = l; }
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) {
-            const float(&x)[4] = w.o[nt][2 * gr];
-            const float(&y)[4] = w.o[nt][2 * gr + 1];
+            const float(&x)[4] = w.o[2 * gr];
+            const float(&y)[4] = w.o[2 * gr + 1];
             *reinterpret_cast<float4*>(&sm.o[warp][h][32 * gr + 4 * g]) =
-                make_float4(x[0] + x[1], x[2] + x[3], y[0] + y[1], y[2] + y[3]);
+                WIDE ? make_float4(x[i], x[2 + i], y[i], y[2 + i]) : make_float4(x[0] + x[1], x[2] + x[3], y[0] + y[1], y[2] + y[3]);
         }
     }
     __syncthreads();
 
     // the warps in order; thread d owns dimension d
     const int d = threadIdx.x;
-    To* out = static_cast<To*>(a.out) + ((size_t)t * a.n_q + (size_t)kvh * G) * D + d;
+    const size_t row = ((size_t)t * a.n_q + (size_t)kvh * G) * D + d;
     bad = false;
     auto put = [&](int h, float O, float L) {
         const float v = L > 0.f ? O / L : 0.f;           // nothing attended: zeros
-        if (sizeof(To) == 2) reinterpret_cast<__half*>(out)[(size_t)h * D] = to_f16(v, bad);
-        else reinterpret_cast<float*>(out)[(size_t)h * D] = v;
+        if (a.out_f32) static_cast<float*>(a.out)[row + (size_t)h * D] = v;
+        else static_cast<__half*>(a.out)[row + (size_t)h * D] = to_f16(v, bad);
     };
+    cg::cluster_group cluster = cg::this_cluster();
+    if (C > 1) cluster.barrier_wait();                   // every CTA of the cluster has started
     for (int h = 0; h < G; ++h) {
         float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
@@ -444,40 +488,60 @@ __global__ void __launch_bounds__(AW * 32, NT == 1 ? 4 : 3) kv4_decode_kernel(co
             put(h, O, L);
             continue;
         }
-        __syncthreads();                                 // every thread has read head h's maxima
-        sm.o[0][h][d] = O;
-        if (d == 0) { sm.m[0][h] = M; sm.l[0][h] = L; }
+        // CTA h % C finishes head h
+        const int at = h / C * C + rank;
+        *cluster.map_shared_rank(&sm.in_o[at][d], h % C) = O;
+        if (d == 0) {
+            *cluster.map_shared_rank(&sm.in_m[at], h % C) = M;
+            *cluster.map_shared_rank(&sm.in_l[at], h % C) = L;
+        }
     }
     if (C > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         for (int h = rank; h < G; h += C) {
+            const int at = h / C * C;
             float M = -INFINITY, L = 0.f, O = 0.f;
-            for (int c = 0; c < C; ++c) M = fmaxf(M, *cluster.map_shared_rank(&sm.m[0][h], c));
+            for (int c = 0; c < C; ++c) M = fmaxf(M, sm.in_m[at + c]);
             if (M != -INFINITY)
                 for (int c = 0; c < C; ++c) {
-                    const float e = fast_ex2(*cluster.map_shared_rank(&sm.m[0][h], c) - M);
-                    L = fmaf(*cluster.map_shared_rank(&sm.l[0][h], c), e, L);
-                    O = fmaf(*cluster.map_shared_rank(&sm.o[0][h][d], c), e, O);
+                    const float e = fast_ex2(sm.in_m[at + c] - M);
+                    L = fmaf(sm.in_l[at + c], e, L);
+                    O = fmaf(sm.in_o[at + c][d], e, O);
                 }
             put(h, O, L);
         }
-        cluster.sync();                                  // nobody's shared memory is read past here
     }
     if (bad) report(a.status, Q3_STATUS_F16_RANGE);
 }
 
-template <int NT, typename Tq, typename To>
-cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a, int C)
+// CTAs of a (row, KV head).  Four fit an SM (16 warps); the splits grow by twos
+// while the grid still fits the SMs at once (608; a second wave costs more than
+// idle SMs: 64 rows of 2,000 positions 37 us unsplit, 40 in two) and a CTA keeps
+// two blocks (one row of 600 positions: 4.8 us in 8 splits, 5.9 in 4), four for
+// 16, whose clusters leave some SMs out (4 rows of 1,000: 6.3 us in 8, 7.2 in
+// 16; of 32,768: 44 in 8, 39 in 16).
+int decode_splits(const Kv4DecodeArgs& a)
 {
+    const int64_t units = (int64_t)a.T * a.n_kv, blocks = (a.max_ctx + 31) / 32;
+    int C = 1;
+    while (C < MAX_SPLITS && units * 2 * C <= 4 * 152 && blocks >= (C < 8 ? 4 : 8) * C) C *= 2;
+    return C;
+}
+
+template <bool WIDE, typename Tq>
+cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a)
+{
+    constexpr auto kernel = kv4_decode_kernel<WIDE, Tq>;
+    constexpr int smem = (int)sizeof(DecodeShared);
+    const int C = decode_splits(a);
     static std::atomic<unsigned long long> attr_done{0}, wide_done{0};
-    if (cudaError_t e = allow_smem_per_device(kv4_decode_kernel<NT, Tq, To>, (int)sizeof(DecodeShared), attr_done)) return e;
+    if (cudaError_t e = allow_smem_per_device(kernel, smem, attr_done)) return e;
     if (C > 8)
-        if (cudaError_t e = allow_wide_clusters(kv4_decode_kernel<NT, Tq, To>, wide_done)) return e;
+        if (cudaError_t e = allow_wide_clusters(kernel, wide_done)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.T * a.n_kv * C);
     cfg.blockDim = dim3(AW * 32);
-    cfg.dynamicSmemBytes = sizeof(DecodeShared);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -488,27 +552,7 @@ cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a, int C)
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (L.counter) ++*L.counter;
-    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<NT, Tq, To>, a, C);
-}
-
-// CTAs of a (row, KV head): as many of 1, 2, 4, 8, 16 as it takes to fill the
-// SMs (four CTAs each) while every warp has a block.
-int decode_splits(const Kv4DecodeArgs& a)
-{
-    const int64_t units = (int64_t)a.T * a.n_kv;
-    const int blocks = (a.max_ctx + 31) / 32;
-    int C = 1;
-    while (C < 16 && units * C < 4 * 152 && AW * C < blocks) C *= 2;
-    return C;
-}
-
-template <int NT>
-cudaError_t launch_decode_nt(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type)
-{
-    const int C = decode_splits(a);
-    if (q_type == Q3_TYPE_F32)
-        return out_type == Q3_TYPE_F32 ? launch_decode<NT, float, float>(L, a, C) : launch_decode<NT, float, __half>(L, a, C);
-    return out_type == Q3_TYPE_F32 ? launch_decode<NT, __half, float>(L, a, C) : launch_decode<NT, __half, __half>(L, a, C);
+    return cudaLaunchKernelEx(&cfg, kernel, a, C);
 }
 
 // ---------------------------------------------------------------- prefill: tile list and fp16 copy
@@ -607,6 +651,7 @@ __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
     grid_dep_wait();
     if (blockIdx.x == 0) plan_tiles(a);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t magic = a.magic;
     const int64_t step = (int64_t)gridDim.x * (XT / 32);
     int64_t u = (int64_t)blockIdx.x * (XT / 32) + warp;      // unit: (block, K or V, KV head) of the sequences in turn
     int64_t base = 0;
@@ -633,8 +678,8 @@ __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
                     const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src + p * 64) + c);
                     const __half2 sb = *reinterpret_cast<const __half2*>(src + KV4_CODES + p * 16 + (c >> 2) * 4);
                     const __half2 sc = __low2half2(sb), bi = __high2half2(sb);
-                    const uint32_t p0 = kv4_pair<0>(w, sc, bi), p1 = kv4_pair<1>(w, sc, bi), p2 = kv4_pair<2>(w, sc, bi),
-                                   p3 = kv4_pair<3>(w, sc, bi);
+                    const uint32_t p0 = kv4_pair<0>(w, sc, bi, magic), p1 = kv4_pair<1>(w, sc, bi, magic), p2 = kv4_pair<2>(w, sc, bi, magic),
+                                   p3 = kv4_pair<3>(w, sc, bi, magic);
                     uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
                                          __byte_perm(p2, p3, 0x7632));
                     if (p >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
@@ -648,10 +693,10 @@ __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
                     const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(src + pr * 128 + (2 * m + 1) * 16) + gr);
                     const uint2 sb = *reinterpret_cast<const uint2*>(src + KV4_CODES + pr * 32 + gr * 8);
                     const __half2 sc = as_h2(sb.x), bi = as_h2(sb.y);
-                    const uint32_t p0 = kv4_pair<0>(w0, sc, bi), p1 = kv4_pair<1>(w0, sc, bi), p2 = kv4_pair<2>(w0, sc, bi),
-                                   p3 = kv4_pair<3>(w0, sc, bi);
-                    const uint32_t r0 = kv4_pair<0>(w1, sc, bi), r1 = kv4_pair<1>(w1, sc, bi), r2 = kv4_pair<2>(w1, sc, bi),
-                                   r3 = kv4_pair<3>(w1, sc, bi);
+                    const uint32_t p0 = kv4_pair<0>(w0, sc, bi, magic), p1 = kv4_pair<1>(w0, sc, bi, magic), p2 = kv4_pair<2>(w0, sc, bi, magic),
+                                   p3 = kv4_pair<3>(w0, sc, bi, magic);
+                    const uint32_t r0 = kv4_pair<0>(w1, sc, bi, magic), r1 = kv4_pair<1>(w1, sc, bi, magic), r2 = kv4_pair<2>(w1, sc, bi, magic),
+                                   r3 = kv4_pair<3>(w1, sc, bi, magic);
                     uint4 e = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(r0, r1, 0x5410),
                                          __byte_perm(r2, r3, 0x5410));
                     uint4 o = make_uint4(__byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632), __byte_perm(r0, r1, 0x7632),
@@ -680,13 +725,20 @@ cudaError_t launch_kv4_append(const Launch& L, const Kv4AppendArgs& a, int type)
     }
 }
 
-cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type)
+cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& args, int q_type, int out_type)
 {
-    return a.n_q / a.n_kv <= 4 ? launch_decode_nt<1>(L, a, q_type, out_type) : launch_decode_nt<2>(L, a, q_type, out_type);
+    Kv4DecodeArgs a = args;
+    a.magic = KV4_MAGIC;
+    a.out_f32 = out_type == Q3_TYPE_F32;
+    if (a.n_q / a.n_kv <= 4)
+        return q_type == Q3_TYPE_F32 ? launch_decode<false, float>(L, a) : launch_decode<false, __half>(L, a);
+    return q_type == Q3_TYPE_F32 ? launch_decode<true, float>(L, a) : launch_decode<true, __half>(L, a);
 }
 
-cudaError_t launch_kv4_expand(const Launch& L, const Kv4PrefillArgs& a)
+cudaError_t launch_kv4_expand(const Launch& L, const Kv4PrefillArgs& args)
 {
+    Kv4PrefillArgs a = args;
+    a.magic = KV4_MAGIC;
     return launch_ex(L, kv4_expand_kernel, dim3(4 * 152), dim3(XT), a);
 }
 

@@ -369,6 +369,8 @@ struct Kv4DecodeArgs {
     int n_blocks;
     void* out;                 // [T][n_q][128]
     int* status;
+    int out_f32;               // set by the launcher, as is
+    uint32_t magic;            // KV4_MAGIC
 };
 cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type);
 
@@ -393,6 +395,7 @@ struct Kv4PrefillArgs {
     int4* tiles;               // at most T / rows_per_tile + ns
     __half* copy;              // [blocks][2][n_kv][32][128]
     int by_seq;                // block i max_blocks + j is sequence i's block j (else the pool's numbers)
+    uint32_t magic;            // KV4_MAGIC, set by the launcher
 };
 // The sequences' tile list, sorted, and an fp16 copy of their blocks; rows
 // that attend nothing become zeros.

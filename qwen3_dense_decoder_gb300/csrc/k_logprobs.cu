@@ -8,14 +8,15 @@
 // to m' turns (s, t) into exp(m - m') (s, t + (m - m') s).  Lanes, warps and
 // CTAs merge by the same rule in a fixed order.
 //
-// Alternatives: a warp keeps the best 32 it has seen as a list sorted over its
-// lanes.  A lane compares the maximum of 16 new values with the list's
-// k-th; only when one passes does the warp offer candidates, singly (an
-// insertion) or, when many lanes have one, as a sorted batch merged with the
-// list.  On data in no special order that is about k ln(n / 512) insertions a
-// warp.  Lists merge pairwise: element i against 31 - i, then five exchange
-// steps.  Whole keys order (value, then index), so ranks do not depend on the
-// schedule.
+// Alternatives: the pass keeps only the maximum of each lane's values of a
+// round of loads (a slot: 16 values, 32 of the 16-bit types).  The k-th largest
+// of the CTA's 256 lane maxima bounds the row's k-th from below, so at most the
+// slots that reach it, about k of 10,000, are read again and ranked: a warp
+// keeps the best 32 it has seen as a list sorted over its lanes, takes single
+// candidates by insertion and many at once as a sorted batch, and lists merge
+// pairwise (element i against 31 - i, then five exchange steps).  Whole keys
+// order (value, then index), so ranks do not depend on the schedule, and rows in
+// rising order or of one value cost what others do.
 //
 // Rows of few are split over the CTAs of a cluster, merged through
 // distributed shared memory: no workspace, no second launch.
@@ -33,12 +34,40 @@ namespace cg = cooperative_groups;
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int NL = 4;                                    // 16-byte loads a lane has in flight
+constexpr int SLOTS = 40;                                // a lane's slots: V = 151,936 in f32 has 38 rounds
 constexpr float LOG2E = 1.4426950408889634f;
 
 Q3_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// pairs of floats: one instruction for two additions, products or both
+Q3_DEV uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+Q3_DEV float2 halves_of(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+Q3_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+Q3_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+Q3_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // ---------------------------------------------------------------- candidates
@@ -80,6 +109,30 @@ Q3_DEV void merge32(Cand& list, const Cand& other, int lane) {
 #pragma unroll
     for (int j = 16; j > 0; j >>= 1) exchange(list, j, (lane & j) == 0);
 }
+// the same of plain values
+Q3_DEV void exchange(float& c, int j, bool larger) {
+    const float o = __shfl_xor_sync(0xffffffffu, c, j);
+    c = larger ? fmaxf(c, o) : fminf(c, o);
+}
+Q3_DEV void sort32(float& c, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int j = size >> 1; j > 0; j >>= 1) exchange(c, j, ((lane & j) == 0) == ((lane & size) == 0));
+}
+Q3_DEV void merge32(float& list, float other, int lane) {
+    list = fmaxf(list, __shfl_sync(0xffffffffu, other, 31 - lane));
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) exchange(list, j, (lane & j) == 0);
+}
+// eight lists into the first, pairwise
+template <typename C>
+Q3_DEV void merge8(C (&c)[8], int lane) {
+#pragma unroll
+    for (int half = 4; half > 0; half >>= 1)
+#pragma unroll
+        for (int i = 0; i < half; ++i) merge32(c[i], c[i + half], lane);
+}
 // one candidate, the same in every lane
 Q3_DEV void insert(Cand& list, const Cand& c, int lane) {
     const int at = __popc(__ballot_sync(0xffffffffu, before(list, c)));
@@ -112,46 +165,62 @@ template <int N>
 Q3_DEV void add_values(Sums& a, const float (&v)[N], float cm) {
     if (cm > a.m) raise(a, cm);
     const float m = a.m == -INFINITY ? 0.f : a.m;        // -inf - -inf is not a number
-    float s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float d = v[i] - m, e = ex2(d * LOG2E);
-        s[i & 1] += e;
-        t[i & 1] = fmaf(fmaxf(d, -1000.f), e, t[i & 1]); // e is 0 from -127 on; -inf * 0 would not be
+    if (N == 1) {
+        const float d = v[0] - m, e = ex2(d * LOG2E);
+        a.s += e;
+        a.t = fmaf(fmaxf(d, -1000.f), e, a.t);
+        return;
     }
-    a.s += s[0] + s[1];
-    a.t += t[0] + t[1];
+    const uint64_t nm = pair_of(-m, -m), l2e = pair_of(LOG2E, LOG2E);
+    uint64_t s = pair_of(0.f, 0.f), t = s;
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const uint64_t d = add2(pair_of(v[i], v[i + 1]), nm);
+        const float2 u = halves_of(mul2(d, l2e)), dd = halves_of(d);
+        const uint64_t e = pair_of(ex2(u.x), ex2(u.y));
+        s = add2(s, e);
+        // e is 0 from -127 on; -inf * 0 would not be
+        t = fma2(pair_of(fmaxf(dd.x, -1000.f), fmaxf(dd.y, -1000.f)), e, t);
+    }
+    const float2 ss = halves_of(s), tt = halves_of(t);
+    a.s += ss.x + ss.y;
+    a.t += tt.x + tt.y;
 }
 
-// the candidates among a chunk's values (index(i) of value i, or -1: none) join the list
+// The candidates among 16 values, none below `bound`, join the warp's list;
+// index(i): the place of this lane's value i in the row, or -1.
+// kth: the list's k-th entry.
 template <int N, typename Index>
-Q3_DEV void add_candidates(Cand& list, Cand& kth, int k, const float (&v)[N], Index index, int lane) {
+Q3_DEV void add_candidates(Cand& list, Cand& kth, int k, float bound, const float (&v)[N], Index index, int lane) {
     uint32_t left = 0;                                   // values that may still pass
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int at = index(i);
-        if (at >= 0 && before(Cand{key_of(v[i]), at}, kth)) left |= 1u << i;
+        const Cand c{key_of(v[i]), at};
+        if (at >= 0 && !(v[i] < bound) && before(c, kth)) left |= 1u << i;
     }
     for (;;) {
-        Cand best = none();
-        int bi = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (left >> i & 1) {
-                const Cand c{key_of(v[i]), index(i)};
-                if (before(c, best)) { best = c; bi = i; }
-            }
-        if (!before(best, kth)) { best = none(); left = 0; }
-        const uint32_t who = __ballot_sync(0xffffffffu, best.idx != 0x7fffffff);
+        const uint32_t who = __ballot_sync(0xffffffffu, left != 0);
         if (!who) return;
-        if (__popc(who) >= 6) {
-            left &= ~(1u << bi);
-            sort32(best, lane);
-            merge32(list, best, lane);
+        Cand c = none();
+        int ci = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)                      // the lane's best
+            if (left >> i & 1) {
+                const Cand o{key_of(v[i]), index(i)};
+                if (before(o, c)) { c = o; ci = i; }
+            }
+        if (!before(c, kth)) { c = none(); left = 0; }
+        if (__popc(who) >= 2) {
+            left &= ~(1u << ci);
+            sort32(c, lane);
+            merge32(list, c, lane);
         } else {
             const int src = __ffs(who) - 1;
-            insert(list, shfl(best, src), lane);
-            if (lane == src) left &= ~(1u << bi);
+            if (lane == src) left &= ~(1u << ci);
+            c = shfl(c, src);
+            if (!before(c, kth)) continue;
+            insert(list, c, lane);
         }
         kth = shfl(list, k - 1);
     }
@@ -188,22 +257,15 @@ template <> struct Vec<__nv_bfloat16> {
 };
 
 struct Shared {
-    Cand list[WARPS][32];
-    Sums sums[WARPS];
+    Cand list[8][32];          // of the warps; in CTA 0 then of the cluster's CTAs
+    Sums sums[8];
+    float maxima[WARPS][32];   // the lanes' maxima, sorted in each warp
+    float slot[SLOTS][THREADS];
 };
-
-// the lists of n warps (a power of two), warp w holding its own, into warp 0's
-Q3_DEV void merge_lists(Shared& sm, Cand& list, int warp, int lane, int n) {
-    for (int half = n >> 1; half > 0; half >>= 1) {
-        if (warp >= half && warp < 2 * half) sm.list[warp][lane] = list;
-        __syncthreads();
-        if (warp < half) merge32(list, sm.list[warp + half][lane], lane);
-        __syncthreads();
-    }
-}
+static_assert(WARPS == 8, "merge8");
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS, 3) logprobs_kernel(const LogprobArgs a, int C)
+__global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobArgs a, int C)
 {
     constexpr int EPL = Vec<T>::N, GL = 16 / EPL;        // words of a group of 16 values
     __shared__ Shared sm;
@@ -228,15 +290,14 @@ __global__ void __launch_bounds__(THREADS, 3) logprobs_kernel(const LogprobArgs 
 
     const int k = a.top;
     Sums sums{-INFINITY, 0.f, 0.f};
-    Cand list = none(), kth = none();
-    // the filter on values: kth's, or nothing passes it without a list
-    auto single = [&](int from, int n) {
-        const int i = from + lane;
-        const float v[1] = {lane < n ? Vec<T>::one(x + i) : -INFINITY};
-        if (lane < n) add_values(sums, v, v[0]);
-        if (k) add_candidates(list, kth, k, v, [&](int) { return lane < n ? i : -1; }, lane);
-    };
-    if (rank == 0 && warp == 0 && head) single(0, head);
+    // what a row has before its first and after its last whole word: a value a lane
+    const bool ends = rank == 0 && warp == 0;
+    const int rest = a.V - tail, end_at = lane < head ? lane : lane - head < rest ? tail + lane - head : -1;
+    float end_v[1] = {-INFINITY};
+    if (ends && end_at >= 0) {
+        end_v[0] = Vec<T>::one(x + end_at);
+        add_values(sums, end_v, end_v[0]);
+    }
 
     // this warp's share of the words, a multiple of a full load each
     const int shares = C * WARPS, share = rank * WARPS + warp;
@@ -250,6 +311,10 @@ __global__ void __launch_bounds__(THREADS, 3) logprobs_kernel(const LogprobArgs 
             if (w < w1) next[l] = ldg_nc_v4(xw + w);
         }
     };
+    // round n of loads belongs to slot n / per_slot
+    const int rounds = (w1 - w0 + NL * 32 - 1) / (NL * 32), per_slot = (rounds + SLOTS - 1) / SLOTS;
+    float most = -INFINITY, slot_max = -INFINITY;        // of the lane, of its current slot
+    int in_slot = 0, slot = 0;
     if (w0 < w1) fetch(w0);
     for (int at = w0; at < w1; at += NL * 32) {
         uint4 cur[NL];
@@ -270,20 +335,16 @@ __global__ void __launch_bounds__(THREADS, 3) logprobs_kernel(const LogprobArgs 
             float cm = v[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) cm = fmaxf(cm, v[i]);
-            if (k) {
-                // past the list's k-th by value, or not comparable with it
-                const bool pass = kth.key <= 1u || !(cm <= value_of(kth.key));
-                if (__any_sync(0xffffffffu, pass))
-                    add_candidates(list, kth, k, v, [&](int i) {
-                        const int w = ag + i / EPL * 32;
-                        return w < w1 ? head + w * EPL + i % EPL : -1;
-                    }, lane);
-            }
+            slot_max = fmaxf(slot_max, cm);
             add_values(sums, v, cm);
         }
+        if (k && (++in_slot == per_slot || at + NL * 32 >= w1)) {
+            sm.slot[slot++][threadIdx.x] = slot_max;
+            most = fmaxf(most, slot_max);
+            slot_max = -INFINITY;
+            in_slot = 0;
+        }
     }
-    if (rank == C - 1 && warp == WARPS - 1 && tail < a.V) single(tail, a.V - tail);
-
     // lanes, then warps, then CTAs
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -295,34 +356,79 @@ __global__ void __launch_bounds__(THREADS, 3) logprobs_kernel(const LogprobArgs 
         sums = lo;
     }
     if (lane == 0) sm.sums[warp] = sums;
-    if (k) merge_lists(sm, list, warp, lane, WARPS);
-    else __syncthreads();
+    Cand list = none();
+    if (k) {
+        // the bound: the k-th largest of the lanes' maxima (-inf where fewer
+        // lanes hold a number: all may be among the k)
+        const float lane_max = most;
+        sort32(most, lane);
+        sm.maxima[warp][lane] = most;
+        __syncthreads();
+        float lists[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) lists[i] = sm.maxima[i][lane];
+        merge8(lists, lane);
+        const float bound = __shfl_sync(0xffffffffu, lists[0], k - 1);
+        Cand kth = none();
+        if (ends) add_candidates(list, kth, k, bound, end_v, [&](int) { return end_at; }, lane);
+        // every lane walks its slots; those that may hold a candidate are read again
+        const int end = lane_max < bound ? 0 : slot;         // a lane below the bound has none
+        for (int n = 0;; ++n) {
+            for (; n < end; ++n) {
+                const float v = sm.slot[n][threadIdx.x];
+                if (v < bound) continue;
+                const int first = w0 + n * per_slot * NL * 32 + lane;
+                if (first < w1 && before(Cand{key_of(v), head + first * EPL}, kth)) break;
+            }
+            if (!__any_sync(0xffffffffu, n < end)) break;
+            for (int p = 0; p < per_slot; ++p) {
+                const int at = w0 + (n * per_slot + p) * NL * 32 + lane;
+#pragma unroll
+                for (int g = 0; g < NL / GL; ++g) {
+                    float v[16];
+                    auto word = [&](int l) { return at + (g * GL + l) * 32; };
+#pragma unroll
+                    for (int l = 0; l < GL; ++l) {
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (n < end && word(l) < w1) w = __ldg(xw + word(l));
+                        Vec<T>::get(w, v + l * EPL);
+                    }
+                    add_candidates(list, kth, k, bound, v, [&](int i) {
+                        const int w = word(i / EPL);
+                        return n < end && w < w1 ? head + w * EPL + i % EPL : -1;
+                    }, lane);
+                }
+            }
+        }
+        sm.list[warp][lane] = list;
+    }
+    __syncthreads();
+    // the warps' in warp 0, then the CTAs' in CTA 0's
+    auto merged = [&](int n) {
+        if (!k) return;
+        Cand c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = i < n ? sm.list[i][lane] : none();
+        merge8(c, lane);
+        list = c[0];
+    };
     if (warp == 0) {
         sums = sm.sums[0];
         for (int w = 1; w < WARPS; ++w) join(sums, sm.sums[w]);
+        merged(WARPS);
     }
     if (C > 1) {
         cg::cluster_group cluster = cg::this_cluster();
-        __syncthreads();
+        cluster.sync();                                  // CTA 0 is done with its warps' lists
         if (warp == 0) {
-            sm.list[0][lane] = list;
-            if (lane == 0) sm.sums[0] = sums;
+            *cluster.map_shared_rank(&sm.list[rank][lane], 0) = list;
+            if (lane == 0) *cluster.map_shared_rank(&sm.sums[rank], 0) = sums;
         }
         cluster.sync();
-        Sums all = sums;
-        if (rank == 0) {
-            list = none();
-            if (k && warp < C) {
-                const Cand* o = cluster.map_shared_rank(&sm.list[0][lane], warp);
-                list = *o;
-            }
-            if (warp == 0)
-                for (int c = 1; c < C; ++c) join(all, *cluster.map_shared_rank(&sm.sums[0], c));
-        }
-        cluster.sync();                                  // nobody's shared memory is read past here
-        if (rank) return;
-        if (k) merge_lists(sm, list, warp, lane, C);
-        sums = all;
+        if (rank || warp) return;
+        sums = sm.sums[0];
+        for (int c = 1; c < C; ++c) join(sums, sm.sums[c]);
+        merged(C);
     }
     if (warp) return;
 
@@ -368,14 +474,14 @@ cudaError_t launch_t(const Launch& L, const LogprobArgs& a, int C)
 
 }  // namespace
 
-// CTAs of a row: 1, or as many of 2, 4, 8 as it takes to give every SM a few
-// (four of 256 threads are resident) while a warp still has a full round of
-// loads.
+// CTAs of a row: twice as many, up to 8, while SMs are left out and a warp keeps
+// a full round of loads (64 rows of 151,936 f32 with 20 alternatives: 19.3 us
+// in 4, 21.9 in 8; one row: 12.7 in 8, 14 in 4).
 cudaError_t launch_logprobs(const Launch& L, const LogprobArgs& a, int type)
 {
     const int64_t round = (int64_t)WARPS * 32 * NL * (type == Q3_TYPE_F32 ? 4 : 8);
     int C = 1;
-    while (C < 8 && (int64_t)a.N * C < 4 * 152 && a.V > round * C) C *= 2;
+    while (C < 8 && (int64_t)a.N * C < 152 && a.V > round * C) C *= 2;
     switch (type) {
     case Q3_TYPE_F32: return launch_t<float>(L, a, C);
     case Q3_TYPE_F16: return launch_t<__half>(L, a, C);

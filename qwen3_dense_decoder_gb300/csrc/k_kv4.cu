@@ -31,6 +31,9 @@ cudaError_t launch_ex(const Launch& L, K kern, dim3 grid, dim3 block, const A& a
     return cudaLaunchKernelEx(&cfg, kern, args);
 }
 
+Q3_DEV __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+Q3_DEV uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
 Q3_DEV void report(int* status, int bits) { if (status) set_status(status, bits); }
 
 // lane l's values [4l, 4l + 4) of a 128-value row, in FP32
@@ -44,76 +47,177 @@ Q3_DEV void load4(const __half* p, int lane, float (&y)[4]) {
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
     y[0] = a.x; y[1] = a.y; y[2] = b.x; y[3] = b.y;
 }
-Q3_DEV void load4(const __nv_bfloat16* p, int lane, float (&y)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p + lane * 4);
-    y[0] = bf16lo(v.x); y[1] = bf16hi(v.x); y[2] = bf16lo(v.y); y[3] = bf16hi(v.y);
-}
-Q3_DEV void store4(__half* p, int lane, const __half (&h)[4]) {
-    const __half2 a = __halves2half2(h[0], h[1]), b = __halves2half2(h[2], h[3]);
-    *reinterpret_cast<uint2*>(p + lane * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 // ---------------------------------------------------------------- append
-// One warp per head of one row: q heads are normed, rotated and stored in
-// fp16; k heads are normed, rotated and packed, v heads packed, into the
-// position's place of the row's block table.
+// Eight lanes take a head, so a warp four heads of a row: q heads are normed,
+// rotated and stored in fp16; k heads are normed, rotated and packed, v heads
+// packed, into the position's place of the row's block table.  Lane j of a head
+// holds dimensions [8j, 8j + 8) and [64 + 8j, ..): both halves of its rotation
+// pairs, and eight values each of groups j / 4 and 2 + j / 4, so a head costs
+// three exchange steps for the norm, none for the rotation and two for a
+// group's range, and the square root, the reciprocals and the divisions serve
+// four heads at once.  A head's value costs about half an instruction (q) to
+// one (k); the bytes are (n_q + 2 n_kv) 128 projections in, 2 bytes a q value
+// and 0.625 a k or v value out.
+Q3_DEV void load8(const float* p, float* y) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w; y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
+}
+Q3_DEV void load8(const __half* p, float* y) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        y[2 * i] = f.x; y[2 * i + 1] = f.y;
+    }
+}
+Q3_DEV void load8(const __nv_bfloat16* p, float* y) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { y[2 * i] = bf16lo(w[i]); y[2 * i + 1] = bf16hi(w[i]); }
+}
+Q3_DEV void store8(__half* p, const uint32_t (&h)[4]) { *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]); }
+
 template <typename Tin>
 __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 {
+    grid_dep_launch();
     grid_dep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const int hh = blockIdx.y * 4 + warp;                // q heads, then k heads, then v heads
-    if (hh >= a.n_q + 2 * a.n_kv) return;
+    const int lane = threadIdx.x & 31, j = lane & 7;
+    const int n_heads = a.n_q + 2 * a.n_kv, chunks = (n_heads + 3) / 4;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int t = (int)(w / chunks), hh = (int)(w % chunks) * 4 + (lane >> 3);
+    if (t >= a.T) return;
+    const bool real = hh < n_heads;                      // a warp's last heads may not exist
     const bool is_q = hh < a.n_q, is_k = !is_q && hh < a.n_q + a.n_kv;
     const int kvh = is_k ? hh - a.n_q : hh - a.n_q - a.n_kv;
-    __half* q_dst = a.q_out ? a.q_out + ((size_t)t * a.n_q + hh) * D : nullptr;
-    __half* kv_dst = a.kv_out ? a.kv_out + (((size_t)t * 2 + (is_k ? 0 : 1)) * a.n_kv + kvh) * D : nullptr;
-    __half* dst = is_q ? q_dst : kv_dst;
-    const int pos = a.row_pos[t];
-    if (pos < 0 || pos >= a.rope_len) {                  // a padding row, or one past the rotation table
-        const __half z[4] = {__half(), __half(), __half(), __half()};
-        if (dst) store4(dst, lane, z);
-        if (pos >= 0 && lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        return;
-    }
-    float y[4];
-    const size_t at = (size_t)t * a.qkv_stride + (size_t)hh * D;
+    const int pos = a.row_pos[t], slot = a.row_slot[t];
+
+    float y[16];                                         // dimensions 8 j + e, then 64 + 8 j + e
+    const size_t from = (size_t)t * a.qkv_stride + (size_t)(real ? hh : 0) * D + 8 * j;
     if (sizeof(Tin) == 4 && a.n_parts > 1) {
-        y[0] = y[1] = y[2] = y[3] = 0.f;
-        for (int i = 0; i < a.n_parts; ++i) {
-            float z[4];
-            load4(a.parts + (size_t)i * a.T * a.qkv_stride + at, lane, z);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] += z[e];
+        for (int e = 0; e < 16; ++e) y[e] = 0.f;
+        for (int n = 0; n < a.n_parts; ++n) {
+            const float* p = a.parts + (size_t)n * a.T * a.qkv_stride + from;
+            float z[16];
+            load8(p, z);
+            load8(p + 64, z + 8);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] += z[e];
         }
     } else {
-        load4(static_cast<const Tin*>(a.qkv) + at, lane, y);
+        const Tin* p = static_cast<const Tin*>(a.qkv) + from;
+        load8(p, y);
+        load8(p + 64, y + 8);
     }
-    if (is_q || is_k)
-        head_norm_rope(y, is_q ? a.q_gain : a.k_gain, a.rope + (size_t)pos * (D / 2), a.eps, lane);
-    if (is_q) {
+    const __nv_bfloat16* gain = (is_q ? a.q_gain : a.k_gain) + 8 * j;
+    const uint4 g0 = *reinterpret_cast<const uint4*>(gain), g1 = *reinterpret_cast<const uint4*>(gain + 64);
+    const bool live = pos >= 0 && pos < a.rope_len;      // else a padding row, or one past the rotation table
+    float cs[16];
+    {
+        const float* rope = reinterpret_cast<const float*>(a.rope + (size_t)(live ? pos : 0) * (D / 2) + 8 * j);
+        load8(rope, cs);
+        load8(rope + 8, cs + 8);
+    }
+    int blk = -1;
+    if (live && !is_q && real && slot >= 0 && slot < a.n_slots && pos / 32 < a.max_blocks)
+        blk = a.tables[(size_t)slot * a.max_blocks + pos / 32];
+    const bool placed = blk >= 0 && blk < a.n_blocks;
+    if (real && j == 0 && pos >= 0 && (!live || (!is_q && !placed))) report(a.status, Q3_STATUS_BLOCK_RANGE);
+    __half* dst = is_q ? (a.q_out ? a.q_out + ((size_t)t * a.n_q + hh) * D : nullptr)
+                       : (a.kv_out ? a.kv_out + (((size_t)t * 2 + (is_k ? 0 : 1)) * a.n_kv + kvh) * D : nullptr);
+    if (!real) dst = nullptr;
+    if (!live) {                                         // the same for all of the warp's heads
+        const uint32_t z[4] = {0, 0, 0, 0};
+        if (dst) { store8(dst + 8 * j, z); store8(dst + 64 + 8 * j, z); }
+        return;
+    }
+
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (is_q || is_k) {
+        float g[16];
+        load8(reinterpret_cast<const __nv_bfloat16*>(&g0), g);
+        load8(reinterpret_cast<const __nv_bfloat16*>(&g1), g + 8);
+        const float r = 1.0f / sqrtf(ss / 128.0f + a.eps);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = y[e] * r * g[e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float lo = y[e], hi = y[8 + e], c = cs[2 * e], sn = cs[2 * e + 1];
+            y[e] = lo * c - hi * sn;
+            y[8 + e] = hi * c + lo * sn;
+        }
+    }
+    // the groups' ranges: this lane's eight values, then the four lanes'
+    float lo[2], hi[2];
+    bool number = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        lo[h] = hi[h] = y[8 * h];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) { lo[h] = fminf(lo[h], y[8 * h + e]); hi[h] = fmaxf(hi[h], y[8 * h + e]); }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) number = number && y[8 * h + e] == y[8 * h + e];
+    }
+    const float most = is_q ? 65504.0f : KV4_MAX;
+    const bool bad = real && (!number || fmaxf(fmaxf(hi[0], hi[1]), -fminf(lo[0], lo[1])) > most);
+    if (bad) report(a.status, Q3_STATUS_F16_RANGE);
+    if (__all_sync(0xffffffffu, is_q)) {
         if (!dst) return;
-        bool bad = false;
-        const __half h[4] = {to_f16(y[0], bad), to_f16(y[1], bad), to_f16(y[2], bad), to_f16(y[3], bad)};
-        store4(dst, lane, h);
-        if (bad) report(a.status, Q3_STATUS_F16_RANGE);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = as_u32(__floats2half2_rn(y[8 * h + 2 * i], y[8 * h + 2 * i + 1]));
+            store8(dst + 64 * h + 8 * j, v);
+        }
         return;
     }
-    uint32_t codes;
-    __half scale, bias, val[4];
-    if (!kv4_pack(y, codes, scale, bias, val)) report(a.status, Q3_STATUS_F16_RANGE);
-    if (dst) store4(dst, lane, val);
-    const int slot = a.row_slot[t], j = pos / 32;
-    const int blk = slot >= 0 && slot < a.n_slots && j < a.max_blocks ? a.tables[(size_t)slot * a.max_blocks + j] : -1;
-    if (blk < 0 || blk >= a.n_blocks) {
-        if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            lo[h] = fminf(lo[h], __shfl_xor_sync(0xffffffffu, lo[h], o));
+            hi[h] = fmaxf(hi[h], __shfl_xor_sync(0xffffffffu, hi[h], o));
+        }
+    uint8_t* tile = placed ? a.kv + (((size_t)blk * 2 + (is_k ? 0 : 1)) * a.n_kv + kvh) * KV4_TILE : nullptr;
+    const int p = pos % 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float(&x)[8] = *reinterpret_cast<const float(*)[8]>(y + 8 * h);
+        uint32_t v[4];
+        if (is_q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = as_u32(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+            if (dst) store8(dst + 64 * h + 8 * j, v);
+            continue;
+        }
+        __half scale, bias;
+        const uint32_t codes = kv4_codes(x, lo[h], hi[h], scale, bias, v);
+        if (dst) store8(dst + 64 * h + 8 * j, v);
+        if (!tile) continue;
+        const int grp = 2 * h + j / 4;
+        if (is_k) {
+            *reinterpret_cast<uint32_t*>(tile + p * 64 + 32 * h + 4 * j) = codes;
+            if (j % 4 == 0)
+                *reinterpret_cast<__half2*>(tile + KV4_CODES + p * 16 + grp * 4) = __halves2half2(scale, bias);
+        } else {
+            uint8_t* word = tile + (p >> 1) * 128 + (j % 4) * 32 + grp * 4 + (p & 1) * 2;
+            *reinterpret_cast<uint16_t*>(word) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t*>(word + 16) = (uint16_t)(codes >> 16);
+            if (j % 4 == 0) {
+                __half* par = reinterpret_cast<__half*>(tile + KV4_CODES + (p >> 1) * 32 + grp * 8);
+                par[p & 1] = scale;
+                par[2 + (p & 1)] = bias;
+            }
+        }
     }
-    uint8_t* tile = a.kv + (((size_t)blk * 2 + (is_k ? 0 : 1)) * a.n_kv + kvh) * KV4_TILE;
-    if (is_k) kv4_store_k(tile, pos % 32, codes, scale, bias, lane);
-    else kv4_store_v(tile, pos % 32, codes, scale, bias, lane);
 }
 
 // ---------------------------------------------------------------- decode attention
@@ -162,8 +266,6 @@ Q3_DEV uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-Q3_DEV __half2 as_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
-Q3_DEV uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
 // mbar_wait with an optional status word
 Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
@@ -715,13 +817,23 @@ __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
 
 }  // namespace
 
+namespace {
+
+template <typename Tin>
+cudaError_t launch_append(const Launch& L, const Kv4AppendArgs& a)
+{
+    const int64_t warps = (int64_t)a.T * ((a.n_q + 2 * a.n_kv + 3) / 4);
+    return launch_ex(L, kv4_append_kernel<Tin>, dim3((unsigned)((warps + 3) / 4)), dim3(128), a);
+}
+
+}  // namespace
+
 cudaError_t launch_kv4_append(const Launch& L, const Kv4AppendArgs& a, int type)
 {
-    const dim3 grid(a.T, (a.n_q + 2 * a.n_kv + 3) / 4);
     switch (type) {
-    case Q3_TYPE_F32: return launch_ex(L, kv4_append_kernel<float>, grid, dim3(128), a);
-    case Q3_TYPE_F16: return launch_ex(L, kv4_append_kernel<__half>, grid, dim3(128), a);
-    default: return launch_ex(L, kv4_append_kernel<__nv_bfloat16>, grid, dim3(128), a);
+    case Q3_TYPE_F32: return launch_append<float>(L, a);
+    case Q3_TYPE_F16: return launch_append<__half>(L, a);
+    default: return launch_append<__nv_bfloat16>(L, a);
     }
 }
 

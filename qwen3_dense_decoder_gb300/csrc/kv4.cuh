@@ -30,48 +30,40 @@ namespace q3 {
 // |x| a packed row may hold: up to here no stored value passes the fp16 range
 constexpr float KV4_MAX = 65000.0f;
 
-// One head row held by a warp, lane l values [4l, 4l + 4): group b is lanes
-// 8b .. 8b + 7.  Returns the lane's four codes (value 4l + i in bits 4 i), its
-// group's scale and bias, and the values the cache then holds.  false in a
-// lane whose values leave the range (or are not numbers).
-Q3_DEV bool kv4_pack(const float (&y)[4], uint32_t& codes, __half& scale, __half& bias, __half (&val)[4]) {
-    float lo = fminf(fminf(y[0], y[1]), fminf(y[2], y[3]));
-    float hi = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-#pragma unroll
-    for (int o = 1; o <= 4; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
+// Eight values x of a group whose least and largest are lo and hi: their codes
+// (value i in bits 4 i), the group's scale and bias, and the values the cache
+// then holds, as fp16 pairs.  The rule divides by the scale and rounds; a
+// product with the reciprocal is within 2^-18 of that quotient (below 16), so
+// only where it lies within 2^-12 of a half does the division decide.
+Q3_DEV uint32_t kv4_codes(const float (&x)[8], float lo, float hi, __half& scale, __half& bias, uint32_t (&val)[4]) {
     scale = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
     bias = __float2half_rn(lo);
     const float s = __half2float(scale), b = __half2float(bias);
-    bool ok = true;
-    codes = 0;
+    const float inv = s != 0.0f ? __frcp_rn(s) : 0.0f;   // a zero scale gives zero codes
+    float q[8];
+    bool close = false;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        ok = ok && fabsf(y[e]) <= KV4_MAX;
-        int q = 0;
-        if (s != 0.0f) q = (int)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y[e], b), s)), 0.0f), 15.0f);
-        codes |= (uint32_t)q << (4 * e);
-        val[e] = __hfma(scale, __int2half_rn(q), bias);
+    for (int i = 0; i < 8; ++i) {
+        const float u = __fsub_rn(x[i], b) * inv;
+        q[i] = rintf(u);
+        close = close || fabsf(u - q[i]) > 0.5f - 0x1p-12f;
     }
-    return ok;
-}
-
-// Store a packed row at position r of a pool tile.
-Q3_DEV void kv4_store_k(uint8_t* tile, int r, uint32_t codes, __half scale, __half bias, int lane) {
-    *reinterpret_cast<uint16_t*>(tile + r * 64 + lane * 2) = (uint16_t)codes;
-    if ((lane & 7) == 0)
-        *reinterpret_cast<__half2*>(tile + KV4_CODES + r * 16 + (lane >> 3) * 4) = __halves2half2(scale, bias);
-}
-Q3_DEV void kv4_store_v(uint8_t* tile, int r, uint32_t codes, __half scale, __half bias, int lane) {
-    const int g = lane & 7, grp = lane >> 3;
-    *reinterpret_cast<uint16_t*>(tile + (r >> 1) * 128 + g * 16 + grp * 4 + (r & 1) * 2) = (uint16_t)codes;
-    if (g == 0) {
-        __half* par = reinterpret_cast<__half*>(tile + KV4_CODES + (r >> 1) * 32 + grp * 8);
-        par[r & 1] = scale;
-        par[2 + (r & 1)] = bias;
+    if (close && s != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = rintf(__fdiv_rn(__fsub_rn(x[i], b), s));
     }
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = fminf(fmaxf(q[i], 0.0f), 15.0f);
+        codes |= (uint32_t)q[i] << (4 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = __hfma2(__floats2half2_rn(q[2 * i], q[2 * i + 1]), __half2half2(scale), __half2half2(bias));
+        val[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return codes;
 }
 
 // The fp16 pair 1024, 1024.  It reaches the kernels as an argument: known at

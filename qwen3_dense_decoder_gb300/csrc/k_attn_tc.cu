@@ -44,11 +44,6 @@
 //                once the buffer is free
 // Tensor memory (512 columns): S[2] at 0 / 128 (P high at +0, low at +64,
 // over S), O at 256, Q high at 384, low at 448.
-// The 4-bit cache (KV4) runs the same kernel over an fp16 copy of the round's
-// blocks (k_kv4.cu expands them; a stored value is an fp16 number): operands
-// are fp16, Q and the cache enter exactly, P is rounded to fp16 once, so each
-// product is one MMA instead of two.  Its items come from tiles sorted on the
-// device, longest context first, dealt to the CTAs back and forth.
 // K/V rows past a row's position are finite (the pool is zeroed when it is
 // made, and only finite BF16 values are stored), so P = 0 there contributes
 // nothing.  Every wait is bounded; a timeout sets the status word and the CTA
@@ -90,53 +85,8 @@ constexpr size_t SMEM_BYTES = sizeof(TcSmem) + 1024;
 // Instruction descriptors: bf16 A/B (format 1 at [7,10) and [10,13)), FP32
 // accumulator, M = 128, N = 128.  S: B K-major.  PV: B (V, positions x dims)
 // MN-major (bit 16).
-// KV4: fp16 A/B (format 0).
-template <bool KV4> constexpr uint32_t IDESC_S = idesc_f16_f32(128, 128) | (KV4 ? 0u : (1u << 7) | (1u << 10));
-template <bool KV4> constexpr uint32_t IDESC_PV = IDESC_S<KV4> | (1u << 16);
-// parts of Q and P: high and low BF16, or one fp16
-template <bool KV4> constexpr int PARTS = KV4 ? 1 : 2;
-
-// MN-major 128-byte-swizzled operand: rows of 64 MN elements (128 bytes),
-// 8-row groups 1024 bytes apart along K (stride offset), 64-element MN blocks
-// `lbo` bytes apart (leading offset).
-Q3_DEV uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16
-Q3_DEV void tc_mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                          uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-Q3_DEV void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-
-Q3_DEV void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-                    "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-                    "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
-}
-Q3_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+constexpr uint32_t IDESC_S = idesc_f16_f32(128, 128) | (1u << 7) | (1u << 10);
+constexpr uint32_t IDESC_PV = IDESC_S | (1u << 16);
 
 // x as a high/low pair of bf16: hi = bf16(x), lo = bf16(x - hi)
 Q3_DEV void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
@@ -165,26 +115,12 @@ Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, TcSmem& sm, int* status) {
 }
 
 struct Item {
-    int row0, nrows, pos0, pos_last, n_kt, kvh, seq;
+    int row0, nrows, pos0, pos_last, n_kt, kvh;
     const int* table;
 };
 
-// Item k of this CTA.  KV4: tile i of the sorted list for KV head h is number
-// i n_kv + h, dealt in rows of gridDim.x, every other row backwards.
-template <bool KV4>
 Q3_DEV Item item_of(const PrefillAttnArgs& p, int k) {
     Item it;
-    if (KV4) {
-        const int P = gridDim.x, n = k * P + ((k & 1) ? P - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        const int4 t = p.tiles[n / p.n_kv];
-        it.kvh = n % p.n_kv;
-        it.row0 = t.x; it.nrows = t.y; it.pos0 = t.z;
-        it.pos_last = t.z + t.y - 1;
-        it.n_kt = it.pos_last / BN + 1;
-        it.seq = t.w;
-        it.table = p.tables + (size_t)(p.seq_slot ? p.seq_slot[t.w] : t.w) * p.max_blocks;
-        return it;
-    }
     const int code = p.sched_items[k];
     const int tile = code / p.n_kv;
     it.kvh = code % p.n_kv;
@@ -198,7 +134,6 @@ Q3_DEV Item item_of(const PrefillAttnArgs& p, int k) {
 }
 
 // ---------------------------------------------------------------- MMA issuer
-template <bool KV4>
 Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0, int i1) {
     uint32_t g = 0;                                  // K/V tiles issued so far by this CTA
     // S = (Q_hi + Q_lo) K^T: 16 dims a step, the high part's 8 steps, then the low part's
@@ -208,12 +143,12 @@ Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0
         tc_fence_after();
         const uint32_t ka = smem_u32(sm.k[st]);
 #pragma unroll
-        for (int part = 0; part < PARTS<KV4>; ++part)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
                 const uint32_t off = (s >> 2) * ATOM + (s & 3) * 32;
                 tc_mma_f16_ts(tmem + T_S + b * 128, tmem + T_Q + part * 64 + s * 8, smem_desc_sw128(ka + off),
-                              IDESC_S<KV4>, (part > 0 || s > 0) ? 1u : 0u);
+                              IDESC_S, (part > 0 || s > 0) ? 1u : 0u);
             }
         tc_commit(&sm.s_full[b]);
         tc_commit(&sm.k_free[st]);
@@ -221,12 +156,12 @@ Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0
     };
     bool ok = true;
     if (i0 < i1) {
-        const Item it0 = item_of<KV4>(p, i0);
+        const Item it0 = item_of(p, i0);
         ok = wait_bar(&sm.q_full, 0, sm, p.status) && issue_s(0);
         if (ok && it0.n_kt == 1) tc_commit(&sm.q_free);
     }
     for (int k = i0, local = 0; k < i1 && ok; ++k, ++local) {
-        const Item it = item_of<KV4>(p, k);
+        const Item it = item_of(p, k);
         for (int t = 0; t < it.n_kt; ++t, ++g) {
             // scores of the item's next tile run while the softmax works on this one;
             // after the item's last scores its Q buffer is free for the next item
@@ -243,11 +178,11 @@ Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0
             // O += (P_hi + P_lo) V, 16 positions a step; P lies over S[b]
             const uint32_t va = smem_u32(sm.v[st]);
 #pragma unroll
-            for (int part = 0; part < PARTS<KV4>; ++part)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int s = 0; s < BN / 16; ++s)
                     tc_mma_f16_ts(tmem + T_O, tmem + T_S + b * 128 + part * 64 + s * 8,
-                                  smem_desc_sw128_mn(va + s * 2048, ATOM), IDESC_PV<KV4>,
+                                  smem_desc_sw128_mn(va + s * 2048, ATOM), IDESC_PV,
                                   (t > 0 || part > 0 || s > 0) ? 1u : 0u);
             tc_commit(&sm.pv_done[b]);
             tc_commit(&sm.v_free[st]);
@@ -256,7 +191,7 @@ Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0
         // the next item's first scores (g is its first tile)
         if (k + 1 < i1) {
             const int nl = local + 1;
-            const Item nx = item_of<KV4>(p, k + 1);
+            const Item nx = item_of(p, k + 1);
             ok = wait_bar(&sm.q_full, nl & 1, sm, p.status) && issue_s(g);
             if (ok && nx.n_kt == 1) tc_commit(&sm.q_free);
         }
@@ -273,13 +208,12 @@ Q3_DEV void mma_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0
 // before the stage is waited for.  A block past the item's last position (or
 // whose table entry is outside the pool) is read at row -32, wholly outside
 // the tensor, and lands as zeros.
-template <bool KV4>
 Q3_DEV void load_role(const PrefillAttnArgs& p, const CUtensorMap* tkv, TcSmem& sm, int i0, int i1, int which) {
     uint64_t* ld = which ? sm.v_load : sm.k_load;
     uint64_t* fr = which ? sm.v_free : sm.k_free;
     uint32_t g = 0;
     for (int k = i0; k < i1; ++k) {
-        const Item it = item_of<KV4>(p, k);
+        const Item it = item_of(p, k);
         for (int t = 0; t < it.n_kt; ++t, ++g) {
             const int b = g % NST;
             int row[BN / 32];
@@ -290,7 +224,7 @@ Q3_DEV void load_role(const PrefillAttnArgs& p, const CUtensorMap* tkv, TcSmem& 
                 if (kp <= it.pos_last) {
                     const int ph = it.table[kp >> 5];
                     if (ph >= 0 && ph < p.n_blocks)
-                        row[j] = KV4 ? (((p.by_seq ? it.seq * p.max_blocks + (kp >> 5) : ph) * 2 + which) * p.n_kv + it.kvh) * 32 : p.kv_row0 + ((ph * 2 + which) * p.n_kv + it.kvh) * 32;
+                        row[j] = p.kv_row0 + ((ph * 2 + which) * p.n_kv + it.kvh) * 32;
                     else if (which == 0)
                         set_status(p.status, Q3_STATUS_BLOCK_RANGE);
                 }
@@ -312,15 +246,14 @@ Q3_DEV void load_role(const PrefillAttnArgs& p, const CUtensorMap* tkv, TcSmem& 
 // index r / G, head r % G of the item (padding rows repeat row 0).  The next
 // item's rows are loaded while the current item's scores still read the
 // buffer; once the last of them is done the high and low parts are stored.
-template <bool KV4>
 Q3_DEV void q_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0, int i1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, row = quad * 32 + lane;
     const int G = p.n_q / p.n_kv, R = 128 / G;
-    const size_t qw = KV4 ? (size_t)p.q_stride : (size_t)p.n_q * D;
+    const int qw = p.n_q * D;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
     for (int k = i0, local = 0; k < i1; ++k, ++local) {
-        const Item it = item_of<KV4>(p, k);
+        const Item it = item_of(p, k);
         int ir = row / G, hh = row % G;
         if (ir >= R) ir = hh = 0;
         const int src_row = it.row0 + min(ir, it.nrows - 1);
@@ -333,12 +266,6 @@ Q3_DEV void q_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0, 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {                      // 32 dims (16 columns) at a time
             uint32_t hi[16], lo[16];
-            if (KV4) {                                     // as it came
-#pragma unroll
-                for (int e = 0; e < 16; ++e) hi[e] = (&qv[c * 4 + e / 4].x)[e & 3];
-                tmem_st_32x32b_x16(tl + T_Q + c * 16, hi);
-                continue;
-            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const uint4 w = qv[c * 4 + e / 4];
@@ -373,7 +300,6 @@ Q3_DEV bool pair_sync(TcSmem& sm, int quad, uint32_t& n, int* status) {
     return ok;
 }
 
-template <bool KV4>
 Q3_DEV void softmax_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, int i0, int i1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, half = (warp - SOFT0) >> 2;
@@ -385,7 +311,7 @@ Q3_DEV void softmax_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, in
     const float scale = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
     uint32_t g = 0, npair = 0;
     for (int k = i0, local = 0; k < i1; ++k, ++local) {
-        const Item it = item_of<KV4>(p, k);
+        const Item it = item_of(p, k);
         const int ir = row / G, hh = row % G;
         const bool valid = ir < R && ir < it.nrows;
         const int qp = it.pos0 + min(ir, it.nrows - 1);
@@ -447,15 +373,10 @@ Q3_DEV void softmax_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, in
                     const float p0 = ex2(fmaf(__uint_as_float(v[hq][2 * e]), scale, -m_used));
                     const float p1 = ex2(fmaf(__uint_as_float(v[hq][2 * e + 1]), scale, -m_used));
                     sum += p0 + p1;
-                    if (KV4) {
-                        const __half2 h2 = __floats2half2_rn(p0, p1);
-                        ph[e] = *reinterpret_cast<const uint32_t*>(&h2);
-                    } else {
-                        split_bf16(p0, p1, ph[e], pl[e]);
-                    }
+                    split_bf16(p0, p1, ph[e], pl[e]);
                 }
                 tmem_st_32x32b_x16(tl + T_S + b * 128 + c0 / 2 + 16 * hq, ph);
-                if (!KV4) tmem_st_32x32b_x16(tl + T_S + b * 128 + 64 + c0 / 2 + 16 * hq, pl);
+                tmem_st_32x32b_x16(tl + T_S + b * 128 + 64 + c0 / 2 + 16 * hq, pl);
             }
             tmem_st_wait();
             l += sum;
@@ -502,7 +423,6 @@ Q3_DEV void softmax_role(const PrefillAttnArgs& p, TcSmem& sm, uint32_t tmem, in
     }
 }
 
-template <bool KV4>
 __global__ void __launch_bounds__(THREADS, 1) prefill_attn_tc_kernel(const __grid_constant__ CUtensorMap tkv,
                                                                       const PrefillAttnArgs p)
 {
@@ -540,25 +460,17 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_attn_tc_kernel(const __gri
     const uint32_t tmem = sm.tmem;
 
     grid_dep_wait();
-    int i0, i1;
-    if (KV4) {
-        const int P = gridDim.x, n = *p.n_tiles_dev * p.n_kv, rows = n / P;
-        i0 = 0;
-        i1 = rows + (((rows & 1) ? P - 1 - (int)blockIdx.x : (int)blockIdx.x) < n % P ? 1 : 0);
-    } else {
-        i0 = p.sched_start[blockIdx.x];
-        i1 = p.sched_start[blockIdx.x + 1];
-    }
+    const int i0 = p.sched_start[blockIdx.x], i1 = p.sched_start[blockIdx.x + 1];
     if (warp == 0) {
-        if ((threadIdx.x & 31) == 0) mma_role<KV4>(p, sm, tmem, i0, i1);
+        if ((threadIdx.x & 31) == 0) mma_role(p, sm, tmem, i0, i1);
         __syncwarp();
     } else if (warp == 1 || warp == 2) {
-        if ((threadIdx.x & 31) == 0) load_role<KV4>(p, &tkv, sm, i0, i1, warp - 1);
+        if ((threadIdx.x & 31) == 0) load_role(p, &tkv, sm, i0, i1, warp - 1);
         __syncwarp();
     } else if (warp >= SOFT0 && warp < SOFT0 + NSOFT) {
-        softmax_role<KV4>(p, sm, tmem, i0, i1);
+        softmax_role(p, sm, tmem, i0, i1);
     } else if (warp >= QL0) {
-        q_role<KV4>(p, sm, tmem, i0, i1);
+        q_role(p, sm, tmem, i0, i1);
     }
     tc_fence_before();
     __syncthreads();
@@ -580,14 +492,11 @@ int prefill_tc_rows(int n_q, int n_kv)
 
 size_t prefill_tc_smem() { return SMEM_BYTES; }
 
-namespace {
-
-template <bool KV4>
-cudaError_t launch_tc(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid)
+cudaError_t launch_prefill_attention_tc(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid)
 {
     if (prefill_tc_rows(a.n_q, a.n_kv) < 1 || grid < 1) return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> attr_done{0};
-    if (cudaError_t e = allow_smem_per_device(prefill_attn_tc_kernel<KV4>, (int)SMEM_BYTES, attr_done)) return e;
+    if (cudaError_t e = allow_smem_per_device(prefill_attn_tc_kernel, (int)SMEM_BYTES, attr_done)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(THREADS);
@@ -599,19 +508,7 @@ cudaError_t launch_tc(const Launch& L, const CUtensorMap& tkv, const PrefillAttn
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (L.counter) ++*L.counter;
-    return cudaLaunchKernelEx(&cfg, prefill_attn_tc_kernel<KV4>, tkv, a);
-}
-
-}  // namespace
-
-cudaError_t launch_prefill_attention_tc(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid)
-{
-    return launch_tc<false>(L, tkv, a, grid);
-}
-
-cudaError_t launch_prefill_attention_kv4(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid)
-{
-    return launch_tc<true>(L, tkv, a, grid);
+    return cudaLaunchKernelEx(&cfg, prefill_attn_tc_kernel, tkv, a);
 }
 
 }  // namespace q3

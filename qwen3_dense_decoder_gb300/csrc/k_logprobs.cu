@@ -37,39 +37,6 @@ constexpr int NL = 4;                                    // 16-byte loads a lane
 constexpr int SLOTS = 40;                                // a lane's slots: V = 151,936 in f32 has 38 rounds
 constexpr float LOG2E = 1.4426950408889634f;
 
-Q3_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// pairs of floats: one instruction for two additions, products or both
-Q3_DEV uint64_t pair_of(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-Q3_DEV float2 halves_of(uint64_t p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
-Q3_DEV uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-Q3_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-Q3_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // ---------------------------------------------------------------- candidates
 // key: a number that orders as the value does, 1 for a NaN, 0 for no candidate
 struct Cand {
@@ -147,7 +114,7 @@ struct Sums {
 };
 // (s, t) moved to the maximum M >= a.m
 Q3_DEV void raise(Sums& a, float M) {
-    const float sc = a.m == M ? 1.f : a.m == -INFINITY ? 0.f : ex2((a.m - M) * LOG2E);
+    const float sc = a.m == M ? 1.f : a.m == -INFINITY ? 0.f : fast_ex2((a.m - M) * LOG2E);
     a.t = sc == 0.f ? 0.f : a.m == M ? a.t : (a.t + (a.m - M) * a.s) * sc;
     a.s *= sc;
     a.m = M;
@@ -166,7 +133,7 @@ Q3_DEV void add_values(Sums& a, const float (&v)[N], float cm) {
     if (cm > a.m) raise(a, cm);
     const float m = a.m == -INFINITY ? 0.f : a.m;        // -inf - -inf is not a number
     if (N == 1) {
-        const float d = v[0] - m, e = ex2(d * LOG2E);
+        const float d = v[0] - m, e = fast_ex2(d * LOG2E);
         a.s += e;
         a.t = fmaf(fmaxf(d, -1000.f), e, a.t);
         return;
@@ -177,7 +144,7 @@ Q3_DEV void add_values(Sums& a, const float (&v)[N], float cm) {
     for (int i = 0; i + 1 < N; i += 2) {
         const uint64_t d = add2(pair_of(v[i], v[i + 1]), nm);
         const float2 u = halves_of(mul2(d, l2e)), dd = halves_of(d);
-        const uint64_t e = pair_of(ex2(u.x), ex2(u.y));
+        const uint64_t e = pair_of(fast_ex2(u.x), fast_ex2(u.y));
         s = add2(s, e);
         // e is 0 from -127 on; -inf * 0 would not be
         t = fma2(pair_of(fmaxf(dd.x, -1000.f), fmaxf(dd.y, -1000.f)), e, t);

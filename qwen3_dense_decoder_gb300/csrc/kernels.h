@@ -240,12 +240,6 @@ struct PrefillAttnArgs {
     int n_blocks;
     __half* out;               // [T][n_q * 128] fp16
     int* status;
-    // tcgen05 kernel over the 4-bit cache's fp16 copy: the device's tile list
-    const int4* tiles;         // (first row, rows, its position, sequence), longest context first
-    const int* n_tiles_dev;
-    const int* seq_slot;       // sequence -> table, or null: the same number
-    int64_t q_stride;          // elements between rows of q
-    int by_seq;                // the copy's block of sequence i's block j is i max_blocks + j (else the pool's)
 };
 cudaError_t launch_prefill_attention(const Launch& L, const PrefillAttnArgs& a);
 // tcgen05 variant: query tiles of prefill_tc_rows() positions carry all query
@@ -253,7 +247,6 @@ cudaError_t launch_prefill_attention(const Launch& L, const PrefillAttnArgs& a);
 int prefill_tc_rows(int n_q, int n_kv);
 size_t prefill_tc_smem();
 cudaError_t launch_prefill_attention_tc(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid);
-cudaError_t launch_prefill_attention_kv4(const Launch& L, const CUtensorMap& tkv, const PrefillAttnArgs& a, int grid);
 
 // fused: every row is the single new token of its session; q/k norm, RoPE
 // and the K/V append of that token happen inside the attention kernel.
@@ -392,7 +385,8 @@ struct Kv4PrefillArgs {
     // what the expansion leaves for the attention kernel
     int rows_per_tile;
     int* n_tiles;
-    int4* tiles;               // at most T / rows_per_tile + ns
+    int4* tiles;               // (first row, rows, its position, sequence), longest context first; at most
+                               // T / rows_per_tile + ns
     __half* copy;              // [blocks][2][n_kv][32][128]
     int by_seq;                // block i max_blocks + j is sequence i's block j (else the pool's numbers)
     uint32_t magic;            // KV4_MAGIC, set by the launcher
@@ -400,6 +394,9 @@ struct Kv4PrefillArgs {
 // The sequences' tile list, sorted, and an fp16 copy of their blocks; rows
 // that attend nothing become zeros.
 cudaError_t launch_kv4_expand(const Launch& L, const Kv4PrefillArgs& a);
+// tkv: the copy as rows of 128; tq: q as (dimension, head, row)
+cudaError_t launch_kv4_prefill(const Launch& L, const CUtensorMap& tkv, const CUtensorMap& tq, const Kv4PrefillArgs& a, int grid);
+size_t kv4_prefill_smem();
 
 // ---------------------------------------------------------------- token log probabilities
 struct LogprobArgs {

@@ -110,6 +110,21 @@ bool tmap_kv16(CUtensorMap* m, const void* ptr, uint64_t rows)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query rows [T][n_q][128] fp16, stride elements apart, in boxes of R rows x G
+// heads x 64 dimensions.
+bool tmap_q16(CUtensorMap* m, const void* ptr, uint64_t T, uint64_t n_q, int64_t stride, uint32_t R, uint32_t G)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {128, n_q, T};
+    cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, G, R};
+    cuuint32_t elem[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 struct Q8Planes {
@@ -450,6 +465,9 @@ size_t kv_block_bytes(const q3_model* m)
 
 // ---------------------------------------------------------------- 4-bit cache prefill
 
+// positions of a work item of the prefill attention: two tiles of 128 / G
+int kv4_tile_rows(int n_q, int n_kv) { return 2 * (128 / (n_q / n_kv)); }
+
 // The prefill attention's workspace: a tile count and a spare status word, the
 // tile list, the fp16 copy of the blocks (numbered as in the pool, or by
 // sequence where that is fewer).
@@ -464,7 +482,7 @@ Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int
     w.by_seq = (int64_t)ns * max_blocks < n_blocks;
     w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
     w.tiles = 256;
-    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
+    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / kv4_tile_rows(n_q, n_kv) + ns), 1024);
     w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
     return w;
 }
@@ -474,24 +492,20 @@ cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int 
 {
     const Kv4Workspace w = kv4_workspace(a.ns, a.T, a.n_q, a.n_kv, a.max_blocks, a.n_blocks);
     int* head = reinterpret_cast<int*>(ws);
-    a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
+    a.rows_per_tile = kv4_tile_rows(a.n_q, a.n_kv);
     a.n_tiles = head;
     a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
     a.copy = reinterpret_cast<f16*>(ws + w.copy);
     a.by_seq = w.by_seq;
-    CUtensorMap map;
-    if (!tmap_kv16(&map, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32)) return cudaErrorInvalidValue;
+    const int G = a.n_q / a.n_kv;
+    CUtensorMap tkv, tq;
+    if (!tmap_kv16(&tkv, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32) ||
+        !tmap_q16(&tq, a.q, a.T, a.n_q, a.q_stride, a.rows_per_tile / 2, G))
+        return cudaErrorInvalidValue;
     if (cudaError_t e = launch_kv4_expand(L, a)) return e;
-    PrefillAttnArgs p{};
-    p.q = a.q; p.q_stride = a.q_stride;
-    p.T = a.T; p.n_q = a.n_q; p.n_kv = a.n_kv;
-    p.tables = a.tables; p.max_blocks = a.max_blocks; p.n_blocks = a.n_blocks;
-    p.seq_slot = a.seq_slot; p.by_seq = a.by_seq;
-    p.tiles = a.tiles; p.n_tiles_dev = a.n_tiles;
-    p.out = a.out;
-    p.status = a.status ? a.status : head + 1;       // a spare word nobody reads
+    if (!a.status) a.status = head + 1;              // a spare word nobody reads
     const Launch after{L.stream, true, L.counter};   // its setup overlaps the expansion
-    return launch_prefill_attention_kv4(after, map, p, n_sm);
+    return launch_kv4_prefill(after, tkv, tq, a, n_sm);
 }
 
 // ---------------------------------------------------------------- the round
@@ -1420,7 +1434,7 @@ int q3_model_create(const q3_config* cfg, const q3_weights* w, int max_round_tok
     // the tcgen05 prefill attention reads the BF16 cache, or the fp16 copy of the
     // 4-bit cache, through a tensor map; the Q8_0 cache takes the mma.sync kernel
     m->prefill_tc_ok = !m->kv_q8 && prefill_tc_rows(c.n_q_heads, c.n_kv_heads) > 0 &&
-                       prefill_tc_smem() <= (size_t)prop.sharedMemPerBlockOptin;
+                       std::max(prefill_tc_smem(), kv4_prefill_smem()) <= (size_t)prop.sharedMemPerBlockOptin;
     if (m->kv4 && !m->prefill_tc_ok) {
         delete m;
         return fail(Q3_ERR_INVALID_ARG, "config: the 4-bit cache needs the tcgen05 prefill attention");

@@ -301,6 +301,15 @@ Q3_DEV bool named_bar_and(int id, int threads, bool pred) {
     return r != 0;
 }
 
+// true in one lane of the (converged) warp
+Q3_DEV bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 Q3_DEV void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(tmap) : "memory");
 }

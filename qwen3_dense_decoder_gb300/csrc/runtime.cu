@@ -465,9 +465,6 @@ size_t kv_block_bytes(const q3_model* m)
 
 // ---------------------------------------------------------------- 4-bit cache prefill
 
-// positions of a work item of the prefill attention: two tiles of 128 / G
-int kv4_tile_rows(int n_q, int n_kv) { return 2 * (128 / (n_q / n_kv)); }
-
 // The prefill attention's workspace: a tile count and a spare status word, the
 // tile list, the fp16 copy of the blocks (numbered as in the pool, or by
 // sequence where that is fewer).
@@ -482,7 +479,7 @@ Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int
     w.by_seq = (int64_t)ns * max_blocks < n_blocks;
     w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
     w.tiles = 256;
-    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / kv4_tile_rows(n_q, n_kv) + ns), 1024);
+    w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
     w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
     return w;
 }
@@ -492,7 +489,7 @@ cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int 
 {
     const Kv4Workspace w = kv4_workspace(a.ns, a.T, a.n_q, a.n_kv, a.max_blocks, a.n_blocks);
     int* head = reinterpret_cast<int*>(ws);
-    a.rows_per_tile = kv4_tile_rows(a.n_q, a.n_kv);
+    a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
     a.n_tiles = head;
     a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
     a.copy = reinterpret_cast<f16*>(ws + w.copy);
@@ -500,7 +497,7 @@ cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int 
     const int G = a.n_q / a.n_kv;
     CUtensorMap tkv, tq;
     if (!tmap_kv16(&tkv, a.copy, (uint64_t)w.blocks * 2 * a.n_kv * 32) ||
-        !tmap_q16(&tq, a.q, a.T, a.n_q, a.q_stride, a.rows_per_tile / 2, G))
+        !tmap_q16(&tq, a.q, a.T, a.n_q, a.q_stride, a.rows_per_tile, G))
         return cudaErrorInvalidValue;
     if (cudaError_t e = launch_kv4_expand(L, a)) return e;
     if (!a.status) a.status = head + 1;              // a spare word nobody reads

@@ -656,12 +656,13 @@ cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a)
 // A prompt's attention reads every block once per query tile, so its blocks
 // are expanded once, into an fp16 copy that the tcgen05 kernel (k_attn_tc.cu)
 // fetches with TMA: 80 + 256 bytes a position and head against 512 flop a row
-// and position.  A warp expands one tile: 4-byte code words in, 16-byte words
-// out, both coalesced.  Places at or past the sequence's end hold whatever
+// and position.  A warp expands half a tile at a time, all its loads first: 4-byte
+// code words in, 16-byte words out, both coalesced.  Places at or past the sequence's end hold whatever
 // the pool holds, made finite (their weights are zero).
 //
-// CTA 0 first lists the query tiles, longest context first: a counting sort by
-// context in 1,024 classes (order within a class does not matter).
+// CTA 0 lists the query tiles meanwhile.  Enough of them, longest context first: a counting
+// sort by context in 1,024 classes (order within a class does not matter).  Fewer
+// stay in order, with the cost before each, for the attention kernel to cut.
 constexpr int XT = 256;
 constexpr int CLASSES = 1024;
 
@@ -683,55 +684,123 @@ Q3_DEV Seq seq_of(const Kv4PrefillArgs& a, int i, bool& bad) {
     return s;
 }
 
+// Tiles in order and the cost before each (one warp)
+Q3_DEV void plan_cuts(const Kv4PrefillArgs& a) {
+    const int lane = threadIdx.x & 31;
+    int n = 0, cost = 0;
+    for (int i0 = 0; i0 < a.ns; i0 += 32) {
+        bool b;
+        Seq mine{};
+        if (i0 + lane < a.ns) mine = seq_of(a, i0 + lane, b);
+        for (unsigned some = __ballot_sync(0xffffffffu, mine.rows > 0); some; some &= some - 1) {
+            const int from = __ffs(some) - 1;
+            const int row0 = __shfl_sync(0xffffffffu, mine.row0, from), rows = __shfl_sync(0xffffffffu, mine.rows, from),
+                      pos0 = __shfl_sync(0xffffffffu, mine.pos0, from), slot = __shfl_sync(0xffffffffu, mine.slot, from);
+            for (int k0 = 0; k0 < rows; k0 += 32 * a.rows_per_tile) {
+                const int k = k0 + lane * a.rows_per_tile, r = min(a.rows_per_tile, rows - k);
+                const int own = r > 0 ? (pos0 + k + r - 1) / 64 + 1 + KV4_TILE_COST : 0;
+                int x = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (r > 0) {
+                    a.tiles[n + lane] = make_int4(row0 + k, slot, (pos0 + k) | ((r - 1) << 25), i0 + from);
+                    a.starts[n + lane] = cost + x - own;
+                }
+                n += __popc(__ballot_sync(0xffffffffu, r > 0));
+                cost += __shfl_sync(0xffffffffu, x, 31);
+            }
+        }
+    }
+    if (lane == 0) {
+        a.n_tiles[0] = n;
+        a.n_tiles[2] = cost;
+    }
+}
+
 Q3_DEV void plan_tiles(const Kv4PrefillArgs& a) {
-    __shared__ int s_most, s_at[CLASSES];
+    __shared__ int s_most;
+    __shared__ alignas(16) int s_at[CLASSES];
+    __shared__ unsigned long long s_tiles, s_cost;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_most = 0;
+    if (threadIdx.x == 0) { s_most = 0; s_tiles = 0; s_cost = 0; }
     for (int i = threadIdx.x; i < CLASSES; i += XT) s_at[i] = 0;
+    for (int i = threadIdx.x; i < 4 * a.ctas; i += XT) a.come[i] = 0;
     __syncthreads();
     bool bad;
     for (int i = threadIdx.x; i < a.ns; i += XT) {
         const Seq s = seq_of(a, i, bad);
         if (bad) report(a.status, Q3_STATUS_BLOCK_RANGE);
-        if (s.rows) atomicMax(&s_most, s.pos0 + s.rows);
+        if (!s.rows) continue;
+        atomicMax(&s_most, s.pos0 + s.rows);
+        const int n = (s.rows - 1) / a.rows_per_tile + 1;
+        atomicAdd(&s_tiles, (unsigned long long)n);
+        atomicAdd(&s_cost, (unsigned long long)n * ((s.pos0 + (s.rows + a.rows_per_tile) / 2) / 64 + 1 + KV4_TILE_COST));
     }
     __syncthreads();
-    const float per = (float)CLASSES / (float)(s_most + 1);
-    auto each = [&](auto&& f) {                          // a warp a sequence, a lane a tile
-        for (int i = warp; i < a.ns; i += XT / 32) {
-            bool b;
-            const Seq s = seq_of(a, i, b);
-            for (int k = lane * a.rows_per_tile; k < s.rows; k += 32 * a.rows_per_tile) {
-                const int rows = min(a.rows_per_tile, s.rows - k);
-                const int last = s.pos0 + k + rows - 1;
-                f(CLASSES - 1 - min((int)((float)last * per), CLASSES - 1), make_int4(s.row0 + k, rows, s.pos0 + k, i));
+    // rows of more than one sequence: what does not fit the list is left out
+    if (threadIdx.x == 0 && s_tiles > (unsigned long long)a.max_tiles) report(a.status, Q3_STATUS_BLOCK_RANGE);
+    // cut where the longest CTA of whole tiles would take longer than a share and a join
+    const unsigned long long items = s_tiles * a.n_kv, cost = s_cost * a.n_kv;
+    const unsigned long long whole = items < KV4_CUT * a.ctas ? max((unsigned long long)(s_most - 1) / 64 + 1 + KV4_TILE_COST,
+                                                                    (items + a.ctas - 1) / a.ctas * cost / max(items, 1ull))
+                                                              : 0;
+    if (s_tiles <= (unsigned long long)a.max_tiles && whole > max(cost / a.ctas, (unsigned long long)KV4_MIN_SHARE) + KV4_JOIN_COST) {
+        if (warp == 0) plan_cuts(a);
+    } else {
+        const float per = (float)CLASSES / (float)(s_most + 1);
+        auto each = [&](auto&& f) {                      // a warp a sequence, a lane a tile
+            for (int i = warp; i < a.ns; i += XT / 32) {
+                bool b;
+                const Seq s = seq_of(a, i, b);
+                for (int k = lane * a.rows_per_tile; k < s.rows; k += 32 * a.rows_per_tile) {
+                    const int rows = min(a.rows_per_tile, s.rows - k);
+                    const int last = s.pos0 + k + rows - 1;
+                    f(CLASSES - 1 - min((int)((float)last * per), CLASSES - 1), make_int4(s.row0 + k, s.slot, (s.pos0 + k) | ((rows - 1) << 25), i));
+                }
             }
-        }
-    };
-    each([&](int c, const int4&) { atomicAdd(&s_at[c], 1); });
-    __syncthreads();
-    if (warp == 0) {                                     // counts to first places
-        int base = 0;
-        for (int i = lane; i < CLASSES; i += 32) {
-            const int n = s_at[i];
-            int x = n;
+        };
+        each([&](int c, const int4&) { atomicAdd(&s_at[c], 1); });
+        __syncthreads();
+        // counts to first places: four classes a thread
+        static_assert(CLASSES == 4 * XT, "classes");
+        __shared__ int s_warp[XT / 32];
+        int4 n = *reinterpret_cast<const int4*>(s_at + 4 * threadIdx.x);
+        const int own = n.x + n.y + n.z + n.w;
+        int x = own;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            s_at[i] = base + x - n;
-            base += __shfl_sync(0xffffffffu, x, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
-        if (lane == 0) *a.n_tiles = base;
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        x -= own;
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < XT / 32; ++i) {
+            if (i < warp) x += s_warp[i];
+            all += s_warp[i];
+        }
+        n = make_int4(x, x + n.x, x + n.x + n.y, x + n.x + n.y + n.z);
+        *reinterpret_cast<int4*>(s_at + 4 * threadIdx.x) = n;
+        if (threadIdx.x == 0) {
+            a.n_tiles[0] = min(all, a.max_tiles);
+            a.n_tiles[2] = 0;
+        }
+        __syncthreads();
+        each([&](int c, const int4& t) {
+            const int at = atomicAdd(&s_at[c], 1);
+            if (at < a.max_tiles) a.tiles[at] = t;
+        });
     }
-    __syncthreads();
-    each([&](int c, const int4& t) { a.tiles[atomicAdd(&s_at[c], 1)] = t; });
     // rows that attend nothing
-    for (int i = 0; i < a.ns; ++i) {
+    for (int i = warp; i < a.ns; i += XT / 32) {
         const Seq s = seq_of(a, i, bad);
         uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)(s.row0 - s.skip) * a.n_q * D);
-        for (int64_t k = threadIdx.x; k < (int64_t)s.skip * a.n_q * (D / 8); k += XT) dst[k] = make_uint4(0, 0, 0, 0);
+        for (int64_t k = lane; k < (int64_t)s.skip * a.n_q * (D / 8); k += 32) dst[k] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -742,71 +811,98 @@ Q3_DEV uint32_t finite_pair(uint32_t v) {
     return v;
 }
 
+// 16 positions of a tile: codes and parameters at src, fp16 rows at dst; places from
+// n_pos on made finite
+Q3_DEV void expand_k(const uint8_t* codes, const uint8_t* params, __half* dst, int n_pos, uint32_t magic, int lane) {
+    const int c = lane & 15, p0 = lane >> 4;             // two positions a step, eight dimensions a lane
+    uint32_t w[8], sb[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + (2 * k + p0) * 64) + c);
+        sb[k] = __ldg(reinterpret_cast<const uint32_t*>(params + (2 * k + p0) * 16) + (c >> 2));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const __half2 sc = __low2half2(as_h2(sb[k])), bi = __high2half2(as_h2(sb[k]));
+        const uint32_t v0 = kv4_pair<0>(w[k], sc, bi, magic), v1 = kv4_pair<1>(w[k], sc, bi, magic), v2 = kv4_pair<2>(w[k], sc, bi, magic),
+                       v3 = kv4_pair<3>(w[k], sc, bi, magic);
+        uint4 o = make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632),
+                             __byte_perm(v2, v3, 0x7632));
+        if (2 * k + p0 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+        *reinterpret_cast<uint4*>(dst + (2 * k + p0) * D + c * 8) = o;
+    }
+}
+Q3_DEV void expand_v(const uint8_t* codes, const uint8_t* params, __half* dst, int n_pos, uint32_t magic, int lane) {
+    const int gr = (lane & 15) >> 2, m = lane & 3, pr0 = lane >> 4;      // two position pairs a step
+    uint32_t w0[4], w1[4];
+    uint2 sb[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int pr = 2 * k + pr0;
+        w0[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + pr * 128 + 2 * m * 16) + gr);
+        w1[k] = __ldg(reinterpret_cast<const uint32_t*>(codes + pr * 128 + (2 * m + 1) * 16) + gr);
+        sb[k] = __ldg(reinterpret_cast<const uint2*>(params + pr * 32) + gr);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int pr = 2 * k + pr0;
+        const __half2 sc = as_h2(sb[k].x), bi = as_h2(sb[k].y);
+        const uint32_t p0 = kv4_pair<0>(w0[k], sc, bi, magic), p1 = kv4_pair<1>(w0[k], sc, bi, magic), p2 = kv4_pair<2>(w0[k], sc, bi, magic),
+                       p3 = kv4_pair<3>(w0[k], sc, bi, magic);
+        const uint32_t r0 = kv4_pair<0>(w1[k], sc, bi, magic), r1 = kv4_pair<1>(w1[k], sc, bi, magic), r2 = kv4_pair<2>(w1[k], sc, bi, magic),
+                       r3 = kv4_pair<3>(w1[k], sc, bi, magic);
+        uint4 e = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(r0, r1, 0x5410), __byte_perm(r2, r3, 0x5410));
+        uint4 o = make_uint4(__byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632), __byte_perm(r0, r1, 0x7632), __byte_perm(r2, r3, 0x7632));
+        if (2 * pr >= n_pos) e = make_uint4(finite_pair(e.x), finite_pair(e.y), finite_pair(e.z), finite_pair(e.w));
+        if (2 * pr + 1 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+        uint4* to = reinterpret_cast<uint4*>(dst + 2 * pr * D + 32 * gr + 8 * m);
+        to[0] = e;
+        to[D / 8] = o;
+    }
+}
+
 __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
 {
     grid_dep_launch();
     grid_dep_wait();
-    if (blockIdx.x == 0) plan_tiles(a);
+    if (blockIdx.x == 0) {
+        plan_tiles(a);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t magic = a.magic;
-    const int64_t step = (int64_t)gridDim.x * (XT / 32);
-    int64_t u = (int64_t)blockIdx.x * (XT / 32) + warp;      // unit: (block, K or V, KV head) of the sequences in turn
+    const int64_t step = (int64_t)(gridDim.x - 1) * (XT / 32);
+    int64_t u = (int64_t)(blockIdx.x - 1) * (XT / 32) + warp;    // half a tile: (block, K or V, KV head, half) of the sequences in turn
     int64_t base = 0;
-    for (int i = 0; i < a.ns; ++i) {
+    const int units = 4 * a.n_kv;
+    for (int i0 = 0; i0 < a.ns; i0 += 32) {
         bool bad;
-        const Seq s = seq_of(a, i, bad);
-        if (!s.rows) continue;
-        const int end = s.pos0 + s.rows, units = 2 * a.n_kv;
-        const int64_t n = (int64_t)((end + 31) / 32) * units;
-        for (; u < base + n; u += step) {
-            const int j = (int)((u - base) / units), part = (int)((u - base) % units);
-            const int phys = a.tables[(size_t)s.slot * a.max_blocks + j];
-            if (phys < 0 || phys >= a.n_blocks) {            // the attention kernel leaves its places zero
+        Seq mine{};
+        if (i0 + lane < a.ns) mine = seq_of(a, i0 + lane, bad);
+        const int64_t own = mine.rows ? (int64_t)((mine.pos0 + mine.rows + 31) / 32) * units : 0;
+        int64_t upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+        for (; u < base + all; u += step) {
+            const int from = __popc(__ballot_sync(0xffffffffu, upto <= u - base));
+            const int64_t rel = u - base - __shfl_sync(0xffffffffu, upto - own, from);
+            const int slot = __shfl_sync(0xffffffffu, mine.slot, from), end = __shfl_sync(0xffffffffu, mine.pos0 + mine.rows, from);
+            const int j = (int)(rel / units), part = (int)(rel - (int64_t)j * units) >> 1, half = (int)(rel & 1);
+            const int phys = a.tables[(size_t)slot * a.max_blocks + j];
+            if (phys < 0 || phys >= a.n_blocks) {                // the attention kernel leaves its places zero
                 if (lane == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
                 continue;
             }
-            const uint8_t* src = a.kv + ((size_t)phys * units + part) * KV4_TILE;
-            __half* dst = a.copy + ((size_t)(a.by_seq ? i * a.max_blocks + j : phys) * units + part) * (32 * D);
-            const int n_pos = min(32, end - 32 * j);
-            if (part < a.n_kv) {
-#pragma unroll 4
-                for (int k = 0; k < 16; ++k) {               // two positions a step, eight dimensions a lane
-                    const int p = 2 * k + (lane >> 4), c = lane & 15;
-                    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(src + p * 64) + c);
-                    const __half2 sb = *reinterpret_cast<const __half2*>(src + KV4_CODES + p * 16 + (c >> 2) * 4);
-                    const __half2 sc = __low2half2(sb), bi = __high2half2(sb);
-                    const uint32_t p0 = kv4_pair<0>(w, sc, bi, magic), p1 = kv4_pair<1>(w, sc, bi, magic), p2 = kv4_pair<2>(w, sc, bi, magic),
-                                   p3 = kv4_pair<3>(w, sc, bi, magic);
-                    uint4 o = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(p0, p1, 0x7632),
-                                         __byte_perm(p2, p3, 0x7632));
-                    if (p >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
-                    *reinterpret_cast<uint4*>(dst + p * D + c * 8) = o;
-                }
-            } else {
-#pragma unroll 4
-                for (int k = 0; k < 8; ++k) {                // two position pairs a step
-                    const int pr = 2 * k + (lane >> 4), gr = (lane & 15) >> 2, m = lane & 3;
-                    const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t*>(src + pr * 128 + 2 * m * 16) + gr);
-                    const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t*>(src + pr * 128 + (2 * m + 1) * 16) + gr);
-                    const uint2 sb = *reinterpret_cast<const uint2*>(src + KV4_CODES + pr * 32 + gr * 8);
-                    const __half2 sc = as_h2(sb.x), bi = as_h2(sb.y);
-                    const uint32_t p0 = kv4_pair<0>(w0, sc, bi, magic), p1 = kv4_pair<1>(w0, sc, bi, magic), p2 = kv4_pair<2>(w0, sc, bi, magic),
-                                   p3 = kv4_pair<3>(w0, sc, bi, magic);
-                    const uint32_t r0 = kv4_pair<0>(w1, sc, bi, magic), r1 = kv4_pair<1>(w1, sc, bi, magic), r2 = kv4_pair<2>(w1, sc, bi, magic),
-                                   r3 = kv4_pair<3>(w1, sc, bi, magic);
-                    uint4 e = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(r0, r1, 0x5410),
-                                         __byte_perm(r2, r3, 0x5410));
-                    uint4 o = make_uint4(__byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632), __byte_perm(r0, r1, 0x7632),
-                                         __byte_perm(r2, r3, 0x7632));
-                    if (2 * pr >= n_pos) e = make_uint4(finite_pair(e.x), finite_pair(e.y), finite_pair(e.z), finite_pair(e.w));
-                    if (2 * pr + 1 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
-                    uint4* to = reinterpret_cast<uint4*>(dst + 2 * pr * D + 32 * gr + 8 * m);
-                    to[0] = e;
-                    to[D / 8] = o;
-                }
-            }
+            const uint8_t* src = a.kv + ((size_t)phys * 2 * a.n_kv + part) * KV4_TILE;
+            __half* dst = a.copy + ((size_t)(a.by_seq ? (i0 + from) * a.max_blocks + j : phys) * 2 * a.n_kv + part) * (32 * D) + half * 16 * D;
+            const int n_pos = end - 32 * j - 16 * half;
+            if (part < a.n_kv) expand_k(src + half * 1024, src + KV4_CODES + half * 256, dst, n_pos, a.magic, lane);
+            else expand_v(src + half * 1024, src + KV4_CODES + half * 256, dst, n_pos, a.magic, lane);
         }
-        base += n;
+        base += all;
     }
 }
 

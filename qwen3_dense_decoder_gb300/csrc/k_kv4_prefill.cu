@@ -22,8 +22,14 @@
 // are raised lazily: O and the sum are rescaled only when one grows by more than
 // 2^8.
 //
-// Roles (one CTA per SM, items dealt from the list; the next item's Q, K and
-// scores are under way while an item ends):
+// Three items a CTA or more are dealt whole, longest first.  Fewer are cut: the
+// items in a row, their steps are shared out evenly, a CTA's share may begin and
+// end inside an item, and a cut item's pieces leave maximum, sum and FP32 output in
+// the workspace, where the warp that finishes a row range last joins them in order.
+// (512 rows after 10,240 positions, 40/8 heads, 176 items: @CUT@.)
+//
+// Roles (one CTA per SM; the next item's Q, K and scores are under way while an
+// item ends):
 //   warps 0..3, 4..7  softmax of half 0 and of half 1 (warp w: TMEM lanes 32 (w % 4)
 //                     .. + 32); half 0's also join the halves and write the output
 //   warps 8, 9        issue the score products and the PV products
@@ -50,6 +56,7 @@ constexpr int S_WARP = 8, PV_WARP = 9, K_WARP = 10;        // V: K_WARP + 1
 constexpr int THREADS = 12 * 32;
 constexpr uint32_t T_S = 0, T_O = 256;
 constexpr float LAZY = 8.0f;
+constexpr int PART = (int)(KV4_PART_BYTES / 16);
 
 struct alignas(1024) Smem {
     uint8_t q[2][2 * Q_ATOM];
@@ -60,7 +67,8 @@ struct alignas(1024) Smem {
     uint64_t k_load[NS], v_load[NS], s_full[NS], p_full[NS], pv_done[NS];
     uint64_t q_full[2], q_free[2];           // by item
     uint64_t b_done, o_free, drain[2];
-    float2 ml[128];                          // B's maxima and sums
+    float2 ml[128];                          // half 1's maxima and sums
+    int2 cut[2];                             // where this CTA's share begins and ends: item, step
     uint32_t tmem;
     int abort;
 };
@@ -85,22 +93,70 @@ Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, Smem& sm, int* status) {
     }
 }
 
-struct Item {
-    int row0, rows, pos0, seq, slot, kvh;
-    int steps;                               // of 64 positions
+// A CTA's work: n items or pieces of items
+struct Work {
+    int n, first, s0, s1;                    // the first piece's first step, the last one's end (0: the item's)
+    int share;                               // cost between cuts; 0: whole items
 };
 
-// Item k of this CTA: tile i of the list for KV head h is number i n_kv + h,
-// dealt in rows of gridDim.x, every other row backwards.
-Q3_DEV Item item_of(const Kv4PrefillArgs& p, int k) {
-    const int P = gridDim.x, n = k * P + ((k & 1) ? P - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    const int4 t = p.tiles[n / p.n_kv];
+struct Item {
+    int row0, rows, pos0, seq, slot, kvh;
+    int t0, t1, steps;                       // steps t0 .. t1 of the item's
+    int tile;
+};
+
+// Item k of this CTA.  Number i n_kv + h is tile i of the list for KV head h, dealt in
+// rows of gridDim.x, every other row backwards; of cut items, number h n_tiles + i.
+Q3_DEV Item item_of(const Kv4PrefillArgs& p, const Work& w, int k) {
     Item it;
-    it.kvh = n % p.n_kv;
-    it.row0 = t.x; it.rows = t.y; it.pos0 = t.z; it.seq = t.w;
-    it.slot = p.seq_slot ? p.seq_slot[t.w] : t.w;
-    it.steps = (t.z + t.y - 1) / BN + 1;
+    if (w.share) {
+        const int n = w.first + k, nt = *p.n_tiles;
+        it.kvh = n / nt;
+        it.tile = n - it.kvh * nt;
+    } else {
+        const int P = gridDim.x, n = k * P + ((k & 1) ? P - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        it.tile = n / p.n_kv;
+        it.kvh = n - it.tile * p.n_kv;
+    }
+    const int4 t = p.tiles[it.tile];
+    it.row0 = t.x; it.slot = t.y; it.pos0 = t.z & 0x1ffffff; it.rows = (int)((unsigned)t.z >> 25) + 1; it.seq = t.w;
+    it.steps = (it.pos0 + it.rows - 1) / BN + 1;
+    it.t0 = w.share && k == 0 ? w.s0 : 0;
+    it.t1 = w.share && k == w.n - 1 && w.s1 ? w.s1 : it.steps;
     return it;
+}
+
+// This CTA's work (all threads)
+Q3_DEV Work work_of(const Kv4PrefillArgs& p, Smem& sm) {
+    const int P = gridDim.x, c = blockIdx.x, nt = p.n_tiles[0], cost = p.n_tiles[2];
+    Work w{};
+    if (cost == 0) {
+        const int n = nt * p.n_kv, full = n / P;
+        w.n = full + (((full & 1) ? P - 1 - c : c) < n % P ? 1 : 0);
+        return w;
+    }
+    const int all = cost * p.n_kv;
+    w.share = max((all + P - 1) / P, KV4_MIN_SHARE);
+    if (c * w.share >= all) return w;
+    // cut c is at cost c share; one within KV4_MIN_PIECE steps of an item's end moves there
+    const int x[2] = {c * w.share, min((c + 1) * w.share, all)};
+    for (int i = threadIdx.x; i < nt; i += THREADS) {
+        const int start = p.starts[i], end = i + 1 < nt ? p.starts[i + 1] : cost;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = x[e] / cost, s = x[e] - h * cost - start;
+            if (s >= 0 && s < end - start) {
+                const int n = h * nt + i;
+                sm.cut[e] = s < KV4_MIN_PIECE ? make_int2(n, 0)
+                                              : s > end - start - KV4_TILE_COST - KV4_MIN_PIECE ? make_int2(n + 1, 0) : make_int2(n, s);
+            }
+        }
+    }
+    __syncthreads();
+    const int2 lo = sm.cut[0], hi = sm.cut[1];
+    w.first = lo.x; w.s0 = lo.y; w.s1 = hi.y;
+    w.n = hi.x - lo.x + (hi.y > 0 ? 1 : 0);
+    return w;
 }
 
 // The phase of step n's slot, and the one before
@@ -110,15 +166,18 @@ Q3_DEV uint32_t phase_before(uint32_t n) { return ((n >> 2) & 1) ^ 1; }
 // ---------------------------------------------------------------- MMA issuers
 // A whole warp walks the loop and one lane issues, so descriptors and addresses
 // stay in uniform registers.
-Q3_DEV int steps_of(const Kv4PrefillArgs& p, int k) { return __shfl_sync(0xffffffffu, item_of(p, k).steps, 0); }
+Q3_DEV int steps_of(const Kv4PrefillArgs& p, const Work& w, int k) {
+    const Item it = item_of(p, w, k);
+    return __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
+}
 
-Q3_DEV void scores_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n_items, int* status) {
+Q3_DEV void scores_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const Work& w, int* status) {
     const bool leader = elect_one();
     const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0])), k0 = smem_desc_sw128(smem_u32(sm.k[0]));
     uint32_t n = 0;
     bool ok = true;
-    for (int k = 0; k < n_items && ok; ++k) {
-        const int steps = steps_of(p, k);
+    for (int k = 0; k < w.n && ok; ++k) {
+        const int steps = steps_of(p, w, k);
         const uint64_t qd = q0 + (uint32_t)(k & 1) * (2 * Q_ATOM >> 4);
         if (!(ok = wait_bar(&sm.q_full[k & 1], (k >> 1) & 1, sm, status))) break;
         for (int t = 0; t < steps; ++t, ++n) {
@@ -144,13 +203,13 @@ Q3_DEV void scores_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n_
     mbar_wait(&sm.drain[0], 0, status);
 }
 
-Q3_DEV void product_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n_items, int* status) {
+Q3_DEV void product_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const Work& w, int* status) {
     const bool leader = elect_one();
     const uint64_t v0 = smem_desc_sw128_mn(smem_u32(sm.v[0]), KV_ATOM);
     uint32_t n = 0;
     bool ok = true;
-    for (int k = 0; k < n_items && ok; ++k) {
-        const int steps = steps_of(p, k);
+    for (int k = 0; k < w.n && ok; ++k) {
+        const int steps = steps_of(p, w, k);
         // the last item's outputs are read out before this one's first products
         if (k > 0 && !(ok = wait_bar(&sm.o_free, (k - 1) & 1, sm, status))) break;
         for (int t = 0; t < steps; ++t, ++n) {
@@ -176,14 +235,14 @@ Q3_DEV void product_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n
 // dimensions: row r of the tile is position r / G, head r % G.  Rows past the
 // sequence read another's (or zeros past T); the last 128 - R G rows of a tile
 // are never written.  What they give is not stored.
-Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUtensorMap* tq, Smem& sm, int n_items, int which,
+Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUtensorMap* tq, Smem& sm, const Work& w, int which,
                       int* status) {
     const int G = p.n_q / p.n_kv;
     uint64_t* ld = which ? sm.v_load : sm.k_load;
     uint64_t* fr = which ? sm.pv_done : sm.s_full;
     uint32_t n = 0;
-    for (int k = 0; k < n_items; ++k) {
-        const Item it = item_of(p, k);
+    for (int k = 0; k < w.n; ++k) {
+        const Item it = item_of(p, w, k);
         const int* table = p.tables + (size_t)it.slot * p.max_blocks;
         const int last = it.pos0 + it.rows - 1;
         if (!which) {
@@ -193,7 +252,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
 #pragma unroll
             for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[b] + h * Q_ATOM, tq, &sm.q_full[b], 64 * h, it.kvh * G, it.row0);
         }
-        for (int t = 0; t < it.steps; ++t, ++n) {
+        for (int t = it.t0; t < it.t1; ++t, ++n) {
             const uint32_t slot = n & 3;
             int row[BN / 32];
 #pragma unroll
@@ -220,7 +279,58 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
 }
 
 // ---------------------------------------------------------------- softmax + output
-Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n_items, int half, int* status) {
+Q3_DEV void store32(__half* dst, const float (&v)[32], bool& bad) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint4 w;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            __half2 h2;
+            h2.x = to_f16(v[8 * e + 2 * f], bad);
+            h2.y = to_f16(v[8 * e + 2 * f + 1], bad);
+            (&w.x)[f] = *reinterpret_cast<uint32_t*>(&h2);
+        }
+        *reinterpret_cast<uint4*>(dst + e * 8) = w;
+    }
+}
+
+// A cut item's pieces lie with consecutive CTAs: the first in its CTA's second
+// place, the others in the first.  This warp has stored its rows of one; the last
+// to come joins its rows of all, in the pieces' order.
+Q3_DEV void join_pieces(const Kv4PrefillArgs& p, const Work& w, const Item& it, int quad, int row, bool valid, __half* dst, bool& bad) {
+    const int start = it.kvh * p.n_tiles[2] + p.starts[it.tile];
+    const int c1 = (start + KV4_MIN_PIECE + w.share - 1) / w.share, c2 = (start + it.steps - KV4_MIN_PIECE) / w.share;
+    const int pieces = c2 - c1 + 2;
+    __threadfence();
+    __syncwarp();
+    int come = 0;
+    if ((threadIdx.x & 31) == 0) come = atomicAdd(p.come + 4 * (c1 - 1) + quad, 1);
+    if (__shfl_sync(0xffffffffu, come, 0) != pieces - 1) return;
+    __threadfence();
+    auto piece = [&](int j) { return p.parts + (size_t)(2 * (c1 - 1 + j) + (j ? 0 : 1)) * PART; };
+    auto ml = [&](int j) { return __ldcg(reinterpret_cast<const float2*>(piece(j) + 32 * 128) + row); };
+    float M = -INFINITY, L = 0.f;
+    for (int j = 0; j < pieces; ++j) M = fmaxf(M, ml(j).x);
+    if (!valid) return;                                  // the others have seen their own position
+    for (int j = 0; j < pieces; ++j) L += fast_ex2(ml(j).x - M) * ml(j).y;
+    const float inv = 1.f / L;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float v[32] = {};
+        for (int j = 0; j < pieces; ++j) {
+            const float f = fast_ex2(ml(j).x - M) * inv;
+            const float4* src = piece(j) + 8 * c * 128 + row;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 x = __ldcg(src + e * 128);
+                v[4 * e] += f * x.x; v[4 * e + 1] += f * x.y; v[4 * e + 2] += f * x.z; v[4 * e + 3] += f * x.w;
+            }
+        }
+        store32(dst + 32 * c, v, bad);
+    }
+}
+
+Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const Work& w, int half, int* status) {
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const int G = p.n_q / p.n_kv;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -228,13 +338,13 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n
     const float scale = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
     const int ir = row / G, hh = row % G;
     uint32_t n0 = 0;                                     // the item's first step
-    for (int k = 0; k < n_items; ++k) {
-        const Item it = item_of(p, k);
+    for (int k = 0; k < w.n; ++k) {
+        const Item it = item_of(p, w, k);
         const int qp = it.pos0 + min(ir, it.rows - 1);
-        const int first = (half ^ (int)n0) & 1;          // of this half's steps in the item
+        const int first = it.t0 + ((half ^ (int)n0) & 1); // of this half's steps in the item
         float m = -INFINITY, l = 0.f;
-        for (int t = first; t < it.steps; t += 2) {
-            const uint32_t n = n0 + t, slot = n & 3, ts = s0 + (slot >> 1) * 64;
+        for (int t = first; t < it.t1; t += 2) {
+            const uint32_t n = n0 + (t - it.t0), slot = n & 3, ts = s0 + (slot >> 1) * 64;
             if (!wait_bar(&sm.s_full[slot], phase(n), sm, status)) return;
             tc_fence_after();
             uint32_t v[2][32];
@@ -297,7 +407,7 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n
             l += a.x + a.y;
         }
         // a half's O is complete once the product of its last step is
-        const uint32_t end = n0 + it.steps;
+        const uint32_t end = n0 + (it.t1 - it.t0);
         n0 = end;
         if (half) {
             // half 0 has read the last item's (so this half is never two items ahead)
@@ -307,16 +417,19 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n
             continue;
         }
         if (!wait_bar(&sm.b_done, k & 1, sm, status)) return;
-        for (int back = 1; back <= min(it.steps, 2); ++back)
+        for (int back = 1; back <= min(it.t1 - it.t0, 2); ++back)
             if (!wait_bar(&sm.pv_done[(end - back) & 3], phase(end - back), sm, status)) return;
         tc_fence_after();
         const float2 other = sm.ml[row];
         const float M = fmaxf(m, other.x);
         const float w0 = m == -INFINITY ? 0.f : fast_ex2(m - M), w1 = other.x == -INFINITY ? 0.f : fast_ex2(other.x - M);
-        const float inv = 1.0f / (l * w0 + other.y * w1);
+        const float sum = l * w0 + other.y * w1;
+        const bool whole = it.t1 - it.t0 == it.steps;
+        const float r0 = whole ? w0 / sum : w0, r1 = whole ? w1 / sum : w1;
         const bool valid = ir < it.rows && ir < p.rows_per_tile;
         bool bad = false;
         __half* dst = p.out + ((size_t)(it.row0 + min(ir, it.rows - 1)) * p.n_q + it.kvh * G + hh) * D;
+        float4* part = p.parts + (size_t)(2 * blockIdx.x + (it.t0 ? 0 : 1)) * PART;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             uint32_t o[32], ob[32];
@@ -325,29 +438,26 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, int n
             tmem_ld_wait();
             // a half that has no step in this item, or a row none of its positions,
             // holds another item's output, or nothing
+            float v[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float x = w0 == 0.f ? 0.f : __uint_as_float(o[e]) * w0, y = w1 == 0.f ? 0.f : __uint_as_float(ob[e]) * w1;
-                o[e] = __float_as_uint((x + y) * inv);
+                const float x = w0 == 0.f ? 0.f : __uint_as_float(o[e]) * r0, y = w1 == 0.f ? 0.f : __uint_as_float(ob[e]) * r1;
+                v[e] = x + y;
             }
-            if (valid) {
+            if (!whole) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 w;
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        __half2 h2;
-                        h2.x = to_f16(__uint_as_float(o[8 * e + 2 * f]), bad);
-                        h2.y = to_f16(__uint_as_float(o[8 * e + 2 * f + 1]), bad);
-                        (&w.x)[f] = *reinterpret_cast<uint32_t*>(&h2);
-                    }
-                    *reinterpret_cast<uint4*>(dst + c * 32 + e * 8) = w;
-                }
+                for (int e = 0; e < 8; ++e) part[(8 * c + e) * 128 + row] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else if (valid) {
+                store32(dst + 32 * c, v, bad);
             }
         }
-        if (bad) set_status(status, Q3_STATUS_F16_RANGE);
         tc_fence_before();
         mbar_arrive(&sm.o_free);
+        if (!whole) {
+            reinterpret_cast<float2*>(part + 32 * 128)[row] = make_float2(M, sum);
+            join_pieces(p, w, it, quad, row, valid, dst, bad);
+        }
+        if (bad) set_status(status, Q3_STATUS_F16_RANGE);
     }
 }
 
@@ -387,12 +497,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prefill_kernel(const __grid_co
     const uint32_t tmem = sm.tmem;
 
     grid_dep_wait();
-    const int P = gridDim.x, n = *p.n_tiles * p.n_kv, full = n / P;
-    const int n_items = full + (((full & 1) ? P - 1 - (int)blockIdx.x : (int)blockIdx.x) < n % P ? 1 : 0);
-    if (warp < 8) softmax_role(p, sm, tmem, n_items, warp >> 2, p.status);
-    else if (warp == S_WARP) scores_role(p, sm, tmem, n_items, p.status);
-    else if (warp == PV_WARP) product_role(p, sm, tmem, n_items, p.status);
-    else if ((threadIdx.x & 31) == 0) load_role(p, &tkv, &tq, sm, n_items, warp - K_WARP, p.status);
+    const Work w = work_of(p, sm);
+    if (warp < 8) softmax_role(p, sm, tmem, w, warp >> 2, p.status);
+    else if (warp == S_WARP) scores_role(p, sm, tmem, w, p.status);
+    else if (warp == PV_WARP) product_role(p, sm, tmem, w, p.status);
+    else if ((threadIdx.x & 31) == 0) load_role(p, &tkv, &tq, sm, w, warp - K_WARP, p.status);
     __syncwarp();
     tc_fence_before();
     __syncthreads();

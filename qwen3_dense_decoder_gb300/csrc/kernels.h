@@ -367,6 +367,13 @@ struct Kv4DecodeArgs {
 };
 cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type);
 
+// The prefill attention's work: fewer than KV4_CUT items (a tile for a KV head) a CTA
+// are cut into shares of equal cost.  A tile costs its steps of 64 positions and
+// KV4_TILE_COST more; a share is KV4_MIN_SHARE or more, a piece KV4_MIN_PIECE steps.
+constexpr int KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 2, KV4_MIN_SHARE = 16, KV4_MIN_PIECE = 4,
+              KV4_JOIN_COST = 12;
+constexpr size_t KV4_PART_BYTES = 128 * (128 + 2) * sizeof(float);   // output, maximum and sum of 128 rows
+
 // Causal attention of sequences of rows: sequence i is rows seq_rows[i] ..
 // seq_rows[i + 1] at positions seq_pos[i] .. of slot seq_slot[i].
 struct Kv4PrefillArgs {
@@ -383,10 +390,13 @@ struct Kv4PrefillArgs {
     __half* out;               // [T][n_q][128]
     int* status;
     // what the expansion leaves for the attention kernel
-    int rows_per_tile;
-    int* n_tiles;
-    int4* tiles;               // (first row, rows, its position, sequence), longest context first; at most
-                               // T / rows_per_tile + ns
+    int rows_per_tile, ctas;   // ctas: the attention kernel's grid, at most KV4_PREFILL_CTAS
+    int* n_tiles;              // [0] tiles, [2] cost of all tiles if they are to be cut, else 0
+    int* come;                 // [4 ctas], zeroed: warps that have left a piece
+    int* starts;               // cost before each tile, where they are to be cut
+    float4* parts;             // [2 ctas] KV4_PART_BYTES: pieces of cut tiles
+    int4* tiles;               // (first row, slot, its position | rows - 1 << 25, sequence), longest context first if not cut
+    int max_tiles;             // T / rows_per_tile + ns
     __half* copy;              // [blocks][2][n_kv][32][128]
     int by_seq;                // block i max_blocks + j is sequence i's block j (else the pool's numbers)
     uint32_t magic;            // KV4_MAGIC, set by the launcher

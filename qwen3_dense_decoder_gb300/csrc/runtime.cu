@@ -465,11 +465,11 @@ size_t kv_block_bytes(const q3_model* m)
 
 // ---------------------------------------------------------------- 4-bit cache prefill
 
-// The prefill attention's workspace: a tile count and a spare status word, the
-// tile list, the fp16 copy of the blocks (numbered as in the pool, or by
-// sequence where that is fewer).
+// The prefill attention's workspace: counts and a spare status word, the tile
+// list, the pieces of cut tiles, the fp16 copy of the blocks (numbered as in the
+// pool, or by sequence where that is fewer).
 struct Kv4Workspace {
-    size_t tiles, copy, bytes;
+    size_t come, starts, parts, tiles, copy, bytes;
     int64_t blocks;
     bool by_seq;
 };
@@ -478,7 +478,10 @@ Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int
     Kv4Workspace w;
     w.by_seq = (int64_t)ns * max_blocks < n_blocks;
     w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
-    w.tiles = 256;
+    w.come = 256;
+    w.starts = w.come + 4 * KV4_PREFILL_CTAS * sizeof(int);
+    w.parts = round_up(w.starts + KV4_CUT * KV4_PREFILL_CTAS * sizeof(int), 1024);
+    w.tiles = w.parts + 2 * KV4_PREFILL_CTAS * KV4_PART_BYTES;
     w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);
     w.bytes = w.copy + (size_t)w.blocks * 2 * n_kv * 32 * 128 * sizeof(f16);
     return w;
@@ -491,7 +494,12 @@ cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int 
     int* head = reinterpret_cast<int*>(ws);
     a.rows_per_tile = prefill_tc_rows(a.n_q, a.n_kv);
     a.n_tiles = head;
+    a.ctas = std::min(n_sm, KV4_PREFILL_CTAS);
+    a.come = reinterpret_cast<int*>(ws + w.come);
+    a.starts = reinterpret_cast<int*>(ws + w.starts);
+    a.parts = reinterpret_cast<float4*>(ws + w.parts);
     a.tiles = reinterpret_cast<int4*>(ws + w.tiles);
+    a.max_tiles = a.T / a.rows_per_tile + a.ns;
     a.copy = reinterpret_cast<f16*>(ws + w.copy);
     a.by_seq = w.by_seq;
     const int G = a.n_q / a.n_kv;
@@ -502,7 +510,7 @@ cudaError_t run_kv4_prefill(const Launch& L, Kv4PrefillArgs a, uint8_t* ws, int 
     if (cudaError_t e = launch_kv4_expand(L, a)) return e;
     if (!a.status) a.status = head + 1;              // a spare word nobody reads
     const Launch after{L.stream, true, L.counter};   // its setup overlaps the expansion
-    return launch_kv4_prefill(after, tkv, tq, a, n_sm);
+    return launch_kv4_prefill(after, tkv, tq, a, a.ctas);
 }
 
 // ---------------------------------------------------------------- the round

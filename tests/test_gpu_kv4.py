@@ -321,6 +321,42 @@ def test_prefill_attention(q3, case):
     assert (got[n:] == 9.0).all()                                  # rows of no sequence are left alone
 
 
+# Few tiles on long contexts, which are cut into pieces: (query heads, KV heads, [(rows, first position)])
+CUT = [(1, 1, [(3, 5000)]), (40, 8, [(60, 3000), (1, 2047)]), (8, 2, [(5, 1), (9, 6000), (0, 9), (70, 513)]), (16, 16, [(260, 800)])]
+
+
+@pytest.mark.parametrize("case", CUT, ids=str)
+def test_prefill_attention_of_few_tiles_on_long_contexts(q3, case):
+    n_q, n_kv, seqs = case
+    q, kv, tables, at, pos = _prefill_case(n_q, n_kv, seqs, 700 + n_q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [dev(at), dev(pos), dev(tables), dev(kv)]
+    n = at[-1]
+    got = q3.op_kv4_prefill_attention(q, *args, status=status)[:n]
+    q3.check_status(status)
+    want, vmax = _prefill_ref(q, kv, tables, at, pos, n_kv)
+    assert np.all(np.abs(got.cpu().numpy().astype(np.float64) - want[:n]) <= _bound(want, vmax, True, prefill=True)[:n])
+    for _ in range(5):                                             # whichever piece is last, the sums' order is one
+        assert torch.equal(got, q3.op_kv4_prefill_attention(q, *args)[:n])
+
+
+def test_prefill_attention_of_rows_in_many_sequences(q3):
+    """Sequences that go back to earlier rows have more tiles than the workspace lists: reported, and nothing is written past
+    it."""
+    T, ns = 256, 40                                                # 20 x 16 tiles for a list of 16 + 40
+    q, kv, _, _, _ = _prefill_case(16, 2, [(T, 0)], 303, tail=0)
+    tables = torch.arange(8, dtype=torch.int32, device="cuda").repeat(ns, 1)
+    at = torch.tensor([0, T] * (ns // 2) + [0], dtype=torch.int32, device="cuda")
+    pos = torch.zeros(ns, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    size = q3.kv4_prefill_workspace(ns, T, 16, 2, 8, kv.shape[0])
+    room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    out = q3.op_kv4_prefill_attention(q, at, pos, tables, dev(kv), workspace=room[:size], status=status)
+    with pytest.raises(q3.Q3Error) as e:
+        q3.check_status(status)
+    assert e.value.code == -7 and (room[size:] == 77).all() and torch.isfinite(out.float()).all()
+
+
 def test_prefill_attention_masked_bytes_and_slots(q3):
     q, kv, tables, at, pos = _prefill_case(32, 8, [(45, 20), (70, 0)], 301)
     slots = np.array([1, 0], np.int32)

@@ -22,11 +22,14 @@
 // are raised lazily: O and the sum are rescaled only when one grows by more than
 // 2^8.
 //
-// Three items a CTA or more are dealt whole, longest first.  Fewer are cut: the
-// items in a row, their steps are shared out evenly, a CTA's share may begin and
-// end inside an item, and a cut item's pieces leave maximum, sum and FP32 output in
-// the workspace, where the warp that finishes a row range last joins them in order.
-// (512 rows after 10,240 positions, 40/8 heads, 176 items: @CUT@.)
+// Items are dealt whole, longest first, where that comes out about even.  Else they
+// are cut: the items in a row, their steps are shared out evenly, a CTA's share may
+// begin and end inside an item, and a cut item's pieces leave maximum, sum and FP32
+// output in the workspace, where the warp that finishes a row range last joins them
+// in order.  (Dealt and cut: 512 rows after 10,240 positions, 40/8 heads, 179.9 and
+// 117.5 us; 64 rows after 4,096, 32/8 heads, 43.2 and 27.5; 16 rows after 32,768,
+// 307.9 and 75.7.  Where a join costs what it saves, 4 x 64 rows after 1,000, 17.8
+// and 20.3.)
 //
 // Roles (one CTA per SM; the next item's Q, K and scores are under way while an
 // item ends):
@@ -78,19 +81,24 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 // fp16 A and B, FP32 accumulator; PV reads V MN-major (bit 16)
 constexpr uint32_t IDESC_S = idesc_f16_f32(128, BN), IDESC_PV = idesc_f16_f32(128, 128) | (1u << 16);
 
-Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, Smem& sm, int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
+// Bounded wait; the slow part is out of line, so that the roles' loops stay small
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort, int* status) {
+    uint64_t t0 = 0;
     for (;;) {
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 512; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (*(volatile int*)&sm.abort) return false;
-        if (global_ns() - t0 > Q3_WAIT_LIMIT_NS) {
+        if (*(volatile int*)abort) return false;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > Q3_WAIT_LIMIT_NS) {
             set_status(status, Q3_STATUS_TIMEOUT);
-            *(volatile int*)&sm.abort = 1;
+            *(volatile int*)abort = 1;
             return false;
         }
     }
+}
+Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, Smem& sm, int* status) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, &sm.abort, status);
 }
 
 // A CTA's work: n items or pieces of items
@@ -240,14 +248,16 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
     const int G = p.n_q / p.n_kv;
     uint64_t* ld = which ? sm.v_load : sm.k_load;
     uint64_t* fr = which ? sm.pv_done : sm.s_full;
-    uint32_t n = 0;
-    for (int k = 0; k < w.n; ++k) {
+    uint32_t n = 0, nq = 0;
+    bool ok = true;
+    for (int k = 0; k < w.n && ok; ++k) {
         const Item it = item_of(p, w, k);
         const int* table = p.tables + (size_t)it.slot * p.max_blocks;
         const int last = it.pos0 + it.rows - 1;
         if (!which) {
             const int b = k & 1;
-            if (k > 1 && !wait_bar(&sm.q_free[b], ((k >> 1) - 1) & 1, sm, status)) return;
+            if (k > 1 && !wait_bar(&sm.q_free[b], ((k >> 1) - 1) & 1, sm, status)) break;
+            ++nq;
             mbar_arrive_expect_tx(&sm.q_full[b], 2 * p.rows_per_tile * G * 128);
 #pragma unroll
             for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[b] + h * Q_ATOM, tq, &sm.q_full[b], 64 * h, it.kvh * G, it.row0);
@@ -266,7 +276,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
                     // the expansion has reported any other
                 }
             }
-            if (n >= 4 && !wait_bar(&fr[slot], phase_before(n), sm, status)) return;
+            if (n >= 4 && !(ok = wait_bar(&fr[slot], phase_before(n), sm, status))) break;
             uint8_t* dst = which ? sm.v[slot] : sm.k[slot];
             mbar_arrive_expect_tx(&ld[slot], KV_TILE);
 #pragma unroll
@@ -276,6 +286,9 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
             }
         }
     }
+    // no copy of this CTA's may still be under way when it ends, even if another role gave up
+    for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&ld[i & 3], phase(i), status);
+    for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1, status);
 }
 
 // ---------------------------------------------------------------- softmax + output
@@ -309,21 +322,35 @@ Q3_DEV void join_pieces(const Kv4PrefillArgs& p, const Work& w, const Item& it, 
     __threadfence();
     auto piece = [&](int j) { return p.parts + (size_t)(2 * (c1 - 1 + j) + (j ? 0 : 1)) * PART; };
     auto ml = [&](int j) { return __ldcg(reinterpret_cast<const float2*>(piece(j) + 32 * 128) + row); };
-    float M = -INFINITY, L = 0.f;
-    for (int j = 0; j < pieces; ++j) M = fmaxf(M, ml(j).x);
     if (!valid) return;                                  // the others have seen their own position
-    for (int j = 0; j < pieces; ++j) L += fast_ex2(ml(j).x - M) * ml(j).y;
+    float M = -INFINITY, L = 0.f;
+    for (int j = 0; j < pieces; j += 4) {
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ml(min(j + i, pieces - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float m = fmaxf(M, x[i].x);
+            if (m == -INFINITY || j + i >= pieces) continue;
+            L = L * fast_ex2(M - m) + x[i].y * fast_ex2(x[i].x - m);
+            M = m;
+        }
+    }
     const float inv = 1.f / L;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32] = {};
-        for (int j = 0; j < pieces; ++j) {
-            const float f = fast_ex2(ml(j).x - M) * inv;
+#pragma unroll 2
+        for (int j = 0; j < pieces; ++j) {               // two pieces' loads under way
+            const float2 x = ml(j);
             const float4* src = piece(j) + 8 * c * 128 + row;
+            float4 o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = __ldcg(src + e * 128);
+            const float f = fast_ex2(x.x - M) * inv;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float4 x = __ldcg(src + e * 128);
-                v[4 * e] += f * x.x; v[4 * e + 1] += f * x.y; v[4 * e + 2] += f * x.z; v[4 * e + 3] += f * x.w;
+                v[4 * e] += f * o[e].x; v[4 * e + 1] += f * o[e].y; v[4 * e + 2] += f * o[e].z; v[4 * e + 3] += f * o[e].w;
             }
         }
         store32(dst + 32 * c, v, bad);

@@ -370,7 +370,7 @@ cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_typ
 // The prefill attention's work: fewer than KV4_CUT items (a tile for a KV head) a CTA
 // are cut into shares of equal cost.  A tile costs its steps of 64 positions and
 // KV4_TILE_COST more; a share is KV4_MIN_SHARE or more, a piece KV4_MIN_PIECE steps.
-constexpr int KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 2, KV4_MIN_SHARE = 16, KV4_MIN_PIECE = 4,
+constexpr int KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 2, KV4_MIN_SHARE = 8, KV4_MIN_PIECE = 4,
               KV4_JOIN_COST = 12;
 constexpr size_t KV4_PART_BYTES = 128 * (128 + 2) * sizeof(float);   // output, maximum and sum of 128 rows
 

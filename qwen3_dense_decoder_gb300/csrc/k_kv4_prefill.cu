@@ -367,6 +367,7 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
     uint32_t n0 = 0;                                     // the item's first step
     for (int k = 0; k < w.n; ++k) {
         const Item it = item_of(p, w, k);
+        const bool valid = ir < it.rows && ir < p.rows_per_tile;     // the others' scores are anything: they decide nothing
         const int qp = it.pos0 + min(ir, it.rows - 1);
         const int first = it.t0 + ((half ^ (int)n0) & 1); // of this half's steps in the item
         float m = -INFINITY, l = 0.f;
@@ -391,7 +392,7 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
             if (t == first) {
                 m = mn;
-            } else if (__any_sync(0xffffffffu, mn > m + LAZY)) {
+            } else if (__any_sync(0xffffffffu, valid && mn > m + LAZY)) {
                 // O, complete up to this half's last step, and l rescale; rows that
                 // have seen nothing (all of the half's positions are later ones)
                 // stay as they are
@@ -450,10 +451,11 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
         const float2 other = sm.ml[row];
         const float M = fmaxf(m, other.x);
         const float w0 = m == -INFINITY ? 0.f : fast_ex2(m - M), w1 = other.x == -INFINITY ? 0.f : fast_ex2(other.x - M);
-        const float sum = l * w0 + other.y * w1;
+        // which half took an item's first step goes by where its CTA's steps began, and that by
+        // an arbitrary order of equal tiles: sums that come out the same with the halves changed over
+        const float sum = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(other.y, w1));
         const bool whole = it.t1 - it.t0 == it.steps;
         const float r0 = whole ? w0 / sum : w0, r1 = whole ? w1 / sum : w1;
-        const bool valid = ir < it.rows && ir < p.rows_per_tile;
         bool bad = false;
         __half* dst = p.out + ((size_t)(it.row0 + min(ir, it.rows - 1)) * p.n_q + it.kvh * G + hh) * D;
         float4* part = p.parts + (size_t)(2 * blockIdx.x + (it.t0 ? 0 : 1)) * PART;
@@ -468,8 +470,9 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             float v[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float x = w0 == 0.f ? 0.f : __uint_as_float(o[e]) * r0, y = w1 == 0.f ? 0.f : __uint_as_float(ob[e]) * r1;
-                v[e] = x + y;
+                const float x = w0 == 0.f ? 0.f : __fmul_rn(__uint_as_float(o[e]), r0);
+                const float y = w1 == 0.f ? 0.f : __fmul_rn(__uint_as_float(ob[e]), r1);
+                v[e] = __fadd_rn(x, y);
             }
             if (!whole) {
 #pragma unroll

@@ -340,6 +340,15 @@ def test_prefill_attention_of_few_tiles_on_long_contexts(q3, case):
         assert torch.equal(got, q3.op_kv4_prefill_attention(q, *args)[:n])
 
 
+def test_prefill_attention_twice_is_the_same(q3):
+    """Tiles of equal length are listed in no fixed order: their places in a CTA's work do not show."""
+    q, kv, tables, at, pos = _prefill_case(24, 8, [(411, 134), (195, 134), (300, 134)] * 2, 304)
+    args = [dev(at), dev(pos), dev(tables), dev(kv)]
+    got = q3.op_kv4_prefill_attention(q, *args)[:at[-1]]
+    for _ in range(20):
+        assert torch.equal(got, q3.op_kv4_prefill_attention(q, *args)[:at[-1]])
+
+
 def test_prefill_attention_of_rows_in_many_sequences(q3):
     """Sequences that go back to earlier rows have more tiles than the workspace lists: reported, and nothing is written past
     it."""
@@ -351,7 +360,8 @@ def test_prefill_attention_of_rows_in_many_sequences(q3):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     size = q3.kv4_prefill_workspace(ns, T, 16, 2, 8, kv.shape[0])
     room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
-    out = q3.op_kv4_prefill_attention(q, at, pos, tables, dev(kv), workspace=room[:size], status=status)
+    out = torch.zeros_like(q)                                      # what is not listed is left as it was
+    q3.op_kv4_prefill_attention(q, at, pos, tables, dev(kv), out=out, workspace=room[:size], status=status)
     with pytest.raises(q3.Q3Error) as e:
         q3.check_status(status)
     assert e.value.code == -7 and (room[size:] == 77).all() and torch.isfinite(out.float()).all()

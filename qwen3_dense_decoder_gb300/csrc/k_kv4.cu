@@ -698,7 +698,7 @@ Q3_DEV void plan_cuts(const Kv4PrefillArgs& a) {
                       pos0 = __shfl_sync(0xffffffffu, mine.pos0, from), slot = __shfl_sync(0xffffffffu, mine.slot, from);
             for (int k0 = 0; k0 < rows; k0 += 32 * a.rows_per_tile) {
                 const int k = k0 + lane * a.rows_per_tile, r = min(a.rows_per_tile, rows - k);
-                const int own = r > 0 ? (pos0 + k + r - 1) / 64 + 1 + KV4_TILE_COST : 0;
+                const int own = r > 0 ? (pos0 + k + r - 1) / KV4_STEP + 1 + KV4_TILE_COST : 0;
                 int x = own;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -737,14 +737,14 @@ Q3_DEV void plan_tiles(const Kv4PrefillArgs& a) {
         atomicMax(&s_most, s.pos0 + s.rows);
         const int n = (s.rows - 1) / a.rows_per_tile + 1;
         atomicAdd(&s_tiles, (unsigned long long)n);
-        atomicAdd(&s_cost, (unsigned long long)n * ((s.pos0 + (s.rows + a.rows_per_tile) / 2) / 64 + 1 + KV4_TILE_COST));
+        atomicAdd(&s_cost, (unsigned long long)n * ((s.pos0 + (s.rows + a.rows_per_tile) / 2) / KV4_STEP + 1 + KV4_TILE_COST));
     }
     __syncthreads();
     // rows of more than one sequence: what does not fit the list is left out
     if (threadIdx.x == 0 && s_tiles > (unsigned long long)a.max_tiles) report(a.status, Q3_STATUS_BLOCK_RANGE);
     // cut where the longest CTA of whole tiles would take longer than a share and a join
     const unsigned long long items = s_tiles * a.n_kv, cost = s_cost * a.n_kv;
-    const unsigned long long whole = items < KV4_CUT * a.ctas ? max((unsigned long long)(s_most - 1) / 64 + 1 + KV4_TILE_COST,
+    const unsigned long long whole = items < KV4_CUT * a.ctas ? max((unsigned long long)(s_most - 1) / KV4_STEP + 1 + KV4_TILE_COST,
                                                                     (items + a.ctas - 1) / a.ctas * cost / max(items, 1ull))
                                                               : 0;
     if (s_tiles <= (unsigned long long)a.max_tiles && whole > max(cost / a.ctas, (unsigned long long)KV4_MIN_SHARE) + KV4_JOIN_COST) {

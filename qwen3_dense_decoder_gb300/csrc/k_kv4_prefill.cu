@@ -7,20 +7,20 @@
 //
 // Work item: R = 128 / G consecutive positions of one sequence for the G query
 // heads of one KV head, as an MMA tile of 128 rows (row r = position r / G, head
-// r % G).  Its context is walked in steps of 64 positions.  A CTA numbers the
-// steps of all its items through: step n belongs to half n % 2 of the CTA, each
-// half with its own running maximum, sum and output, joined at an item's end, and
-// uses slot n % 4 of everything: K and V stages, scores, barriers.
-//   S = Q K^T       tcgen05.mma, Q and K from shared memory, FP32 in tensor memory
+// r % G).  Its context is walked in steps of 128 positions, half h of the CTA taking
+// positions 64 h .. 64 h + 64 of each, with its own running maximum, sum and output;
+// the halves are joined at an item's end.
+//   S = Q K^T       tcgen05.mma, Q and K from shared memory, FP32 in tensor memory; both
+//                   halves' 64 columns at once (64 alone take the time of 128)
 //   P = 2^(S c - m) one thread a row, so nothing is exchanged; written over S
 //   O_h += P V      P from tensor memory, V read MN-major from shared memory
-// A half's next scores are ready while it works, and the halves' exponentials
-// overlap each other and the products.  (A row shared by two threads spent 480 of
-// 2,300 cycles a step on its maximum; scores issued only after the product before
-// them left the softmax waiting for 1,600; and one warp issuing both products
-// took 1,550 cycles a step, with its commits, against the 512 they run.)  Maxima
-// are raised lazily: O and the sum are rescaled only when one grows by more than
-// 2^8.
+// A step's scores are made while the last one's weights are, and the halves'
+// exponentials overlap each other and the products.  (A row shared by two threads
+// spent 480 of 2,300 cycles a step on its maximum; scores issued only after the
+// product before them left the softmax waiting for 1,600; one warp issuing both
+// products took 1,550 cycles for 64 positions, with its commits, against the 512 they
+// run.)  Maxima are raised lazily: O and the sum are rescaled only when one grows by
+// more than 2^8.
 //
 // Items are dealt whole, longest first, where that comes out about even.  Else they
 // are cut: the items in a row, their steps are shared out evenly, a CTA's share may
@@ -39,9 +39,8 @@
 //   warps 10, 11      lane 0 fetches K (and Q) or V with TMA (blocks past the item's
 //                     last position, or outside the pool, are read at a negative
 //                     row and land as zeros)
-// Tensor memory: scores of half h in columns 128 h and 128 h + 64, O_h at 256 +
-// 128 h.  Every wait is bounded; a timeout sets the status word and the CTA winds
-// down.
+// Tensor memory: two buffers of scores at 0 and 128, O_h at 256 + 128 h.  Every wait
+// is bounded; a timeout sets the status word and the CTA winds down.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -50,11 +49,11 @@ namespace q3 {
 namespace {
 
 constexpr int D = 128;
-constexpr int BN = 64;                       // positions of a step
+constexpr int BN = KV4_STEP;                 // positions of a step
 constexpr int Q_ATOM = 128 * 128;            // 128 rows x 64 fp16, one swizzle atom column
-constexpr int KV_ATOM = BN * 128;            // 64 rows x 64 fp16
+constexpr int KV_ATOM = BN * 128;            // 128 rows x 64 fp16
 constexpr int KV_TILE = 2 * KV_ATOM;
-constexpr int NS = 4;                        // slots
+constexpr int NS = 2;                        // slots
 constexpr int S_WARP = 8, PV_WARP = 9, K_WARP = 10;        // V: K_WARP + 1
 constexpr int THREADS = 12 * 32;
 constexpr uint32_t T_S = 0, T_O = 256;
@@ -65,9 +64,9 @@ struct alignas(1024) Smem {
     uint8_t q[2][2 * Q_ATOM];
     uint8_t k[NS][KV_TILE];
     uint8_t v[NS][KV_TILE];
-    // by slot, phase n / 4 of step n: K and V landed; scores done (K's stage is
-    // free); weights stored; product done (V's stage and the scores' columns are)
-    uint64_t k_load[NS], v_load[NS], s_full[NS], p_full[NS], pv_done[NS];
+    // by slot n % 2 of step n, phase n / 2: K and V landed; scores done (K's stage is
+    // free); by half: weights stored; product done (V's stage and the scores are free)
+    uint64_t k_load[NS], v_load[NS], s_full[NS], p_full[2][NS], pv_done[2][NS];
     uint64_t q_full[2], q_free[2];           // by item
     uint64_t b_done, o_free, drain[2];
     float2 ml[128];                          // half 1's maxima and sums
@@ -168,8 +167,8 @@ Q3_DEV Work work_of(const Kv4PrefillArgs& p, Smem& sm) {
 }
 
 // The phase of step n's slot, and the one before
-Q3_DEV uint32_t phase(uint32_t n) { return (n >> 2) & 1; }
-Q3_DEV uint32_t phase_before(uint32_t n) { return ((n >> 2) & 1) ^ 1; }
+Q3_DEV uint32_t phase(uint32_t n) { return (n >> 1) & 1; }
+Q3_DEV uint32_t phase_before(uint32_t n) { return ((n >> 1) & 1) ^ 1; }
 
 // ---------------------------------------------------------------- MMA issuers
 // A whole warp walks the loop and one lane issues, so descriptors and addresses
@@ -189,13 +188,14 @@ Q3_DEV void scores_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const 
         const uint64_t qd = q0 + (uint32_t)(k & 1) * (2 * Q_ATOM >> 4);
         if (!(ok = wait_bar(&sm.q_full[k & 1], (k >> 1) & 1, sm, status))) break;
         for (int t = 0; t < steps; ++t, ++n) {
-            const uint32_t slot = n & 3;
-            // the slot's last product has read the weights that lie over its scores
-            if (n >= 4 && !(ok = wait_bar(&sm.pv_done[slot], phase_before(n), sm, status))) break;
+            const uint32_t slot = n & 1;
             if (!(ok = wait_bar(&sm.k_load[slot], phase(n), sm, status))) break;
+            // the slot's last products have read the weights that lie over its scores
+            if (n >= NS && !(ok = wait_bar(&sm.pv_done[0][slot], phase_before(n), sm, status))) break;
+            if (n >= NS && !(ok = wait_bar(&sm.pv_done[1][slot], phase_before(n), sm, status))) break;
             tc_fence_after();
             const uint64_t kd = k0 + slot * (KV_TILE >> 4);
-            const uint32_t d = tmem + T_S + (n & 1) * 128 + (slot >> 1) * 64;
+            const uint32_t d = tmem + T_S + slot * 128;
             if (leader) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
@@ -221,17 +221,23 @@ Q3_DEV void product_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
         // the last item's outputs are read out before this one's first products
         if (k > 0 && !(ok = wait_bar(&sm.o_free, (k - 1) & 1, sm, status))) break;
         for (int t = 0; t < steps; ++t, ++n) {
-            const uint32_t slot = n & 3;
+            const uint32_t slot = n & 1;
             if (!(ok = wait_bar(&sm.v_load[slot], phase(n), sm, status))) break;
-            if (!(ok = wait_bar(&sm.p_full[slot], phase(n), sm, status))) break;
-            tc_fence_after();
             const uint64_t vd = v0 + slot * (KV_TILE >> 4);
-            const uint32_t d = tmem + T_O + (n & 1) * 128, a = tmem + T_S + (n & 1) * 128 + (slot >> 1) * 64, more = t > 1 ? 1u : 0u;
-            if (leader) {
+            const uint32_t more = t > 0 ? 1u : 0u;
 #pragma unroll
-                for (int s = 0; s < BN / 16; ++s) tc_mma_f16_ts(d, a + s * 8, vd + (s * 2048 >> 4), IDESC_PV, s > 0 ? 1u : more);
-                tc_commit(&sm.pv_done[slot]);
+            for (int h = 0; h < 2; ++h) {
+                if (!(ok = wait_bar(&sm.p_full[h][slot], phase(n), sm, status))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + T_O + h * 128, a = tmem + T_S + slot * 128 + h * 64;
+                if (leader) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        tc_mma_f16_ts(d, a + s * 8, vd + ((4 * h + s) * 2048 >> 4), IDESC_PV, s > 0 ? 1u : more);
+                    tc_commit(&sm.pv_done[h][slot]);
+                }
             }
+            if (!ok) break;
         }
     }
     if (leader) tc_commit(&sm.drain[1]);
@@ -247,7 +253,6 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
                       int* status) {
     const int G = p.n_q / p.n_kv;
     uint64_t* ld = which ? sm.v_load : sm.k_load;
-    uint64_t* fr = which ? sm.pv_done : sm.s_full;
     uint32_t n = 0, nq = 0;
     bool ok = true;
     for (int k = 0; k < w.n && ok; ++k) {
@@ -263,7 +268,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
             for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[b] + h * Q_ATOM, tq, &sm.q_full[b], 64 * h, it.kvh * G, it.row0);
         }
         for (int t = it.t0; t < it.t1; ++t, ++n) {
-            const uint32_t slot = n & 3;
+            const uint32_t slot = n & 1;
             int row[BN / 32];
 #pragma unroll
             for (int j = 0; j < BN / 32; ++j) {
@@ -276,7 +281,11 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
                     // the expansion has reported any other
                 }
             }
-            if (n >= 4 && !(ok = wait_bar(&fr[slot], phase_before(n), sm, status))) break;
+            if (n >= NS) {
+                if (which) ok = wait_bar(&sm.pv_done[0][slot], phase_before(n), sm, status) && wait_bar(&sm.pv_done[1][slot], phase_before(n), sm, status);
+                else ok = wait_bar(&sm.s_full[slot], phase_before(n), sm, status);
+                if (!ok) break;
+            }
             uint8_t* dst = which ? sm.v[slot] : sm.k[slot];
             mbar_arrive_expect_tx(&ld[slot], KV_TILE);
 #pragma unroll
@@ -287,7 +296,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
         }
     }
     // no copy of this CTA's may still be under way when it ends, even if another role gave up
-    for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&ld[i & 3], phase(i), status);
+    for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&ld[i & 1], phase(i), status);
     for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1, status);
 }
 
@@ -361,26 +370,26 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
     const int quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (threadIdx.x & 31);
     const int G = p.n_q / p.n_kv;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t s0 = tmem + T_S + half * 128 + lanes, to = tmem + T_O + lanes;
+    const uint32_t s0 = tmem + T_S + half * 64 + lanes, to = tmem + T_O + lanes;
     const float scale = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
     const int ir = row / G, hh = row % G;
-    uint32_t n0 = 0;                                     // the item's first step
+    uint32_t n = 0;                                      // steps so far
     for (int k = 0; k < w.n; ++k) {
         const Item it = item_of(p, w, k);
         const bool valid = ir < it.rows && ir < p.rows_per_tile;     // the others' scores are anything: they decide nothing
         const int qp = it.pos0 + min(ir, it.rows - 1);
-        const int first = it.t0 + ((half ^ (int)n0) & 1); // of this half's steps in the item
         float m = -INFINITY, l = 0.f;
-        for (int t = first; t < it.t1; t += 2) {
-            const uint32_t n = n0 + (t - it.t0), slot = n & 3, ts = s0 + (slot >> 1) * 64;
+        for (int t = it.t0; t < it.t1; ++t, ++n) {
+            const uint32_t slot = n & 1, ts = s0 + slot * 128;
+            const int p0 = t * BN + half * 64;           // this half's first position
             if (!wait_bar(&sm.s_full[slot], phase(n), sm, status)) return;
             tc_fence_after();
             uint32_t v[2][32];
             tmem_ld_32x32b_x32(ts, v[0]);
             tmem_ld_32x32b_x32(ts + 32, v[1]);
             tmem_ld_wait();
-            if (t * BN + BN - 1 > it.pos0) {
-                const int left = qp - t * BN;            // columns past it are later positions
+            if (p0 + 63 > it.pos0) {
+                const int left = qp - p0;                // columns past it are later positions
 #pragma unroll
                 for (int e = 0; e < 64; ++e)
                     if (e > left) v[e >> 5][e & 31] = __float_as_uint(-INFINITY);
@@ -390,14 +399,14 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             for (int e = 0; e < 64; e += 2)
                 mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31])), __uint_as_float(v[e >> 5][(e & 31) + 1]));
             const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
-            if (t == first) {
+            if (t == it.t0) {
                 m = mn;
             } else if (__any_sync(0xffffffffu, valid && mn > m + LAZY)) {
                 // O, complete up to this half's last step, and l rescale; rows that
                 // have seen nothing (all of the half's positions are later ones)
                 // stay as they are
                 const float alpha = m == mn ? 1.f : fast_ex2(m - mn);
-                if (!wait_bar(&sm.pv_done[(n - 2) & 3], phase(n - 2), sm, status)) return;
+                if (!wait_bar(&sm.pv_done[half][slot ^ 1], phase(n - 1), sm, status)) return;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {            // 16 columns at a time: S stays in registers
@@ -421,22 +430,19 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float2 u = halves_of(fma2(pair_of(__uint_as_float(v[h][2 * e]), __uint_as_float(v[h][2 * e + 1])), sc, nm));
-                    const float p0 = fast_ex2(u.x), p1 = fast_ex2(u.y);
-                    sum[e & 1] = add2(sum[e & 1], pair_of(p0, p1));
-                    const __half2 h2 = __floats2half2_rn(p0, p1);
+                    const float w0 = fast_ex2(u.x), w1 = fast_ex2(u.y);
+                    sum[e & 1] = add2(sum[e & 1], pair_of(w0, w1));
+                    const __half2 h2 = __floats2half2_rn(w0, w1);
                     ph[e] = *reinterpret_cast<const uint32_t*>(&h2);
                 }
                 tmem_st_32x32b_x16(ts + 16 * h, ph);
             }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sm.p_full[slot]);
+            mbar_arrive(&sm.p_full[half][slot]);
             const float2 a = halves_of(add2(sum[0], sum[1]));
             l += a.x + a.y;
         }
-        // a half's O is complete once the product of its last step is
-        const uint32_t end = n0 + (it.t1 - it.t0);
-        n0 = end;
         if (half) {
             // half 0 has read the last item's (so this half is never two items ahead)
             if (k > 0 && !wait_bar(&sm.o_free, (k - 1) & 1, sm, status)) return;
@@ -445,15 +451,14 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             continue;
         }
         if (!wait_bar(&sm.b_done, k & 1, sm, status)) return;
-        for (int back = 1; back <= min(it.t1 - it.t0, 2); ++back)
-            if (!wait_bar(&sm.pv_done[(end - back) & 3], phase(end - back), sm, status)) return;
+        // a half's O is complete once the product of its last step is
+        for (int h = 0; h < 2; ++h)
+            if (!wait_bar(&sm.pv_done[h][(n - 1) & 1], phase(n - 1), sm, status)) return;
         tc_fence_after();
         const float2 other = sm.ml[row];
         const float M = fmaxf(m, other.x);
         const float w0 = m == -INFINITY ? 0.f : fast_ex2(m - M), w1 = other.x == -INFINITY ? 0.f : fast_ex2(other.x - M);
-        // which half took an item's first step goes by where its CTA's steps began, and that by
-        // an arbitrary order of equal tiles: sums that come out the same with the halves changed over
-        const float sum = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(other.y, w1));
+        const float sum = l * w0 + other.y * w1;
         const bool whole = it.t1 - it.t0 == it.steps;
         const float r0 = whole ? w0 / sum : w0, r1 = whole ? w1 / sum : w1;
         bool bad = false;
@@ -465,15 +470,9 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             tmem_ld_32x32b_x32(to + 32 * c, o);
             tmem_ld_32x32b_x32(to + 128 + 32 * c, ob);
             tmem_ld_wait();
-            // a half that has no step in this item, or a row none of its positions,
-            // holds another item's output, or nothing
             float v[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const float x = w0 == 0.f ? 0.f : __fmul_rn(__uint_as_float(o[e]), r0);
-                const float y = w1 == 0.f ? 0.f : __fmul_rn(__uint_as_float(ob[e]), r1);
-                v[e] = __fadd_rn(x, y);
-            }
+            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * r0 + __uint_as_float(ob[e]) * r1;
             if (!whole) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) part[(8 * c + e) * 128 + row] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -502,8 +501,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prefill_kernel(const __grid_co
             mbar_init(&sm.k_load[i], 1);
             mbar_init(&sm.v_load[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 128);
-            mbar_init(&sm.pv_done[i], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.p_full[h][i], 128);
+                mbar_init(&sm.pv_done[h][i], 1);
+            }
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);

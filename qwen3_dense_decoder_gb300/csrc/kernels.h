@@ -368,10 +368,11 @@ struct Kv4DecodeArgs {
 cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_type, int out_type);
 
 // The prefill attention's work: fewer than KV4_CUT items (a tile for a KV head) a CTA
-// are cut into shares of equal cost.  A tile costs its steps of 64 positions and
-// KV4_TILE_COST more; a share is KV4_MIN_SHARE or more, a piece KV4_MIN_PIECE steps.
-constexpr int KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 2, KV4_MIN_SHARE = 8, KV4_MIN_PIECE = 4,
-              KV4_JOIN_COST = 12;
+// are cut into shares of equal cost.  A tile costs its steps of KV4_STEP
+// positions and KV4_TILE_COST more; a share is KV4_MIN_SHARE or more, a piece
+// KV4_MIN_PIECE steps.
+constexpr int KV4_STEP = 128, KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 1, KV4_MIN_SHARE = 4, KV4_MIN_PIECE = 2,
+              KV4_JOIN_COST = 6;
 constexpr size_t KV4_PART_BYTES = 128 * (128 + 2) * sizeof(float);   // output, maximum and sum of 128 rows
 
 // Causal attention of sequences of rows: sequence i is rows seq_rows[i] ..

@@ -727,7 +727,7 @@ Q3_DEV void plan_tiles(const Kv4PrefillArgs& a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) { s_most = 0; s_tiles = 0; s_cost = 0; }
     for (int i = threadIdx.x; i < CLASSES; i += XT) s_at[i] = 0;
-    for (int i = threadIdx.x; i < 4 * a.ctas; i += XT) a.come[i] = 0;
+    for (int i = threadIdx.x; i < 8 * a.ctas; i += XT) a.come[i] = 0;
     __syncthreads();
     bool bad;
     for (int i = threadIdx.x; i < a.ns; i += XT) {

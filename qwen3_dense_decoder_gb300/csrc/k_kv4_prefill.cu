@@ -34,7 +34,7 @@
 // Roles (one CTA per SM; the next item's Q, K and scores are under way while an
 // item ends):
 //   warps 0..3, 4..7  softmax of half 0 and of half 1 (warp w: TMEM lanes 32 (w % 4)
-//                     .. + 32); half 0's also join the halves and write the output
+//                     .. + 32); half 0 writes an item's output, both write a piece's
 //   warps 8, 9        issue the score products and the PV products
 //   warps 10, 11      fetch K (and Q) or V with TMA (blocks past the item's last
 //                     position, or outside the pool, are read at a negative row and
@@ -68,8 +68,8 @@ struct alignas(1024) Smem {
     // free); by half: weights stored; product done (V's stage and the scores are free)
     uint64_t k_load[NS], v_load[NS], s_full[NS], p_full[2][NS], pv_done[2][NS];
     uint64_t q_full[2], q_free[2];           // by item
-    uint64_t b_done, o_free, drain[2];
-    float2 ml[128];                          // half 1's maxima and sums
+    uint64_t ml_done[2], o_free, drain[2];
+    float2 ml[2][128];                       // the halves' maxima and sums
     int2 cut[2];                             // where this CTA's share begins and ends: item, step
     uint32_t tmem;
     int abort;
@@ -322,18 +322,18 @@ Q3_DEV void store32(__half* dst, const float (&v)[32], bool& bad) {
 // A cut item's pieces lie with consecutive CTAs: the first in its CTA's second
 // place, the others in the first.  This warp has stored its rows of one; the last
 // to come joins its rows of all, in the pieces' order.
-Q3_DEV void join_pieces(const Kv4PrefillArgs& p, const Work& w, const Item& it, int quad, int row, bool valid, __half* dst, bool& bad) {
+Q3_DEV void join_pieces(const Kv4PrefillArgs& p, const Work& w, const Item& it, int half, int quad, int row, bool valid, __half* dst, bool& bad) {
     const int start = it.kvh * p.n_tiles[2] + p.starts[it.tile];
     const int c1 = (start + KV4_MIN_PIECE + w.share - 1) / w.share, c2 = (start + it.steps - KV4_MIN_PIECE) / w.share;
     const int pieces = c2 - c1 + 2;
     __threadfence();
     __syncwarp();
     int come = 0;
-    if ((threadIdx.x & 31) == 0) come = atomicAdd(p.come + 4 * (c1 - 1) + quad, 1);
+    if ((threadIdx.x & 31) == 0) come = atomicAdd(p.come + 8 * (c1 - 1) + 4 * half + quad, 1);
     if (__shfl_sync(0xffffffffu, come, 0) != pieces - 1) return;
     __threadfence();
     auto piece = [&](int j) { return p.parts + (size_t)(2 * (c1 - 1 + j) + (j ? 0 : 1)) * PART; };
-    auto ml = [&](int j) { return __ldcg(reinterpret_cast<const float2*>(piece(j) + 32 * 128) + row); };
+    auto ml = [&](int j) { return __ldcg(reinterpret_cast<const float2*>(piece(j) + 32 * 128) + 128 * half + row); };
     if (!valid) return;                                  // the others have seen their own position
     float M = -INFINITY, L = 0.f;
     for (int j = 0; j < pieces; j += 4) {
@@ -350,7 +350,7 @@ Q3_DEV void join_pieces(const Kv4PrefillArgs& p, const Work& w, const Item& it, 
     }
     const float inv = 1.f / L;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 2 * half; c < 2 * half + 2; ++c) {
         float v[32] = {};
 #pragma unroll 2
         for (int j = 0; j < pieces; ++j) {               // two pieces' loads under way
@@ -446,29 +446,32 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             const float2 a = halves_of(add2(sum[0], sum[1]));
             l += a.x + a.y;
         }
-        if (half) {
-            // half 0 has read the last item's (so this half is never two items ahead)
-            if (k > 0 && !wait_bar(&sm.o_free, (k - 1) & 1, sm, status)) return;
-            sm.ml[row] = make_float2(m, l);
-            mbar_arrive(&sm.b_done);
+        // The halves tell each other their maxima and sums, once both have read the last
+        // item's.  Half 0 writes an item's output while half 1 goes on; a piece, whose
+        // join takes longer, they write 64 columns each.
+        const bool whole = it.t1 - it.t0 == it.steps;
+        if (k > 0 && !wait_bar(&sm.o_free, (k - 1) & 1, sm, status)) return;
+        sm.ml[half][row] = make_float2(m, l);
+        mbar_arrive(&sm.ml_done[half]);
+        if (half && whole) {
+            mbar_arrive(&sm.o_free);
             continue;
         }
-        if (!wait_bar(&sm.b_done, k & 1, sm, status)) return;
+        if (!wait_bar(&sm.ml_done[half ^ 1], k & 1, sm, status)) return;
         // a half's O is complete once the product of its last step is
         for (int h = 0; h < 2; ++h)
             if (!wait_bar(&sm.pv_done[h][(n - 1) & 1], phase(n - 1), sm, status)) return;
         tc_fence_after();
-        const float2 other = sm.ml[row];
-        const float M = fmaxf(m, other.x);
-        const float w0 = m == -INFINITY ? 0.f : fast_ex2(m - M), w1 = other.x == -INFINITY ? 0.f : fast_ex2(other.x - M);
-        const float sum = l * w0 + other.y * w1;
-        const bool whole = it.t1 - it.t0 == it.steps;
+        const float2 a = sm.ml[0][row], b = sm.ml[1][row];
+        const float M = fmaxf(a.x, b.x);
+        const float w0 = a.x == -INFINITY ? 0.f : fast_ex2(a.x - M), w1 = b.x == -INFINITY ? 0.f : fast_ex2(b.x - M);
+        const float sum = a.y * w0 + b.y * w1;
         const float r0 = whole ? w0 / sum : w0, r1 = whole ? w1 / sum : w1;
         bool bad = false;
         __half* dst = p.out + ((size_t)(it.row0 + min(ir, it.rows - 1)) * p.n_q + it.kvh * G + hh) * D;
         float4* part = p.parts + (size_t)(2 * blockIdx.x + (it.t0 ? 0 : 1)) * PART;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = whole ? 0 : 2 * half; c < (whole ? 4 : 2 * half + 2); ++c) {
             uint32_t o[32], ob[32];
             tmem_ld_32x32b_x32(to + 32 * c, o);
             tmem_ld_32x32b_x32(to + 128 + 32 * c, ob);
@@ -486,8 +489,8 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
         tc_fence_before();
         mbar_arrive(&sm.o_free);
         if (!whole) {
-            reinterpret_cast<float2*>(part + 32 * 128)[row] = make_float2(M, sum);
-            join_pieces(p, w, it, quad, row, valid, dst, bad);
+            reinterpret_cast<float2*>(part + 32 * 128)[128 * half + row] = make_float2(M, sum);
+            join_pieces(p, w, it, half, quad, row, valid, dst, bad);
         }
         if (bad) set_status(status, Q3_STATUS_F16_RANGE);
     }
@@ -514,8 +517,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prefill_kernel(const __grid_co
             mbar_init(&sm.q_free[i], 1);
             mbar_init(&sm.drain[i], 1);
         }
-        mbar_init(&sm.b_done, 128);
-        mbar_init(&sm.o_free, 128);
+        mbar_init(&sm.ml_done[0], 128);
+        mbar_init(&sm.ml_done[1], 128);
+        mbar_init(&sm.o_free, 256);
         sm.abort = 0;
         fence_barrier_init();
         prefetch_tmap(&tkv);

@@ -373,7 +373,7 @@ cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_typ
 // KV4_MIN_PIECE steps.
 constexpr int KV4_STEP = 128, KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 1, KV4_MIN_SHARE = 4, KV4_MIN_PIECE = 2,
               KV4_JOIN_COST = 6;
-constexpr size_t KV4_PART_BYTES = 128 * (128 + 2) * sizeof(float);   // output, maximum and sum of 128 rows
+constexpr size_t KV4_PART_BYTES = 128 * (128 + 4) * sizeof(float);   // output, maximum and sum (by half) of 128 rows
 
 // Causal attention of sequences of rows: sequence i is rows seq_rows[i] ..
 // seq_rows[i + 1] at positions seq_pos[i] .. of slot seq_slot[i].
@@ -393,7 +393,7 @@ struct Kv4PrefillArgs {
     // what the expansion leaves for the attention kernel
     int rows_per_tile, ctas;   // ctas: the attention kernel's grid, at most KV4_PREFILL_CTAS
     int* n_tiles;              // [0] tiles, [2] cost of all tiles if they are to be cut, else 0
-    int* come;                 // [4 ctas], zeroed: warps that have left a piece
+    int* come;                 // [8 ctas], zeroed: warps that have left a piece
     int* starts;               // cost before each tile, where they are to be cut
     float4* parts;             // [2 ctas] KV4_PART_BYTES: pieces of cut tiles
     int4* tiles;               // (first row, slot, its position | rows - 1 << 25, sequence), longest context first if not cut

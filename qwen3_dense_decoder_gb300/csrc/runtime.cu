@@ -479,7 +479,7 @@ Kv4Workspace kv4_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int
     w.by_seq = (int64_t)ns * max_blocks < n_blocks;
     w.blocks = w.by_seq ? (int64_t)ns * max_blocks : n_blocks;
     w.come = 256;
-    w.starts = w.come + 4 * KV4_PREFILL_CTAS * sizeof(int);
+    w.starts = w.come + 8 * KV4_PREFILL_CTAS * sizeof(int);
     w.parts = round_up(w.starts + KV4_CUT * KV4_PREFILL_CTAS * sizeof(int), 1024);
     w.tiles = w.parts + 2 * KV4_PREFILL_CTAS * KV4_PART_BYTES;
     w.copy = round_up(w.tiles + sizeof(int4) * ((size_t)T / prefill_tc_rows(n_q, n_kv) + ns), 1024);

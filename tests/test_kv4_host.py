@@ -126,7 +126,7 @@ def test_binding_refuses_before_the_library():
 def test_prefill_workspace_is_planned_on_the_host(L):
     import qwen3_dense_decoder_gb300 as q3
     copy = 8 * 16384                                    # one block of eight KV heads in fp16, K and V
-    rest = 2 * 152 * 128 * (128 + 2) * 4 + (1 << 16)    # two pieces of a cut tile a CTA: output, maximum and sum of 128 rows; lists
+    rest = 2 * 152 * 128 * (128 + 4) * 4 + (1 << 16)    # two pieces of a cut tile a CTA: output, maximum and sum of 128 rows; lists
     # the pool's blocks, or the sequences' tables where those are fewer
     assert q3.kv4_prefill_workspace(1, 2048, 32, 8, 64, 40) - 40 * copy < rest
     assert q3.kv4_prefill_workspace(2, 100, 32, 8, 4, 100000) - 8 * copy < rest

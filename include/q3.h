@@ -420,7 +420,8 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
  * Q3_STATUS_* bits into *status_dev, an int32 the caller owns, clears and
  * reads when it likes, or NULL.  Arguments the host can see are refused with
  * Q3_ERR_INVALID_ARG before anything is launched; zero rows are Q3_OK and
- * launch nothing.  The caller's buffers are those of the current device.
+ * launch nothing.  The caller's buffers are those of the current device;
+ * outputs and workspaces overlap nothing else of a call.
  * The Kipp pages have no counterpart beyond "Kipp Roadmap", status v0.0.4 (a
  * quantized cache is opt-in) and "Kipp Model Support", section "Quantization
  * (AFFINE4_GS32)", whose rule packs the rows.
@@ -438,7 +439,8 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
  *     [position / 2][group][scale even, scale odd, bias even, bias odd].
  * tables_dev: int32 [n_slots][max_blocks], the physical block of each 32
  * positions of a slot.  Sizes: 1 <= n_kv, n_q a multiple of n_kv and at most
- * 8 n_kv, 1 <= n_blocks, n_slots, max_blocks; max_blocks at most 2^20.
+ * 8 n_kv, 1 <= n_blocks, n_slots, max_blocks; max_blocks at most 2^20, rows
+ * T times n_kv below 2^31.
  *
  * q3_op_kv4_append: per row t of projections (n_q q heads, then n_kv k heads,
  * then n_kv v heads of 128) at position row_pos_dev[t] of slot
@@ -481,7 +483,8 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
 
 /* q3_op_kv4_prefill_attention: causal GQA attention of ns sequences of rows.
  * Sequence i is rows seq_rows_dev[i] .. seq_rows_dev[i + 1] - 1 (int32 [ns +
- * 1], not decreasing, within [0, T]; a sequence may be empty) at positions
+ * 1], not decreasing, within [0, T]; a sequence may be empty; rows in many
+ * sequences are reported and in part left out) at positions
  * seq_pos_dev[i] .. of slot seq_slot_dev[i] (NULL: slot i); each row attends
  * the slot's positions up to its own, which the cache must hold (the round's
  * rows are appended first).  Rows of no sequence keep their output; rows of
@@ -498,8 +501,9 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
                                 int n_kv, const int32_t* tables_dev, int n_slots, int max_blocks, const void* kv_dev,
                                 int n_blocks, void* out_dev, void* workspace_dev, int64_t workspace_bytes,
                                 int32_t* status_dev, void* stream);
-/* Bytes of workspace for these sizes: mostly an fp16 copy of the blocks a call
- * may read, min(n_blocks, ns * max_blocks) blocks of n_kv * 16 KB.  Host only.
+/* Bytes of workspace for these sizes: an fp16 copy of the blocks a call may
+ * read, min(n_blocks, ns * max_blocks) blocks of n_kv * 16 KB, and about 20 MB
+ * for lists and for tiles that several SMs share.  Host only.
  * Errors: Q3_ERR_INVALID_ARG. */
 int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks, int64_t* bytes);
 

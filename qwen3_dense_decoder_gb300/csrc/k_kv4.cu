@@ -57,7 +57,8 @@ Q3_DEV void load4(const __half* p, int lane, float (&y)[4]) {
 // group's range, and the square root, the reciprocals and the divisions serve
 // four heads at once.  A head's value costs about half an instruction (q) to
 // one (k); the bytes are (n_q + 2 n_kv) 128 projections in, 2 bytes a q value
-// and 0.625 a k or v value out.
+// and 0.625 a k or v value out.  2,048 rows of 48 heads in f32: 18.8 us, 4.2 TB/s
+// of those bytes (a warp a head took 29.7); 32 rows: 3.1 us, latency.
 Q3_DEV void load8(const float* p, float* y) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w; y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
@@ -245,6 +246,11 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 //
 // Splits of a (row, KV head) are one cluster; warps merge in order through
 // shared memory, CTAs in order through distributed shared memory.
+//
+// tcgen05 would want the expanded values in shared memory, 256 bytes where 80 come
+// in, for at most eight columns.  8 rows of 16,384 positions (40/8 heads): 43 us,
+// 3.9 TB/s, bound by the instructions that unpack; 32 rows of 1,184 (32/8): 20.6 us;
+// one row of 2,176: 6.7 us, latency.
 constexpr int AW = 4;
 constexpr int STAGES = 2;
 constexpr int KV4_STAGE = 2 * KV4_TILE;
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(AW * 32, 4) kv4_decode_kernel(const Kv4DecodeA
 
 // CTAs of a (row, KV head).  Four fit an SM (16 warps); the splits grow by twos
 // while the grid still fits the SMs at once (608; a second wave costs more than
-// idle SMs: 64 rows of 2,000 positions 37 us unsplit, 40 in two) and a CTA keeps
+// idle SMs: 64 rows of 2,000 positions 38 us unsplit, 41 in two) and a CTA keeps
 // two blocks (one row of 600 positions: 4.8 us in 8 splits, 5.9 in 4), four for
 // 16, whose clusters leave some SMs out (4 rows of 1,000: 6.3 us in 8, 7.2 in
 // 16; of 32,768: 44 in 8, 39 in 16).
@@ -654,15 +660,17 @@ cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a)
 
 // ---------------------------------------------------------------- prefill: tile list and fp16 copy
 // A prompt's attention reads every block once per query tile, so its blocks
-// are expanded once, into an fp16 copy that the tcgen05 kernel (k_attn_tc.cu)
+// are expanded once, into an fp16 copy that the tcgen05 kernel (k_kv4_prefill.cu)
 // fetches with TMA: 80 + 256 bytes a position and head against 512 flop a row
 // and position.  A warp expands half a tile at a time, all its loads first: 4-byte
-// code words in, 16-byte words out, both coalesced.  Places at or past the sequence's end hold whatever
-// the pool holds, made finite (their weights are zero).
+// code words in, 16-byte words out, both coalesced.  Places at or past the
+// sequence's end hold whatever the pool holds, made finite (their weights are zero).
 //
-// CTA 0 lists the query tiles meanwhile.  Enough of them, longest context first: a counting
-// sort by context in 1,024 classes (order within a class does not matter).  Fewer
-// stay in order, with the cost before each, for the attention kernel to cut.
+// CTA 0 lists the query tiles meanwhile.  Enough of them, longest context first: a
+// counting sort by context in 1,024 classes (order within a class does not matter).
+// Fewer stay in order, with the cost before each, for the attention kernel to cut.
+// (Expansion behind the list, a quarter of a tile's loads at a time: 2,048 positions
+// 4 us more, 10,752 10 us more.)
 constexpr int XT = 256;
 constexpr int CLASSES = 1024;
 

@@ -26,10 +26,16 @@
 // are cut: the items in a row, their steps are shared out evenly, a CTA's share may
 // begin and end inside an item, and a cut item's pieces leave maximum, sum and FP32
 // output in the workspace, where the warp that finishes a row range last joins them
-// in order.  (Dealt and cut: 512 rows after 10,240 positions, 40/8 heads, 179.9 and
-// 117.5 us; 64 rows after 4,096, 32/8 heads, 43.2 and 27.5; 16 rows after 32,768,
-// 307.9 and 75.7.  Where a join costs what it saves, 4 x 64 rows after 1,000, 17.8
-// and 20.3.)
+// in order.  Cut where fewer than three items a CTA would take the longest CTA 12 steps
+// more than an even share.  (Dealt and cut: 512 rows after 10,240 positions, 40/8
+// heads, 123 and 88 us; 64 rows after 4,096, 32/8 heads, 30.8 and 23.2; 16 rows after
+// 32,768, 221 and 68.  The other way: 256 rows after 2,000, 21.2 and 24.0; 2,048 rows,
+// 35.7 and 47.9.)
+//
+// A step of 128 positions reads 64 KB of K and V: 1,024 cycles of an SM's 64 bytes, as
+// many as its products take; it takes 1,450 with long contexts (512 rows after 10,240:
+// 88 us, 1.25 PFLOP/s over the whole call), 1,760 where a CTA has three items of nine
+// steps (2,048 rows: 35.7 us, 0.96 PFLOP/s).
 //
 // Roles (one CTA per SM; the next item's Q, K and scores are under way while an
 // item ends):

@@ -2349,7 +2349,7 @@ namespace {
 // what the three cache operators share: heads, tables, pool
 bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int max_blocks, const void* kv, int n_blocks)
 {
-    return T >= 0 && n_kv >= 1 && n_kv <= 4096 && n_q >= 1 && n_q <= 8 * n_kv && n_q % n_kv == 0 && tables && n_slots >= 1 &&
+    return T >= 0 && n_kv >= 1 && n_kv <= 4096 && (int64_t)T * n_kv <= 0x7fffffff && n_q >= 1 && n_q <= 8 * n_kv && n_q % n_kv == 0 && tables && n_slots >= 1 &&
            max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) && n_blocks >= 1;
 }
 

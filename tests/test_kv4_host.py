@@ -45,7 +45,7 @@ def _logprobs(L, **kw):
 
 
 SIZES = [dict(n_kv=0), dict(n_q=31), dict(n_q=72), dict(T=-1), dict(tables=None), dict(n_slots=0), dict(max_blocks=0),
-         dict(max_blocks=(1 << 20) + 1), dict(kv=None), dict(kv=ODD), dict(n_blocks=0)]
+         dict(max_blocks=(1 << 20) + 1), dict(kv=None), dict(kv=ODD), dict(n_blocks=0), dict(T=1 << 28)]
 
 
 @pytest.mark.parametrize("bad", SIZES + [

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(AW * 32, 4) kv4_decode_kernel(const Kv4DecodeA
     grid_dep_wait();
 
     const int slot = a.row_slot[t];
-    int ctx = a.row_pos[t] + 1;
+    int ctx = min(a.row_pos[t], 0x7ffffffe) + 1;
     if (ctx > 0 && (slot < 0 || slot >= a.n_slots || ctx > a.max_blocks * 32)) {
         if (rank == 0 && threadIdx.x == 0) report(a.status, Q3_STATUS_BLOCK_RANGE);
         ctx = 0;

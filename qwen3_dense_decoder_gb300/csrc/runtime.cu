@@ -1844,7 +1844,7 @@ int q3_session_score(q3_session* s, const int32_t* tokens_dev, int n, int n_scor
     q3_model* m = s->pool->m;
     if (top_k < 0 || top_k > m->c.vocab || top_k > Q3_LOGPROB_MAX_TOP)
         return fail(Q3_ERR_INVALID_ARG, "score: top_k outside [0, %d]", Q3_LOGPROB_MAX_TOP);
-    if (s->pos + n > m->c.max_ctx)
+    if (n > m->c.max_ctx - s->pos)
         return fail(Q3_ERR_CTX_OVERFLOW, "position %d + %d exceeds max_ctx %d", s->pos, n, m->c.max_ctx);
     if (m->poisoned) return fail(Q3_ERR_POISONED, "model poisoned by an earlier error");
     if (!m->score_logits) {
@@ -2349,8 +2349,9 @@ namespace {
 // what the three cache operators share: heads, tables, pool
 bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int max_blocks, const void* kv, int n_blocks)
 {
-    return T >= 0 && n_kv >= 1 && n_kv <= 4096 && (int64_t)T * n_kv <= 0x7fffffff && n_q >= 1 && n_q <= 8 * n_kv && n_q % n_kv == 0 && tables && n_slots >= 1 &&
-           max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) && n_blocks >= 1;
+    return T >= 0 && n_kv >= 1 && n_kv <= 4096 && (int64_t)T * n_kv <= 0x7fffffff && n_q >= 1 && n_q <= 8 * n_kv &&
+           n_q % n_kv == 0 && tables && n_slots >= 1 && max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) &&
+           n_blocks >= 1;
 }
 
 bool row_stride_ok(int64_t stride, int type, int64_t width)

@@ -249,7 +249,7 @@ def test_decode_attention_rows_share_a_slot_and_strides(q3):
 def test_decode_attention_reports_bad_places(q3):
     q, kv, tables, pos = _decode_case(32, 8, [70, 70], "f16", 93)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    for bad in (dict(t=kv.shape[0]), dict(t=-1), dict(s=2), dict(s=-1), dict(p=tables.shape[1] * 32)):
+    for bad in (dict(t=kv.shape[0]), dict(t=-1), dict(s=2), dict(s=-1), dict(p=tables.shape[1] * 32), dict(p=2 ** 31 - 1)):
         t, s, p = tables.copy(), np.arange(2, dtype=np.int32), pos.copy()
         if "t" in bad:
             t[1, 1] = bad["t"]

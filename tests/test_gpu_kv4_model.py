@@ -258,6 +258,8 @@ def test_score_refusals_and_bad_targets():
         s.score(torch.zeros(65, dtype=torch.int32, device="cuda"))
     assert e.value.code == -5
     assert s.pos == 0
+    s.score(toks[:1])
+    assert q3.lib().q3_session_score(s.h, toks.data_ptr(), 2 ** 31 - 1, 1, None, 0, None, None, None, None) == -5
     t[3] = shape.vocab
     s.score(toks, t)
     with pytest.raises(q3.Q3Error) as e:

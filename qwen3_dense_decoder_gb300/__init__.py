@@ -309,30 +309,27 @@ def op_prefill_attention(q: torch.Tensor, kv: torch.Tensor, table: torch.Tensor,
 
 KV4_TILE = 2560
 LOGPROB_MAX_TOP = 32
-_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-def _launch(name: str, fn, stream, tensors, *args) -> None:
-    """fn(*args, stream) with the tensors' device current.  On a stream other
-    than the current one the tensors are kept from reuse until it is done."""
-    i = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != i or i < 0):
-            raise ValueError(f"{name}: tensors must be on one CUDA device")
-    if torch.cuda.current_device() != i:
-        with torch.cuda.device(i):
-            return _launch(name, fn, stream, tensors, *args)
-    raw = torch._C._cuda_getCurrentRawStream(i)
-    if stream is not None and stream.cuda_stream != raw:
-        if stream.device_index != i:
-            raise ValueError(f"{name}: the stream is another device's")
-        raw = stream.cuda_stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    rc = fn(*args, raw)
-    if rc:
-        _check(rc)
+_native = None
+
+
+def _op(name: str):
+    """The operator `name` of the extension module (csrc/bind.cpp), which checks
+    its arguments, allocates outputs and calls libq3.so; raises if it has not been built."""
+    global _native
+    if _native is None:
+        L = lib()
+        try:
+            from . import _ops
+        except ImportError as e:
+            raise RuntimeError("_ops is missing: build it with qwen3_dense_decoder_gb300.build()") from e
+        address = [C.cast(f, C.c_void_p).value for f in (L.q3_op_kv4_append, L.q3_op_kv4_decode_attention,
+                                                         L.q3_op_kv4_prefill_attention, L.q3_kv4_prefill_workspace,
+                                                         L.q3_op_token_logprobs)]
+        _ops.init(_check, *address)
+        _native = _ops
+    return getattr(_native, name)
 
 
 def check_status(status: torch.Tensor) -> None:
@@ -348,34 +345,12 @@ def _int32(name: str, what: str, t: torch.Tensor, shape: tuple) -> None:
         raise ValueError(f"{name}: {what} must be contiguous int32 {list(shape)}")
 
 
-def _kv4_pool(name: str, kv: torch.Tensor, tables: torch.Tensor, status) -> None:
-    if kv.dtype != torch.uint8 or kv.dim() != 4 or kv.shape[1] != 2 or kv.shape[3] != KV4_TILE or not kv.is_contiguous():
-        raise ValueError(f"{name}: kv must be contiguous uint8 [n_blocks, 2, n_kv, {KV4_TILE}]")
-    if tables.dtype != torch.int32 or tables.dim() != 2 or not tables.is_contiguous():
-        raise ValueError(f"{name}: tables must be contiguous int32 [n_slots, max_blocks]")
-    if status is not None:
-        _int32(name, "status", status, (1,))
-
-
-def _rows(name: str, q: torch.Tensor, types: tuple) -> None:
-    if q.dtype not in types or q.dim() != 3 or q.shape[2] != 128 or q.stride(2) != 1 or (q.stride(1) != 128 and q.shape[1] > 1):
-        raise ValueError(f"{name}: q must be [T, n_q, 128] of {types} with contiguous rows")
-
-
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """Memory of the stream that writes it: none of its earlier uses can still be running."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _out(name: str, out, shape: tuple, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    if out is None:
-        return _new(shape, dtype, like, stream)
-    if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
-        raise ValueError(f"{name}: outputs must be contiguous {dtype} {list(shape)}")
-    return out
 
 
 def _p(t):
@@ -399,31 +374,7 @@ def op_kv4_append(qkv: torch.Tensor, q_gain: torch.Tensor, k_gain: torch.Tensor,
     n_kv, 2560]) at each row's position and slot.  rope: rope_table's; a row
     of negative position is padding.  kv_out: fp16 [T, 2, n_kv, 128], if given,
     receives the values the cache then holds."""
-    name = "op_kv4_append"
-    _kv4_pool(name, kv, tables, status)
-    n_blocks, _, n_kv, _ = kv.shape
-    width = (n_q + 2 * n_kv) * 128
-    if qkv.dtype not in _TYPES or qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
-        raise ValueError(f"{name}: qkv must be f32, fp16 or bf16 [T, (n_q + 2 n_kv) * 128]")
-    T = qkv.shape[0]
-    for g in (q_gain, k_gain):
-        if g.dtype != torch.bfloat16 or g.shape != (128,) or not g.is_contiguous():
-            raise ValueError(f"{name}: gains must be bf16 [128]")
-    if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[1:] != (64, 2) or not rope.is_contiguous():
-        raise ValueError(f"{name}: rope must be f32 [n, 64, 2]")
-    _int32(name, "row_pos", row_pos, (T,))
-    _int32(name, "row_slot", row_slot, (T,))
-    q_out = _out(name, q_out, (T, n_q, 128), torch.float16, qkv, stream)
-    if kv_out is not None:
-        _out(name, kv_out, (T, 2, n_kv, 128), torch.float16, qkv, stream)
-    if T == 0:
-        return q_out
-    _launch(name, lib().q3_op_kv4_append, stream,
-            (qkv, q_gain, k_gain, rope, row_pos, row_slot, tables, kv, q_out, kv_out, status),
-            qkv.data_ptr(), _TYPES[qkv.dtype], qkv.stride(0) if T > 1 else width, q_gain.data_ptr(), k_gain.data_ptr(), eps,
-            rope.data_ptr(), rope.shape[0], row_pos.data_ptr(), row_slot.data_ptr(), T, n_q, n_kv, tables.data_ptr(),
-            tables.shape[0], tables.shape[1], kv.data_ptr(), n_blocks, q_out.data_ptr(), _p(kv_out), _p(status))
-    return q_out
+    return _op("kv4_append")(qkv, q_gain, k_gain, rope, row_pos, row_slot, tables, kv, n_q, eps, q_out, kv_out, status, stream)
 
 
 def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: torch.Tensor, tables: torch.Tensor,
@@ -434,20 +385,7 @@ def op_kv4_decode_attention(q: torch.Tensor, row_pos: torch.Tensor, row_slot: to
     128], fp16 unless out is f32.  A row of negative position gives zeros.
     max_ctx: the longest context expected (0: what the tables hold); it chooses
     the split of the work only."""
-    name = "op_kv4_decode_attention"
-    _kv4_pool(name, kv, tables, status)
-    _rows(name, q, (torch.float32, torch.float16))
-    T, n_q, _ = q.shape
-    _int32(name, "row_pos", row_pos, (T,))
-    _int32(name, "row_slot", row_slot, (T,))
-    out = _out(name, out, (T, n_q, 128), torch.float32 if out is not None and out.dtype == torch.float32 else torch.float16, q, stream)
-    if T == 0:
-        return out
-    _launch(name, lib().q3_op_kv4_decode_attention, stream, (q, row_pos, row_slot, tables, kv, out, status),
-            q.data_ptr(), _TYPES[q.dtype], q.stride(0) if T > 1 else n_q * 128, row_pos.data_ptr(), row_slot.data_ptr(), T, n_q,
-            kv.shape[2], tables.data_ptr(), tables.shape[0], tables.shape[1], max_ctx, kv.data_ptr(), kv.shape[0], out.data_ptr(),
-            _TYPES[out.dtype], _p(status))
-    return out
+    return _op("kv4_decode_attention")(q, row_pos, row_slot, tables, kv, max_ctx, out, status, stream)
 
 
 def kv4_prefill_workspace(ns: int, T: int, n_q: int, n_kv: int, max_blocks: int, n_blocks: int) -> int:
@@ -467,29 +405,7 @@ def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: t
     cache already holds.  Returns fp16 [T, n_q, 128]; rows of no sequence keep
     what out held.  workspace: uint8, kv4_prefill_workspace bytes (default:
     allocated here)."""
-    name = "op_kv4_prefill_attention"
-    _kv4_pool(name, kv, tables, status)
-    _rows(name, q, (torch.float16,))
-    n_blocks, _, n_kv, _ = kv.shape
-    T, n_q, _ = q.shape
-    ns = seq_pos.shape[0]
-    _int32(name, "seq_rows", seq_rows, (ns + 1,))
-    _int32(name, "seq_pos", seq_pos, (ns,))
-    if seq_slot is not None:
-        _int32(name, "seq_slot", seq_slot, (ns,))
-    out = _out(name, out, (T, n_q, 128), torch.float16, q, stream)
-    if T == 0 or ns == 0:
-        return out
-    need = kv4_prefill_workspace(ns, T, n_q, n_kv, tables.shape[1], n_blocks)
-    if workspace is None:
-        workspace = _new(need, torch.uint8, q, stream)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError(f"{name}: workspace must be contiguous uint8, at least {need} bytes")
-    _launch(name, lib().q3_op_kv4_prefill_attention, stream, (q, seq_rows, seq_pos, seq_slot, tables, kv, out, workspace, status),
-            q.data_ptr(), q.stride(0) if T > 1 else n_q * 128, seq_rows.data_ptr(), seq_pos.data_ptr(), _p(seq_slot), ns, T, n_q,
-            n_kv, tables.data_ptr(), tables.shape[0], tables.shape[1], kv.data_ptr(), n_blocks, out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _p(status))
-    return out
+    return _op("kv4_prefill_attention")(q, seq_rows, seq_pos, tables, kv, seq_slot, out, workspace, status, stream)
 
 
 def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0,
@@ -499,26 +415,7 @@ def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None,
     gives 0), the entropy in nats (f32 [N]), and the top_k most probable tokens
     in order, lowest index first among equals (int32 [N, top_k]), with their
     log probabilities (f32 [N, top_k])."""
-    name = "op_token_logprobs"
-    if logits.dtype not in _TYPES or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError(f"{name}: logits must be f32, fp16 or bf16 [N, V] with contiguous rows")
-    N, V = logits.shape
-    if targets is not None:
-        _int32(name, "targets", targets, (N,))
-    if status is not None:
-        _int32(name, "status", status, (1,))
-    if top_k < 0:
-        raise ValueError(f"{name}: top_k must not be negative")
-    logprob = None if targets is None else _new(N, torch.float32, logits, stream)
-    entropy = _new(N, torch.float32, logits, stream)
-    ids = _new((N, top_k), torch.int32, logits, stream)
-    values = _new((N, top_k), torch.float32, logits, stream)
-    if N == 0:
-        return logprob, entropy, ids, values
-    _launch(name, lib().q3_op_token_logprobs, stream, (logits, targets, logprob, entropy, ids, values, status),
-            logits.data_ptr(), _TYPES[logits.dtype], logits.stride(0) if N > 1 else V, N, V, _p(targets), top_k, _p(logprob),
-            entropy.data_ptr(), ids.data_ptr(), values.data_ptr(), _p(status))
-    return logprob, entropy, ids, values
+    return _op("token_logprobs")(logits, targets, top_k, status, stream)
 
 
 class Model:

@@ -3,21 +3,26 @@
 Each translation unit under csrc/ compiles in parallel for
 ``-gencode arch=compute_103a,code=sm_103a``; the objects link into one shared
 library with the CUDA runtime linked statically, so the library loads on a
-host without a GPU (the CPU tests check its exported symbols).
+host without a GPU (the CPU tests check its exported symbols).  The host
+compiler builds csrc/bind.cpp, the asynchronous operators' Python side, into
+the extension module _ops beside it.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq3.so")
+OPS = os.path.join(HERE, "_ops.so")
 
 SOURCES = ["runtime.cu", "k_gemm.cu", "k_gemv.cu", "k_attn.cu", "k_attn_prefill.cu", "k_misc.cu",
            "noalloc.cu", "k_decode.cu", "k_attn_tc.cu", "k_gemv_a4.cu",
@@ -40,9 +45,26 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def compile_ops() -> None:
+    """csrc/bind.cpp into _ops.so, against the headers and libraries of the torch that will load it."""
+    torch = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin))
+    libs = os.path.join(torch, "lib")
+    includes = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+                sysconfig.get_paths()["include"]]
+    tmp = OPS + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+           *(x for d in includes for x in ("-isystem", d)), os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+           "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile csrc/*.cu into libq3.so (skipped when up to date)."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    """Compile csrc/*.cu into libq3.so and csrc/bind.cpp into _ops.so (skipped when up to date)."""
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, OPS)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -58,8 +80,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ops = ex.submit(compile_ops)
         objs = list(ex.map(compile_one, SOURCES))
+        ops.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

@@ -116,6 +116,8 @@ def test_binding_refuses_before_the_library():
         lambda: q3.op_token_logprobs(qkv.t()),
         lambda: q3.op_token_logprobs(qkv, row[:2]),
         lambda: q3.op_token_logprobs(qkv, row),                                                      # CPU tensors
+        lambda: q3.op_token_logprobs([1.0, 2.0]),
+        lambda: q3.op_token_logprobs(qkv, top_k=1 << 40),
     ]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError):

@@ -58,7 +58,7 @@ Q3_DEV void load4(const __half* p, int lane, float (&y)[4]) {
 // four heads at once.  A head's value costs about half an instruction (q) to
 // one (k); the bytes are (n_q + 2 n_kv) 128 projections in, 2 bytes a q value
 // and 0.625 a k or v value out.  2,048 rows of 48 heads in f32: 18.8 us, 4.2 TB/s
-// of those bytes (a warp a head took 29.7); 32 rows: 3.1 us, latency.
+// of those bytes (a warp a head took 29.7); 32 rows: 2.9 us, latency.
 Q3_DEV void load8(const float* p, float* y) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w; y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 //
 // tcgen05 would want the expanded values in shared memory, 256 bytes where 80 come
 // in, for at most eight columns.  8 rows of 16,384 positions (40/8 heads): 43 us,
-// 3.9 TB/s, bound by the instructions that unpack; 32 rows of 1,184 (32/8): 20.6 us;
-// one row of 2,176: 6.7 us, latency.
+// 3.9 TB/s, bound by the instructions that unpack; 32 rows of 129 to 2,239 (32/8):
+// 20.4 us; one row of 2,176: 6.3 us, latency.
 constexpr int AW = 4;
 constexpr int STAGES = 2;
 constexpr int KV4_STAGE = 2 * KV4_TILE;

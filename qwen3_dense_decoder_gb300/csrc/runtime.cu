@@ -2354,6 +2354,12 @@ bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int
            n_blocks >= 1;
 }
 
+// A programmatic launch: a call's set-up overlaps the end of the kernel before it on
+// the stream, whichever that is, and the call's kernels wait for that one before they
+// read or write (calls in a row: one decode row 8.3 -> 6.4 us, a 701-row ragged prefill
+// 20.6 -> 18.0).
+Launch op_launch(void* stream) { return Launch{static_cast<cudaStream_t>(stream), true, nullptr}; }
+
 bool row_stride_ok(int64_t stride, int type, int64_t width)
 {
     return stride >= width && stride % (type == Q3_TYPE_F32 ? 4 : 8) == 0;
@@ -2389,7 +2395,7 @@ int q3_op_kv4_append(const void* qkv_dev, int qkv_type, int64_t qkv_stride, cons
     a.kv = static_cast<uint8_t*>(kv_dev); a.n_blocks = n_blocks;
     a.q_out = static_cast<f16*>(q_out_dev); a.kv_out = static_cast<f16*>(kv_out_dev);
     a.status = status_dev;
-    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const Launch L = op_launch(stream);
     const cudaError_t e = launch_kv4_append(L, a, qkv_type);
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_append: %s", cudaGetErrorString(e));
     return Q3_OK;
@@ -2418,7 +2424,7 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
     a.max_ctx = max_ctx ? max_ctx : 32 * max_blocks;
     a.kv = static_cast<const uint8_t*>(kv_dev); a.n_blocks = n_blocks;
     a.out = out_dev; a.status = status_dev;
-    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const Launch L = op_launch(stream);
     const cudaError_t e = launch_kv4_decode(L, a, q_type, out_type);
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_decode_attention: %s", cudaGetErrorString(e));
     return Q3_OK;
@@ -2462,7 +2468,7 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
     int dev = 0, n_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return fail(Q3_ERR_CUDA, "op_kv4_prefill_attention: no CUDA device");
-    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const Launch L = op_launch(stream);
     const cudaError_t e = run_kv4_prefill(L, a, static_cast<uint8_t*>(workspace_dev), n_sm);
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_kv4_prefill_attention: %s", cudaGetErrorString(e));
     return Q3_OK;
@@ -2487,7 +2493,7 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
     a.targets = targets_dev; a.logprob = logprob_dev; a.entropy = entropy_dev;
     a.top_ids = top_ids_dev; a.top_logprob = top_logprob_dev;
     a.status = status_dev;
-    const Launch L{static_cast<cudaStream_t>(stream), false, nullptr};
+    const Launch L = op_launch(stream);
     const cudaError_t e = launch_logprobs(L, a, type);
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_token_logprobs: %s", cudaGetErrorString(e));
     return Q3_OK;

@@ -462,3 +462,46 @@ def test_append_prefill_decode_together_captured_and_on_another_stream(q3):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(kv, kv3) and all(torch.equal(a, b) for a, b in zip(outs, got))
+
+
+def test_operators_follow_copies_and_other_streams_in_a_graph(q3):
+    """Calls captured behind a copy, behind a memset and behind another stream's work read what those wrote."""
+    n_q, n_kv, T = 32, 8, 40
+    g = torch.Generator(device="cuda").manual_seed(8)
+    gains = [(1 + 0.1 * torch.randn(D, generator=g, device="cuda")).bfloat16() for _ in range(2)]
+    rope = q3.rope_table(64, 1e6)
+    source = torch.randn(T, 48 * D, generator=g, device="cuda")
+    tables = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(T, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    qkv, kv = torch.empty_like(source), torch.empty(3, 2, n_kv, 2560, dtype=torch.uint8, device="cuda")
+    logits = torch.empty(T, 1000, device="cuda")
+    seed = torch.randn(T, 1000, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+
+    def steps():
+        kv.zero_()
+        qkv.copy_(source)
+        q = q3.op_kv4_append(qkv, *gains, rope, pos, zero, tables, kv, n_q)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            logits.copy_(seed)
+            logits.mul_(3.0)
+            rows = q3.op_kv4_prefill_attention(q, at, zero[:1], tables, kv)
+        one = q3.op_kv4_decode_attention(q[-1:], pos[-1:], zero[:1], tables, kv)
+        main.wait_stream(side)
+        return [q, rows, one, kv, *q3.op_token_logprobs(logits, zero, 3)]
+
+    want = [t.clone() for t in steps()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = steps()
+    for _ in range(3):
+        for t in (kv, qkv, logits):
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -102,8 +102,10 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abor
         }
     }
 }
+// By a whole warp, of one mind about the outcome: what follows needs all of its lanes
 Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, Smem& sm, int* status) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, &sm.abort, status);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_long(bar, parity, &sm.abort, status));
 }
 
 // A CTA's work: n items or pieces of items
@@ -272,7 +274,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
         int chunk = it.t0 * PER >> 5, now = entry(32 * chunk + lane), next = entry(32 * chunk + 32 + lane);
         if (!which) {
             const int b = k & 1;
-            if (k > 1 && !__all_sync(0xffffffffu, wait_bar(&sm.q_free[b], ((k >> 1) - 1) & 1, sm, status))) break;
+            if (k > 1 && !wait_bar(&sm.q_free[b], ((k >> 1) - 1) & 1, sm, status)) break;
             ++nq;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sm.q_full[b], 2 * p.rows_per_tile * G * 128);
@@ -293,7 +295,7 @@ Q3_DEV void load_role(const Kv4PrefillArgs& p, const CUtensorMap* tkv, const CUt
             if (n >= NS) {
                 if (which) ok = wait_bar(&sm.pv_done[0][slot], phase_before(n), sm, status) && wait_bar(&sm.pv_done[1][slot], phase_before(n), sm, status);
                 else ok = wait_bar(&sm.s_full[slot], phase_before(n), sm, status);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (!ok) break;
             }
             uint8_t* dst = (which ? sm.v[slot] : sm.k[slot]) + lane * 32 * 128;
             if (lane == 0) mbar_arrive_expect_tx(&ld[slot], KV_TILE);

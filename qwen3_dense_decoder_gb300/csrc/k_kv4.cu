@@ -268,14 +268,15 @@ Q3_DEV uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-// mbar_wait with an optional status word
+// mbar_wait by a whole warp, of one mind about the outcome (the products need all of
+// its lanes), with an optional status word
 Q3_DEV bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (global_ns() - t0 > Q3_WAIT_LIMIT_NS) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, global_ns() - t0 > Q3_WAIT_LIMIT_NS)) {
             report(status, Q3_STATUS_TIMEOUT);
             return false;
         }

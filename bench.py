@@ -71,7 +71,7 @@ def parse():
                     help="measure the other named shapes instead (one JSON line each; 0.6b, 8b-q8_0 "
                          "and 14b if none given; 14b-kvq8 is the 14B workload over the Q8_0 K/V cache)")
     ap.add_argument("--ncu-case", choices=("decode-4layer", "gemm-gateup", "attn-prefill", "attn-decode-b32",
-                                           "attn-decode-kvq8-b32", "gemv-a4", "prefill-2layer"),
+                                           "attn-decode-kvq8-b32", "gemv-a4", "prefill-2layer", "kv4-scoring"),
                     default=None,
                     help="run only a small case sized for an ncu capture (a few GB on the device) and exit")
     return ap.parse_args()
@@ -156,6 +156,33 @@ def ncu_case(name: str):
         for _ in range(4):
             m.eval_batch(ss, toks, [1] * B, lg, toks)
         m.sync()
+    elif name == "kv4-scoring":
+        # the 4-bit cache's operators and token scoring, three rounds: 2,048
+        # rows appended (32/8 heads), 512 rows attended after 10,240 positions
+        # and 8 rows of 16,384 (40/8 heads), 2,048 rows of 151,936 logits scored
+        g = torch.Generator(device="cuda")
+        g.manual_seed(9)
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        qkv = torch.randn(2048, 48 * 128, device="cuda", generator=g)
+        gain = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+        rope = q3.rope_table(16384, 1e6)
+        pos = torch.arange(2048, dtype=torch.int32, device="cuda")
+        # eight sessions' blocks in permuted order, filled through the writer
+        tables = torch.randperm(8 * 512, generator=g, device="cuda").to(torch.int32).view(8, 512)
+        kv = torch.zeros(8 * 512, 2, 8, q3.KV4_TILE, dtype=torch.uint8, device="cuda")
+        rows = torch.randn(16384, 24 * 128, device="cuda", generator=g)
+        places = torch.arange(16384, dtype=torch.int32, device="cuda")
+        for i in range(8):
+            q3.op_kv4_append(rows, gain, gain, rope, places, torch.full_like(places, i), tables, kv, 8)
+        q = torch.randn(512, 40, 128, device="cuda", generator=g).half()
+        logits = torch.randn(2048, 151936, device="cuda", generator=g) * 2
+        zero, ends = torch.zeros(2048, dtype=torch.int32, device="cuda"), ints([16383] * 8)
+        for _ in range(3):
+            q3.op_kv4_append(qkv, gain, gain, rope, pos, zero, tables, kv, 32)
+            q3.op_kv4_prefill_attention(q, ints([0, 512]), ints([10240]), tables, kv)
+            q3.op_kv4_decode_attention(q[:8], ends, ints(list(range(8))), tables, kv)
+            q3.op_token_logprobs(logits, zero, 5)
+        torch.cuda.synchronize()
     elif name == "gemv-a4":
         # the gate/up projection of a Qwen3-4B AFFINE4_GS32 decode step as one
         # operator call: 19,456 x 2,560 weights, 31 MB at 5.0 bits a weight

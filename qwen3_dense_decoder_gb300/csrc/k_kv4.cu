@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 //
 // tcgen05 would want the expanded values in shared memory, 256 bytes where 80 come
 // in, for at most eight columns.  8 rows of 16,384 positions (40/8 heads): 43 us,
-// 3.9 TB/s, bound by the instructions that unpack; 32 rows of 129 to 2,239 (32/8):
+// 3.9 TB/s, bound by the arithmetic pipes (unpacking, products, exponentials) with the
+// four warps a scheduler that 128 registers allow; 32 rows of 129 to 2,239 (32/8):
 // 20.4 us; one row of 2,176: 6.3 us, latency.
 constexpr int AW = 4;
 constexpr int STAGES = 2;

@@ -505,3 +505,28 @@ def test_operators_follow_copies_and_other_streams_in_a_graph(q3):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("default", [False, True])
+def test_operators_wait_for_events(q3, default):
+    """A call behind another call and an event of slow work elsewhere reads what that work wrote."""
+    other, here = torch.cuda.Stream(), torch.cuda.default_stream() if default else torch.cuda.Stream()
+    a = torch.randn(4096, 4096, device="cuda")
+    source, targets = torch.randn(64, 5000, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+    late = torch.empty_like(source)
+    want = q3.op_token_logprobs(source, targets, 4)
+    for _ in range(5):
+        late.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            b = a
+            for _ in range(6):
+                b = b @ a * 1e-2
+            late.copy_(source)
+            event = other.record_event()
+        with torch.cuda.stream(here):
+            q3.op_token_logprobs(source, targets, 4)
+            here.wait_event(event)
+            got = q3.op_token_logprobs(late, targets, 4)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))

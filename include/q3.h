@@ -430,7 +430,10 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
  * then V), 16-byte aligned: 32 positions of one KV head, each head row of 128
  * packed by the AFFINE4_GS32 rule straight from FP32 (q3_quantize_affine4's,
  * groups of 32 dimensions), 80 bytes a position and head.  A stored value is
- * fp16(scale * code + bias), rounded once.
+ * fp16(scale * code + bias), rounded once.  Attention's scores, softmax and
+ * sums are FP32; its weights enter the product with V as one fp16 in prefill
+ * (2^-11 relative) and as two in decode (2^-22), none finer than 2^-32 of the
+ * row's largest, so a sum over n positions may lose n 2^-32 of itself.
  *   K tile: 16 code bytes [position][group], dimension i of a group in bits
  *     4 i (low nibble first); from byte 2,048 fp16 (scale, bias)
  *     [position][group].

@@ -236,13 +236,14 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 //   O^T += V^T P^T  rows dimensions (a lane's word pairs two positions), columns
 //                 heads; the weights turn from the score fragment's layout into
 //                 B fragments by 8 x 8 transposes.
-// q and the weights enter as fp16 high and low parts (22 bits).  Up to four
+// q and the weights enter as fp16 high and low parts (22 bits, the weights' no finer
+// than 2^-32 of the largest; kv4.cuh).  Up to four
 // heads the two parts are columns 2h and 2h + 1 of one tile (c0 + c1 is the
 // result of one head in one lane); from five on the columns are eight heads and
 // the parts two products into the same accumulators.  An fp16 q has no low
 // part, so the wide form leaves its product out.
-// Softmax is online in base 2; O and the sums are rescaled only when a maximum
-// grows by more than 2^8 (the weights then reach 2^8, far inside fp16).
+// Softmax is online in base 2; O and the sums are rescaled only when a score passes
+// its reference by KV4_HIGH, 2^8 above the maximum that set it.
 //
 // Splits of a (row, KV head) are one cluster; warps merge in order through
 // shared memory, CTAs in order through distributed shared memory.
@@ -255,7 +256,6 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 constexpr int AW = 4;
 constexpr int STAGES = 2;
 constexpr int KV4_STAGE = 2 * KV4_TILE;
-constexpr float LAZY = 8.0f;
 
 Q3_DEV void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -308,7 +308,7 @@ Q3_DEV void load_q(const Tq* q, bool low, uint32_t (&b)[16], bool& bad) {
 template <bool WIDE>
 struct Attend {
     static constexpr int NH = WIDE ? 2 : 1;
-    float m[NH], l[NH];        // running maximum and this lane's part of the sum
+    float m[NH], l[NH];        // the weights' reference (kv4.cuh) and this lane's part of the sum
     float o[8][4];             // O^T: row tile 2 g + h holds dimensions 32 g + 4 (lane / 4) + 2 h, + 1
 };
 
@@ -363,15 +363,15 @@ Q3_DEV void attend_block(const uint8_t* kt, const uint8_t* vt, const uint32_t (&
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
         mx[h] = fmaxf(fmaxf(s[h][0], s[h][1]), fmaxf(s[h][2], s[h][3]));
-        grow = grow || mx[h] > w.m[h] + LAZY;
+        grow = grow || mx[h] > w.m[h] + KV4_HIGH;
     }
-    if (__any_sync(0xffffffffu, grow)) {                 // every lane of a head takes the head's maximum
+    if (__any_sync(0xffffffffu, grow)) {                 // every lane of a head takes the head's reference
         float alpha[NH];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
-            const float mn = fmaxf(w.m[h], mx[h]);
+            const float mn = fmaxf(w.m[h], mx[h] - KV4_BELOW);
             alpha[h] = fast_ex2(w.m[h] - mn);            // 0 at first
             w.m[h] = mn;
             w.l[h] *= alpha[h];

@@ -2,29 +2,30 @@
 // cache on the tcgen05 tensor cores.  kv4_expand_kernel (k_kv4.cu) leaves an
 // fp16 copy of the sequences' blocks and a list of query tiles, longest context
 // first; a stored value is an fp16 number and q arrives in fp16, so both
-// products run on single fp16 operands and only the softmax weights are rounded
-// (once, to fp16).
+// products run on single fp16 operands and only the softmax weights are rounded (once,
+// to fp16: 11 bits, no finer than 2^-32 of the largest).
 //
 // Work item: R = 128 / G consecutive positions of one sequence for the G query
 // heads of one KV head, as an MMA tile of 128 rows (row r = position r / G, head
 // r % G).  Its context is walked in steps of 128 positions, half h of the CTA taking
-// positions 64 h .. 64 h + 64 of each, with its own running maximum, sum and output;
+// positions 64 h .. 64 h + 64 of each, with its own reference, sum and output;
 // the halves are joined at an item's end.
 //   S = Q K^T       tcgen05.mma, Q and K from shared memory, FP32 in tensor memory; both
 //                   halves' 64 columns at once (64 alone take the time of 128)
-//   P = 2^(S c - m) one thread a row, so nothing is exchanged; written over S
+//   P = 2^(S c - m) one thread a row, so nothing is exchanged; written over S.  m is the
+//                   weights' reference, under the row's maximum (kv4.cuh)
 //   O_h += P V      P from tensor memory, V read MN-major from shared memory
 // A step's scores are made while the last one's weights are, and the halves'
 // exponentials overlap each other and the products.  (A row shared by two threads
 // spent 480 of 2,300 cycles a step on its maximum; scores issued only after the
 // product before them left the softmax waiting for 1,600; one warp issuing both
 // products took 1,550 cycles for 64 positions, with its commits, against the 512 they
-// run.)  Maxima are raised lazily: O and the sum are rescaled only when one grows by
-// more than 2^8.
+// run.)  References are raised lazily: O and the sum are rescaled only when a score
+// passes its own by KV4_HIGH, 2^8 above the maximum that set it.
 //
 // Items are dealt whole, longest first, where that comes out about even.  Else they
 // are cut: the items in a row, their steps are shared out evenly, a CTA's share may
-// begin and end inside an item, and a cut item's pieces leave maximum, sum and FP32
+// begin and end inside an item, and a cut item's pieces leave reference, sum and FP32
 // output in the workspace, where the warp that finishes a row range last joins them
 // in order.  Cut where fewer than three items a CTA would take the longest CTA 12 steps
 // more than an even share.  (Dealt and cut: 512 rows after 10,240 positions, 40/8
@@ -49,6 +50,7 @@
 // is bounded; a timeout sets the status word and the CTA winds down.
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace q3 {
 
@@ -63,7 +65,6 @@ constexpr int NS = 2;                        // slots
 constexpr int S_WARP = 8, PV_WARP = 9, K_WARP = 10;        // V: K_WARP + 1
 constexpr int THREADS = 12 * 32;
 constexpr uint32_t T_S = 0, T_O = 256;
-constexpr float LAZY = 8.0f;
 constexpr int PART = (int)(KV4_PART_BYTES / 16);
 
 struct alignas(1024) Smem {
@@ -75,7 +76,7 @@ struct alignas(1024) Smem {
     uint64_t k_load[NS], v_load[NS], s_full[NS], p_full[2][NS], pv_done[2][NS];
     uint64_t q_full[2], q_free[2];           // by item
     uint64_t ml_done[2], o_free, drain[2];
-    float2 ml[2][128];                       // the halves' maxima and sums
+    float2 ml[2][128];                       // the halves' references and sums
     int2 cut[2];                             // where this CTA's share begins and ends: item, step
     uint32_t tmem;
     int abort;
@@ -409,10 +410,10 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
                 mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31])), __uint_as_float(v[e >> 5][(e & 31) + 1]));
-            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale);
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale - KV4_BELOW);
             if (t == it.t0) {
                 m = mn;
-            } else if (__any_sync(0xffffffffu, valid && mn > m + LAZY)) {
+            } else if (__any_sync(0xffffffffu, valid && mn > m + (KV4_HIGH - KV4_BELOW))) {
                 // O, complete up to this half's last step, and l rescale; rows that
                 // have seen nothing (all of the half's positions are later ones)
                 // stay as they are
@@ -454,7 +455,7 @@ Q3_DEV void softmax_role(const Kv4PrefillArgs& p, Smem& sm, uint32_t tmem, const
             const float2 a = halves_of(add2(sum[0], sum[1]));
             l += a.x + a.y;
         }
-        // The halves tell each other their maxima and sums, once both have read the last
+        // The halves tell each other their references and sums, once both have read the last
         // item's.  Half 0 writes an item's output while half 1 goes on; a piece, whose
         // join takes longer, they write 64 columns each.
         const bool whole = it.t1 - it.t0 == it.steps;

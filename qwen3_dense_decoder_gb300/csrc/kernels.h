@@ -373,7 +373,7 @@ cudaError_t launch_kv4_decode(const Launch& L, const Kv4DecodeArgs& a, int q_typ
 // KV4_MIN_PIECE steps.
 constexpr int KV4_STEP = 128, KV4_PREFILL_CTAS = 152, KV4_CUT = 3, KV4_TILE_COST = 1, KV4_MIN_SHARE = 4, KV4_MIN_PIECE = 2,
               KV4_JOIN_COST = 12;
-constexpr size_t KV4_PART_BYTES = 128 * (128 + 4) * sizeof(float);   // output, maximum and sum (by half) of 128 rows
+constexpr size_t KV4_PART_BYTES = 128 * (128 + 4) * sizeof(float);   // output, reference and sum (by half) of 128 rows
 
 // Causal attention of sequences of rows: sequence i is rows seq_rows[i] ..
 // seq_rows[i + 1] at positions seq_pos[i] .. of slot seq_slot[i].

@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(THREADS, 4) logprobs_kernel(const LogprobArgs 
 
     const float logs = logf(sums.s);
     const bool empty = sums.m == -INFINITY && sums.s == 0.f;         // every token ruled out
-    const float lse = empty ? -INFINITY : sums.m + logs;
-    auto lp = [&](float v) { return empty ? -INFINITY : v - lse; };
+    // m + log s would round at the size of m: 4e-3 where logits lie near 60,000
+    auto lp = [&](float v) { return empty ? -INFINITY : (v - sums.m) - logs; };
     if (lane == 0) {
         if (a.entropy) a.entropy[r] = empty ? 0.f : logs - sums.t / sums.s;
         if (a.logprob) {

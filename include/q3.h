@@ -498,7 +498,9 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
  * aligned, needing no preparation; calls that may overlap on the GPU take one
  * each.  Status: Q3_STATUS_BLOCK_RANGE (a table entry outside the pool: its
  * positions count as zeros; a slot, or a sequence longer than its table: the
- * sequence's rows are zeros), Q3_STATUS_F16_RANGE, Q3_STATUS_TIMEOUT.
+ * sequence's rows are zeros), Q3_STATUS_F16_RANGE (a result is not a finite
+ * fp16 number, or a V value that a sequence holds is not: it counts as zero,
+ * and rows before its position are as without it), Q3_STATUS_TIMEOUT.
  * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32_t* seq_rows_dev,
                                 const int32_t* seq_pos_dev, const int32_t* seq_slot_dev, int ns, int T, int n_q,

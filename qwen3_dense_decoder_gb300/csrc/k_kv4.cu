@@ -665,8 +665,11 @@ cudaError_t launch_decode(const Launch& L, const Kv4DecodeArgs& a)
 // are expanded once, into an fp16 copy that the tcgen05 kernel (k_kv4_prefill.cu)
 // fetches with TMA: 80 + 256 bytes a position and head against 512 flop a row
 // and position.  A warp expands half a tile at a time, all its loads first: 4-byte
-// code words in, 16-byte words out, both coalesced.  Places at or past the
-// sequence's end hold whatever the pool holds, made finite (their weights are zero).
+// code words in, 16-byte words out, both coalesced.  A V value that is not finite
+// becomes zero, for a row's weight of a position that it does not attend is zero and the
+// product with an infinity would not be; it is reported where a sequence's place holds
+// it (places past a sequence's end hold whatever the pool holds).  K needs no such care:
+// a score of a position that is not attended is replaced, whatever it is.
 //
 // CTA 0 lists the query tiles meanwhile.  Enough of them, longest context first: a
 // counting sort by context in 1,024 classes (order within a class does not matter).
@@ -814,16 +817,22 @@ Q3_DEV void plan_tiles(const Kv4PrefillArgs& a) {
     }
 }
 
-// infinities and NaN of an fp16 pair become zeros
-Q3_DEV uint32_t finite_pair(uint32_t v) {
+// infinities and NaN of fp16 pairs become zeros; whether there were any
+Q3_DEV bool make_finite(uint32_t& v) {
+    const uint32_t was = v;
     if ((v & 0x7c00u) == 0x7c00u) v &= 0xffff0000u;
     if ((v & 0x7c000000u) == 0x7c000000u) v &= 0xffffu;
-    return v;
+    return v != was;
+}
+Q3_DEV bool make_finite(uint4& v) {
+    bool any = make_finite(v.x);
+    any |= make_finite(v.y);
+    any |= make_finite(v.z);
+    return any | make_finite(v.w);
 }
 
-// 16 positions of a tile: codes and parameters at src, fp16 rows at dst; places from
-// n_pos on made finite
-Q3_DEV void expand_k(const uint8_t* codes, const uint8_t* params, __half* dst, int n_pos, uint32_t magic, int lane) {
+// 16 positions of a tile: codes and parameters at src, fp16 rows at dst
+Q3_DEV void expand_k(const uint8_t* codes, const uint8_t* params, __half* dst, uint32_t magic, int lane) {
     const int c = lane & 15, p0 = lane >> 4;             // two positions a step, eight dimensions a lane
     uint32_t w[8], sb[8];
 #pragma unroll
@@ -836,13 +845,14 @@ Q3_DEV void expand_k(const uint8_t* codes, const uint8_t* params, __half* dst, i
         const __half2 sc = __low2half2(as_h2(sb[k])), bi = __high2half2(as_h2(sb[k]));
         const uint32_t v0 = kv4_pair<0>(w[k], sc, bi, magic), v1 = kv4_pair<1>(w[k], sc, bi, magic), v2 = kv4_pair<2>(w[k], sc, bi, magic),
                        v3 = kv4_pair<3>(w[k], sc, bi, magic);
-        uint4 o = make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632),
-                             __byte_perm(v2, v3, 0x7632));
-        if (2 * k + p0 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+        const uint4 o = make_uint4(__byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410), __byte_perm(v0, v1, 0x7632),
+                                   __byte_perm(v2, v3, 0x7632));
         *reinterpret_cast<uint4*>(dst + (2 * k + p0) * D + c * 8) = o;
     }
 }
-Q3_DEV void expand_v(const uint8_t* codes, const uint8_t* params, __half* dst, int n_pos, uint32_t magic, int lane) {
+// true if one of the first n_pos positions held a value that is not finite
+Q3_DEV bool expand_v(const uint8_t* codes, const uint8_t* params, __half* dst, int n_pos, uint32_t magic, int lane) {
+    bool lost = false;
     const int gr = (lane & 15) >> 2, m = lane & 3, pr0 = lane >> 4;      // two position pairs a step
     uint32_t w0[4], w1[4];
     uint2 sb[4];
@@ -863,12 +873,18 @@ Q3_DEV void expand_v(const uint8_t* codes, const uint8_t* params, __half* dst, i
                        r3 = kv4_pair<3>(w1[k], sc, bi, magic);
         uint4 e = make_uint4(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410), __byte_perm(r0, r1, 0x5410), __byte_perm(r2, r3, 0x5410));
         uint4 o = make_uint4(__byte_perm(p0, p1, 0x7632), __byte_perm(p2, p3, 0x7632), __byte_perm(r0, r1, 0x7632), __byte_perm(r2, r3, 0x7632));
-        if (2 * pr >= n_pos) e = make_uint4(finite_pair(e.x), finite_pair(e.y), finite_pair(e.z), finite_pair(e.w));
-        if (2 * pr + 1 >= n_pos) o = make_uint4(finite_pair(o.x), finite_pair(o.y), finite_pair(o.z), finite_pair(o.w));
+        // a group's values lie between its bias and 15 scale + bias: where both are finite, all are
+        const __half2 top = __hfma2(sc, __float2half2_rn(15.0f), bi);
+        if (((as_u32(bi) & 0x7c00u) == 0x7c00u) | ((as_u32(bi) & 0x7c000000u) == 0x7c000000u) | ((as_u32(top) & 0x7c00u) == 0x7c00u) |
+            ((as_u32(top) & 0x7c000000u) == 0x7c000000u)) {
+            lost |= make_finite(e) & (2 * pr < n_pos);
+            lost |= make_finite(o) & (2 * pr + 1 < n_pos);
+        }
         uint4* to = reinterpret_cast<uint4*>(dst + 2 * pr * D + 32 * gr + 8 * m);
         to[0] = e;
         to[D / 8] = o;
     }
+    return lost;
 }
 
 __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
@@ -909,8 +925,8 @@ __global__ void __launch_bounds__(XT) kv4_expand_kernel(const Kv4PrefillArgs a)
             const uint8_t* src = a.kv + ((size_t)phys * 2 * a.n_kv + part) * KV4_TILE;
             __half* dst = a.copy + ((size_t)(a.by_seq ? (i0 + from) * a.max_blocks + j : phys) * 2 * a.n_kv + part) * (32 * D) + half * 16 * D;
             const int n_pos = end - 32 * j - 16 * half;
-            if (part < a.n_kv) expand_k(src + half * 1024, src + KV4_CODES + half * 256, dst, n_pos, a.magic, lane);
-            else expand_v(src + half * 1024, src + KV4_CODES + half * 256, dst, n_pos, a.magic, lane);
+            if (part < a.n_kv) expand_k(src + half * 1024, src + KV4_CODES + half * 256, dst, a.magic, lane);
+            else if (expand_v(src + half * 1024, src + KV4_CODES + half * 256, dst, n_pos, a.magic, lane)) report(a.status, Q3_STATUS_F16_RANGE);
         }
         base += all;
     }

@@ -477,8 +477,9 @@ int q3_op_kv4_append(const void* qkv_dev, int qkv_type, int64_t qkv_stride, cons
  * only chooses how contexts are split over the GPU, never the result's
  * meaning.  Positions past a row's own are not read into the result, whatever
  * their bytes hold.  Status: Q3_STATUS_BLOCK_RANGE (a slot, table entry or
- * position outside its range: what it names is left out), Q3_STATUS_F16_RANGE,
- * Q3_STATUS_TIMEOUT.
+ * position outside its range: what it names is left out), Q3_STATUS_F16_RANGE
+ * (q, or a result in fp16, is not a finite fp16 number; a row with a score
+ * that is no number is NaN), Q3_STATUS_TIMEOUT.
  * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, const int32_t* row_pos_dev,
                                const int32_t* row_slot_dev, int T, int n_q, int n_kv, const int32_t* tables_dev,

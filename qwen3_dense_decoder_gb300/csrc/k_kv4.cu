@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(AW * 32, 4) kv4_decode_kernel(const Kv4DecodeA
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         if (h >= G) continue;
-        if (g == 0) { sm.m[warp][h] = w.m[i]; sm.l[warp][h] = l; }
+        // a sum that is no number is joined under an infinite reference, so it is none in every sum
+        if (g == 0) { sm.m[warp][h] = l == l ? w.m[i] : INFINITY; sm.l[warp][h] = l; }
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) {
             const float(&x)[4] = w.o[2 * gr];
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(AW * 32, 4) kv4_decode_kernel(const Kv4DecodeA
     const size_t row = ((size_t)t * a.n_q + (size_t)kvh * G) * D + d;
     bad = false;
     auto put = [&](int h, float O, float L) {
-        const float v = L > 0.f ? O / L : 0.f;           // nothing attended: zeros
+        const float v = L == 0.f ? 0.f : O / L;          // nothing attended: zeros
         if (a.out_f32) static_cast<float*>(a.out)[row + (size_t)h * D] = v;
         else static_cast<__half*>(a.out)[row + (size_t)h * D] = to_f16(v, bad);
     };

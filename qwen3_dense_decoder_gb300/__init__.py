@@ -323,7 +323,7 @@ def _op(name: str):
         try:
             from . import _ops
         except ImportError as e:
-            raise RuntimeError("_ops is missing: build it with qwen3_dense_decoder_gb300.build()") from e
+            raise RuntimeError(f"the operators' extension module cannot be loaded (qwen3_dense_decoder_gb300.build() makes it): {e}") from e
         address = [C.cast(f, C.c_void_p).value for f in (L.q3_op_kv4_append, L.q3_op_kv4_decode_attention,
                                                          L.q3_op_kv4_prefill_attention, L.q3_kv4_prefill_workspace,
                                                          L.q3_op_token_logprobs)]

@@ -63,12 +63,34 @@ def compile_ops() -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile csrc/*.cu into libq3.so and csrc/bind.cpp into _ops.so (skipped when up to date)."""
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, OPS)):
-        return LIB
+    """Compile csrc/*.cu into libq3.so and csrc/bind.cpp into _ops.so (each skipped when up to date).
+
+    The library and the model paths need nothing of torch's headers; where the
+    extension cannot be built, that is written to stderr, and its operators
+    raise when they are called."""
+    newest = _deps_mtime()
+
+    def stale(f: str) -> bool:
+        return force or not os.path.exists(f) or os.path.getmtime(f) < newest
+
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        ops = ex.submit(compile_ops) if stale(OPS) else None
+        if stale(LIB):
+            compile_lib(verbose, list(extra or []))
+        try:
+            if ops:
+                ops.result()
+        except Exception as e:
+            if os.path.exists(OPS):
+                os.remove(OPS)
+            sys.stderr.write(f"_ops.so was not built: {e}\n")
+    return LIB
+
+
+def compile_lib(verbose: bool, extra: list[str]) -> None:
+    """csrc/*.cu into libq3.so."""
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
-    extra = list(extra or [])
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -80,16 +102,13 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ops = ex.submit(compile_ops)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        ops.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 FAULT_LIB = os.path.join(BUILD, "faults", "libq3_faults.so")

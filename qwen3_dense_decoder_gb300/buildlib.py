@@ -45,9 +45,34 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def ops_stamp() -> str:
+    """What _ops.so's binary interface depends on: this Python's and the installed torch's."""
+    try:
+        with open(os.path.join(torch_dir(), "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return f"{sysconfig.get_config_var('EXT_SUFFIX')}\n{torch_dir()}\n{version}"
+
+
+def ops_stale(newest: float) -> bool:
+    """Whether _ops.so is missing, older than its sources or made for another torch or Python."""
+    if not os.path.exists(OPS) or os.path.getmtime(OPS) < newest:
+        return True
+    try:
+        with open(OPS + ".stamp") as f:
+            return f.read() != ops_stamp()
+    except OSError:
+        return True
+
+
 def compile_ops() -> None:
     """csrc/bind.cpp into _ops.so, against the headers and libraries of the torch that will load it."""
-    torch = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin))
+    torch = torch_dir()
     libs = os.path.join(torch, "lib")
     includes = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                 os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
@@ -60,6 +85,8 @@ def compile_ops() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS)
+    with open(OPS + ".stamp", "w") as f:
+        f.write(ops_stamp())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -69,13 +96,9 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     extension cannot be built, that is written to stderr, and its operators
     raise when they are called."""
     newest = _deps_mtime()
-
-    def stale(f: str) -> bool:
-        return force or not os.path.exists(f) or os.path.getmtime(f) < newest
-
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        ops = ex.submit(compile_ops) if stale(OPS) else None
-        if stale(LIB):
+        ops = ex.submit(compile_ops) if force or ops_stale(newest) else None
+        if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
             compile_lib(verbose, list(extra or []))
         try:
             if ops:

@@ -55,3 +55,28 @@ def test_operators_without_their_extension_say_why(monkeypatch):
     monkeypatch.setattr(builtins, "__import__", refuse)
     with pytest.raises(RuntimeError, match="a_name_of_another_torch"):
         q3.op_token_logprobs(None)
+
+
+def test_the_extension_is_rebuilt_for_another_torch_or_python(monkeypatch, tmp_path):
+    c = Compiler(monkeypatch, tmp_path)
+    buildlib.build()
+    buildlib.build()
+    assert c.runs == {"nvcc": len(buildlib.SOURCES) + 1, "g++": 1}         # up to date
+    torch = tmp_path / "torch"
+    torch.mkdir()
+    (torch / "__init__.py").write_text("")
+    (torch / "version.py").write_text("__version__ = '9.9'\n")
+    real = buildlib.importlib.util.find_spec
+    spec = type("Spec", (), {"origin": str(torch / "__init__.py")})
+    monkeypatch.setattr(buildlib.importlib.util, "find_spec", lambda name: spec if name == "torch" else real(name))
+    buildlib.build()
+    buildlib.build()
+    assert c.runs["g++"] == 2
+    (torch / "version.py").write_text("__version__ = '9.10'\n")            # the same place, another version
+    buildlib.build()
+    assert c.runs["g++"] == 3
+    ext = buildlib.sysconfig.get_config_var
+    monkeypatch.setattr(buildlib.sysconfig, "get_config_var", lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else ext(n))
+    buildlib.build()
+    buildlib.build()
+    assert c.runs == {"nvcc": len(buildlib.SOURCES) + 1, "g++": 4}         # the library needs neither

@@ -35,6 +35,19 @@ PyObject* g_check;
 struct Refusal { std::string what; };        // becomes a ValueError
 struct Raised {};                            // a Python error is set
 
+// Allocating may wait for the device and a launch for room in its queue: other Python
+// threads run meanwhile
+class Unlocked {
+public:
+    Unlocked() : state_(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+    Unlocked(const Unlocked&) = delete;
+    Unlocked& operator=(const Unlocked&) = delete;
+
+private:
+    PyThreadState* state_;
+};
+
 #define Q3_BEGIN HANDLE_TH_ERRORS try {
 #define Q3_END                                                  \
     }                                                           \
@@ -203,11 +216,17 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     int32(c, "row_slot", slot, {T});
     const Where w(c, {&qkv, &qg, &kg, &rope, &pos, &slot, &tables, &kv, q_given, kv_out, status}, a[13], T > 0);
     if (kv_out) Where::check(c, *kv_out, {T, 2, n_kv, 128}, at::kHalf);
-    const at::Tensor q = w.out(c, q_given, {T, n_q, 128}, at::kHalf);
-    if (T > 0)
-        check(p_append(ptr(qkv), type, T > 1 ? qkv.stride(0) : width, ptr(qg), ptr(kg), (float)eps, ptr<float>(rope), c.size(rope, 0),
-                       ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, n_kv, ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1), ptr(kv),
-                       c.size(kv, 0), ptr(q), ptr(kv_out), ptr<int32_t>(status), w.stream()));
+    at::Tensor q;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        q = w.out(c, q_given, {T, n_q, 128}, at::kHalf);
+        if (T > 0)
+            rc = p_append(ptr(qkv), type, T > 1 ? qkv.stride(0) : width, ptr(qg), ptr(kg), (float)eps, ptr<float>(rope), c.size(rope, 0),
+                          ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, n_kv, ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1),
+                          ptr(kv), c.size(kv, 0), ptr(q), ptr(kv_out), ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
     return THPVariable_Wrap(q);
     Q3_END
 }
@@ -226,11 +245,17 @@ PyObject* kv4_decode_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     int32(c, "row_pos", pos, {T});
     int32(c, "row_slot", slot, {T});
     const Where w(c, {&q, &pos, &slot, &tables, &kv, given, status}, a[8], T > 0);
-    const at::Tensor out = w.out(c, given, {T, n_q, 128}, given && given->scalar_type() == at::kFloat ? at::kFloat : at::kHalf);
-    if (T > 0)
-        check(p_decode(ptr(q), type_of(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, c.size(kv, 2),
-                       ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1), max_ctx, ptr(kv), c.size(kv, 0), ptr(out), type_of(out),
-                       ptr<int32_t>(status), w.stream()));
+    at::Tensor out;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        out = w.out(c, given, {T, n_q, 128}, given && given->scalar_type() == at::kFloat ? at::kFloat : at::kHalf);
+        if (T > 0)
+            rc = p_decode(ptr(q), type_of(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, c.size(kv, 2),
+                          ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1), max_ctx, ptr(kv), c.size(kv, 0), ptr(out), type_of(out),
+                          ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
     return THPVariable_Wrap(out);
     Q3_END
 }
@@ -252,17 +277,25 @@ PyObject* kv4_prefill_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (slot) int32(c, "seq_slot", *slot, {ns});
     const bool launch = T > 0 && ns > 0;
     const Where w(c, {&q, &rows, &pos, &tables, &kv, slot, given, space, status}, a[9], launch);
-    const at::Tensor out = w.out(c, given, {T, n_q, 128}, at::kHalf);
+    int64_t need = 0;
     if (launch) {
-        int64_t need = 0;
         check(p_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks, &need));
         if (space && (space->scalar_type() != at::kByte || !space->is_contiguous() || space->numel() < need))
             c.refuse("workspace must be contiguous uint8, at least " + std::to_string(need) + " bytes");
-        const at::Tensor ws = space ? *space : w.make({need}, at::kByte);
-        check(p_prefill(ptr(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(rows), ptr<int32_t>(pos), ptr<int32_t>(slot), ns, T, n_q, n_kv,
-                        ptr<int32_t>(tables), n_slots, max_blocks, ptr(kv), n_blocks, ptr(out), ptr(ws), ws.numel(), ptr<int32_t>(status),
-                        w.stream()));
     }
+    at::Tensor out;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        out = w.out(c, given, {T, n_q, 128}, at::kHalf);
+        if (launch) {
+            const at::Tensor ws = space ? *space : w.make({need}, at::kByte);
+            rc = p_prefill(ptr(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(rows), ptr<int32_t>(pos), ptr<int32_t>(slot), ns, T, n_q,
+                           n_kv, ptr<int32_t>(tables), n_slots, max_blocks, ptr(kv), n_blocks, ptr(out), ptr(ws), ws.numel(),
+                           ptr<int32_t>(status), w.stream());
+        }
+    }
+    check(rc);
     return THPVariable_Wrap(out);
     Q3_END
 }
@@ -281,12 +314,19 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (status) int32(c, "status", *status, {1});
     if (top < 0) c.refuse("top_k must not be negative");
     const Where w(c, {&x, targets, status}, a[4], N > 0);
-    at::Tensor lp;
-    if (targets) lp = w.make({N}, at::kFloat);
-    const at::Tensor entropy = w.make({N}, at::kFloat), ids = w.make({N, top}, at::kInt), values = w.make({N, top}, at::kFloat);
-    if (N > 0)
-        check(p_logprobs(ptr(x), type, N > 1 ? x.stride(0) : V, N, V, ptr<int32_t>(targets), top, targets ? ptr<float>(lp) : nullptr,
-                         ptr<float>(entropy), ptr<int32_t>(ids), ptr<float>(values), ptr<int32_t>(status), w.stream()));
+    at::Tensor lp, entropy, ids, values;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        if (targets) lp = w.make({N}, at::kFloat);
+        entropy = w.make({N}, at::kFloat);
+        ids = w.make({N, top}, at::kInt);
+        values = w.make({N, top}, at::kFloat);
+        if (N > 0)
+            rc = p_logprobs(ptr(x), type, N > 1 ? x.stride(0) : V, N, V, ptr<int32_t>(targets), top, targets ? ptr<float>(lp) : nullptr,
+                            ptr<float>(entropy), ptr<int32_t>(ids), ptr<float>(values), ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
     PyObject* r = PyTuple_New(4);
     if (!r) throw Raised{};
     if (targets) PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(lp));

@@ -441,9 +441,9 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
  *     dimension 32 group + 4 g + i in bits 4 i; from byte 2,048 fp16
  *     [position / 2][group][scale even, scale odd, bias even, bias odd].
  * tables_dev: int32 [n_slots][max_blocks], the physical block of each 32
- * positions of a slot.  Sizes: 1 <= n_kv, n_q a multiple of n_kv and at most
- * 8 n_kv, 1 <= n_blocks, n_slots, max_blocks; max_blocks at most 2^20, rows
- * T times n_kv below 2^31.
+ * positions of a slot.  Sizes: 1 <= n_kv <= 4,096, n_q a multiple of n_kv and
+ * at most 8 n_kv, 1 <= n_blocks, n_slots, max_blocks; max_blocks at most 2^20,
+ * rows T times n_kv below 2^31.
  *
  * q3_op_kv4_append: per row t of projections (n_q q heads, then n_kv k heads,
  * then n_kv v heads of 128) at position row_pos_dev[t] of slot
@@ -509,8 +509,10 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
                                 int n_blocks, void* out_dev, void* workspace_dev, int64_t workspace_bytes,
                                 int32_t* status_dev, void* stream);
 /* Bytes of workspace for these sizes: an fp16 copy of the blocks a call may
- * read, min(n_blocks, ns * max_blocks) blocks of n_kv * 16 KB, and about 20 MB
- * for lists and for tiles that several SMs share.  Host only.
+ * read, min(n_blocks, ns * max_blocks) blocks of n_kv * 16 KB (below 2^31 / (64
+ * n_kv) of them; tables that hold only as many entries as their sequences use
+ * keep it small in a large pool), and about 20 MB for lists and for tiles that
+ * several SMs share.  Host only.
  * Errors: Q3_ERR_INVALID_ARG. */
 int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks, int64_t* bytes);
 

@@ -2347,12 +2347,18 @@ int q3_op_prefill_attention(const void* q_dev, const void* kv_dev, const int32_t
 namespace {
 
 // what the three cache operators share: heads, tables, pool
-bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int max_blocks, const void* kv, int n_blocks)
+bool kv4_counts_ok(int T, int n_q, int n_kv, int max_blocks, int n_blocks)
 {
     return T >= 0 && n_kv >= 1 && n_kv <= 4096 && (int64_t)T * n_kv <= 0x7fffffff && n_q >= 1 && n_q <= 8 * n_kv &&
-           n_q % n_kv == 0 && tables && n_slots >= 1 && max_blocks >= 1 && max_blocks <= (1 << 20) && kv && aligned16(kv) &&
-           n_blocks >= 1;
+           n_q % n_kv == 0 && max_blocks >= 1 && max_blocks <= (1 << 20) && n_blocks >= 1;
 }
+bool kv4_sizes_ok(int T, int n_q, int n_kv, const void* tables, int n_slots, int max_blocks, const void* kv, int n_blocks)
+{
+    return kv4_counts_ok(T, n_q, n_kv, max_blocks, n_blocks) && tables && n_slots >= 1 && kv && aligned16(kv);
+}
+
+// rows of 128 in the prefill attention's copy: 32-bit coordinates of its tensor map
+bool kv4_copy_ok(const Kv4Workspace& w, int n_kv) { return w.blocks * 2 * n_kv * 32 <= 0x7fffffffll; }
 
 // A programmatic launch: a call's set-up overlaps the end of the kernel before it on
 // the stream, whichever that is, and the call's kernels wait for that one before they
@@ -2432,10 +2438,11 @@ int q3_op_kv4_decode_attention(const void* q_dev, int q_type, int64_t q_stride, 
 
 int q3_kv4_prefill_workspace(int ns, int T, int n_q, int n_kv, int max_blocks, int n_blocks, int64_t* bytes)
 {
-    if (!bytes || ns < 0 || T < 0 || n_kv < 1 || n_q < 1 || n_q % n_kv || n_q > 8 * n_kv || max_blocks < 1 ||
-        max_blocks > (1 << 20) || n_blocks < 1)
+    if (!bytes || ns < 0 || !kv4_counts_ok(T, n_q, n_kv, max_blocks, n_blocks))
         return fail(Q3_ERR_INVALID_ARG, "kv4_prefill_workspace: bad argument");
-    *bytes = (int64_t)kv4_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks).bytes;
+    const Kv4Workspace w = kv4_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks);
+    if (!kv4_copy_ok(w, n_kv)) return fail(Q3_ERR_INVALID_ARG, "kv4_prefill_workspace: more than 2^31 cache rows in one call");
+    *bytes = (int64_t)w.bytes;
     return Q3_OK;
 }
 
@@ -2451,10 +2458,10 @@ int q3_op_kv4_prefill_attention(const void* q_dev, int64_t q_stride, const int32
     if (!row_stride_ok(q_stride, Q3_TYPE_F16, (int64_t)n_q * 128))
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: row stride too small or not a multiple of 16 bytes");
     const Kv4Workspace w = kv4_workspace(ns, T, n_q, n_kv, max_blocks, n_blocks);
+    if (!kv4_copy_ok(w, n_kv))
+        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: more than 2^31 cache rows in one call");
     if (T > 0 && ns > 0 && (!workspace_dev || workspace_bytes < (int64_t)w.bytes || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: workspace of %lld bytes, 256-byte aligned", (long long)w.bytes);
-    if (w.blocks * 2 * n_kv * 32 > 0x7fffffffll)
-        return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: more than 2^31 cache rows in one call");
     if (!aligned16(q_dev) || !aligned16(out_dev))
         return fail(Q3_ERR_INVALID_ARG, "op_kv4_prefill_attention: pointers must be 16-byte aligned");
     if (T == 0 || ns == 0) return Q3_OK;

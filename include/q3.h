@@ -106,7 +106,9 @@ typedef struct q3_session q3_session;
  * bias).  Its prefill rounds attend an fp16 copy of the round's blocks on the
  * tcgen05 kernel (a pool holds that copy's room for one layer: n_blocks *
  * n_kv * 16 KB), its decode rounds the 4-bit tiles; one-session decode takes
- * the per-operation path. */
+ * the per-operation path (the 4B shape at 2,048 positions: 365 tokens/s,
+ * against 353 with the BF16 cache on that path and 444 on its fused step;
+ * 32 sessions 9,980 against 9,220, a 2,048-token prompt 14.6 ms against 15.8). */
 typedef struct q3_config {
     int n_layers, hidden, n_q_heads, n_kv_heads, head_dim, ffn, vocab, max_ctx;
     float rope_theta, rms_eps;

@@ -404,7 +404,8 @@ def op_kv4_prefill_attention(q: torch.Tensor, seq_rows: torch.Tensor, seq_pos: t
     positions seq_pos[i] .. of slot seq_slot[i] (default i), whose K and V the
     cache already holds.  Returns fp16 [T, n_q, 128]; rows of no sequence keep
     what out held.  workspace: uint8, kv4_prefill_workspace bytes (default:
-    allocated here)."""
+    allocated here; it grows with ns * max_blocks up to the pool, so tables cut
+    to the blocks in use keep it small)."""
     return _op("kv4_prefill_attention")(q, seq_rows, seq_pos, tables, kv, seq_slot, out, workspace, status, stream)
 
 

@@ -1,8 +1,8 @@
 // bind.cpp -- the Python side of the asynchronous operators: arguments checked,
 // outputs allocated and the C entry point called in one step.  For a few rows their
 // kernels take 3 to 20 us, and the same steps written in Python took 12 to 15 us of
-// host time beside the launch (a call that appends 32 rows: 21.2 us, 7.3 from here;
-// one row's decode attention 16.0 and 4.0).
+// host time beside the launch (a call that appends 32 rows: 21.2 us, 7.5 from here;
+// one row's decode attention 16.0 and 3.8).
 //
 // The module has one function an operator, called positionally by the documented
 // wrappers of __init__.py.  init() hands over the entry points of libq3.so and the

@@ -57,8 +57,10 @@ Q3_DEV void load4(const __half* p, int lane, float (&y)[4]) {
 // group's range, and the square root, the reciprocals and the divisions serve
 // four heads at once.  A head's value costs about half an instruction (q) to
 // one (k); the bytes are (n_q + 2 n_kv) 128 projections in, 2 bytes a q value
-// and 0.625 a k or v value out.  2,048 rows of 48 heads in f32: 18.8 us, 4.2 TB/s
-// of those bytes (a warp a head took 29.7); 32 rows: 2.9 us, latency.
+// and 0.625 a k or v value out.  2,048 rows of 48 heads in f32: 18.7 us, 4.2 TB/s
+// of those bytes (a warp a head took 29.7), bound by the latency of a warp's one round
+// of loads (4.4 of its stalls an issue are for them, at 31 % of DRAM and 39 % of the
+// warps); 32 rows: 3.0 us, that chain alone.
 Q3_DEV void load8(const float* p, float* y) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w; y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
@@ -249,10 +251,11 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const Kv4AppendArgs a)
 // shared memory, CTAs in order through distributed shared memory.
 //
 // tcgen05 would want the expanded values in shared memory, 256 bytes where 80 come
-// in, for at most eight columns.  8 rows of 16,384 positions (40/8 heads): 43 us,
-// 3.9 TB/s, bound by the arithmetic pipes (unpacking, products, exponentials) with the
-// four warps a scheduler that 128 registers allow; 32 rows of 129 to 2,239 (32/8):
-// 20.4 us; one row of 2,176: 6.3 us, latency.
+// in, for at most eight columns.  8 rows of 16,384 positions (40/8 heads): 43 us, 3.9
+// TB/s.  No unit is full then (FMA pipe 42 % of its cycles, ALU 33, tensor 27, DRAM 46,
+// issue 51): a block is a chain of unpacking, products and exponentials, which the four
+// warps a scheduler that 128 registers allow do not hide.  32 rows of 129 to 2,239
+// (32/8): 20.4 us, the longest row's CTAs; one row of 2,176: 6.4 us, latency.
 constexpr int AW = 4;
 constexpr int STAGES = 2;
 constexpr int KV4_STAGE = 2 * KV4_TILE;

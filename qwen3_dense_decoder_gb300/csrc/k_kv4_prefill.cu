@@ -35,8 +35,9 @@
 //
 // A step of 128 positions reads 64 KB of K and V: 1,024 cycles of an SM's 64 bytes, as
 // many as its products take; it takes 1,450 with long contexts (512 rows after 10,240:
-// 88 us, 1.25 PFLOP/s over the whole call), 1,760 where a CTA has three items of nine
-// steps (2,048 rows: 35.7 us, 0.96 PFLOP/s).
+// 88 us, 1.25 PFLOP/s over the whole call, and 95 called without a pause, when 1.36 kW
+// bring the clock from 2,070 to 1,850 MHz), 1,760 where a CTA has three items of nine
+// steps (2,048 rows: 35.8 us, 0.96 PFLOP/s, either way).
 //
 // Roles (one CTA per SM; the next item's Q, K and scores are under way while an
 // item ends):

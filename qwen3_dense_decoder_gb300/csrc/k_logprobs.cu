@@ -21,9 +21,10 @@
 // Rows of few are split over the CTAs of a cluster, merged through
 // distributed shared memory: no workspace, no second launch.
 //
-// 2,048 rows of 151,936 f32 with 5 alternatives: 212 us, 5.9 TB/s of the logits
-// (lists kept in the pass took 337); one row with 20: 11.1 us, a chain of load,
-// merge and exchange latencies (24).
+// 2,048 rows of 151,936 f32 with 5 alternatives: 214 us, 5.8 TB/s of the logits
+// (lists kept in the pass took 337); in bf16 130 us, 4.8 TB/s, where the values'
+// instructions count for as much as their bytes; one row with 20: 10.9 us, a chain of
+// load, merge and exchange latencies (24).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -446,8 +447,8 @@ cudaError_t launch_t(const Launch& L, const LogprobArgs& a, int C)
 }  // namespace
 
 // CTAs of a row: twice as many, up to 8, while SMs are left out and a warp keeps
-// a full round of loads (64 rows of 151,936 f32 with 20 alternatives: 19.3 us
-// in 4, 21.9 in 8; one row: 12.7 in 8, 14 in 4).
+// a full round of loads (64 rows of 151,936 f32 with 20 alternatives: 18.7 us
+// in 4, 20.4 in 8; one row: 10.9 in 8, 12.5 in 4).
 cudaError_t launch_logprobs(const Launch& L, const LogprobArgs& a, int type)
 {
     const int64_t round = (int64_t)WARPS * 32 * NL * (type == Q3_TYPE_F32 ? 4 : 8);

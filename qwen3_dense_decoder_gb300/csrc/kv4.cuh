@@ -85,7 +85,9 @@ constexpr uint32_t KV4_MAGIC = 0x64006400u;
 // Nibble pair i of a code word (bits 4 i and 16 + 4 i) as fp16(scale * code +
 // bias): an odd i keeps its place as 1024 + 16 code, so a word needs one shift.
 // 1024 + code is exact in fp16, so are the code left by one exact operation and
-// the fused multiply-add's argument; the last rounds once.
+// the fused multiply-add's argument; the last rounds once.  (Integers turned into
+// fp16 by an exponent put over their bits: Kim, Henry, Fahim and Awadalla, "Who Says
+// Elephants Can't Run", 2022.)
 template <int I>
 Q3_DEV uint32_t kv4_pair(uint32_t w, __half2 scale, __half2 bias, uint32_t magic) {
     const uint32_t x = I >= 2 ? w >> 8 : w;

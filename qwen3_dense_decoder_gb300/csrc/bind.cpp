@@ -36,7 +36,7 @@ struct Refusal { std::string what; };        // becomes a ValueError
 struct Raised {};                            // a Python error is set
 
 // Allocating may wait for the device and a launch for room in its queue: other Python
-// threads run meanwhile
+// threads run meanwhile.  No tensor that Python knows is copied or let go here.
 class Unlocked {
 public:
     Unlocked() : state_(PyEval_SaveThread()) {}
@@ -156,11 +156,11 @@ public:
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
         return at::empty(shape, at::TensorOptions().dtype(type).device(device_));
     }
-    // out as given, checked, or a new tensor
-    at::Tensor out(const Args& c, const at::Tensor* given, at::IntArrayRef shape, at::ScalarType type) const {
-        if (!given) return make(shape, type);
-        check(c, *given, shape, type);
-        return *given;
+    // a caller's tensor, checked, or none yet
+    static at::Tensor given(const Args& c, const at::Tensor* t, at::IntArrayRef shape, at::ScalarType type) {
+        if (!t) return {};
+        check(c, *t, shape, type);
+        return *t;
     }
     static void check(const Args& c, const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type) {
         if (t.sizes() != shape || t.scalar_type() != type || !t.is_contiguous())
@@ -216,11 +216,11 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n)
     int32(c, "row_slot", slot, {T});
     const Where w(c, {&qkv, &qg, &kg, &rope, &pos, &slot, &tables, &kv, q_given, kv_out, status}, a[13], T > 0);
     if (kv_out) Where::check(c, *kv_out, {T, 2, n_kv, 128}, at::kHalf);
-    at::Tensor q;
+    at::Tensor q = Where::given(c, q_given, {T, n_q, 128}, at::kHalf);
     int rc = 0;
     {
         const Unlocked other_threads_run;
-        q = w.out(c, q_given, {T, n_q, 128}, at::kHalf);
+        if (!q.defined()) q = w.make({T, n_q, 128}, at::kHalf);
         if (T > 0)
             rc = p_append(ptr(qkv), type, T > 1 ? qkv.stride(0) : width, ptr(qg), ptr(kg), (float)eps, ptr<float>(rope), c.size(rope, 0),
                           ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, n_kv, ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1),
@@ -245,11 +245,11 @@ PyObject* kv4_decode_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     int32(c, "row_pos", pos, {T});
     int32(c, "row_slot", slot, {T});
     const Where w(c, {&q, &pos, &slot, &tables, &kv, given, status}, a[8], T > 0);
-    at::Tensor out;
+    at::Tensor out = Where::given(c, given, {T, n_q, 128}, given && given->scalar_type() == at::kFloat ? at::kFloat : at::kHalf);
     int rc = 0;
     {
         const Unlocked other_threads_run;
-        out = w.out(c, given, {T, n_q, 128}, given && given->scalar_type() == at::kFloat ? at::kFloat : at::kHalf);
+        if (!out.defined()) out = w.make({T, n_q, 128}, at::kHalf);
         if (T > 0)
             rc = p_decode(ptr(q), type_of(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(pos), ptr<int32_t>(slot), T, n_q, c.size(kv, 2),
                           ptr<int32_t>(tables), c.size(tables, 0), c.size(tables, 1), max_ctx, ptr(kv), c.size(kv, 0), ptr(out), type_of(out),
@@ -283,13 +283,14 @@ PyObject* kv4_prefill_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (space && (space->scalar_type() != at::kByte || !space->is_contiguous() || space->numel() < need))
             c.refuse("workspace must be contiguous uint8, at least " + std::to_string(need) + " bytes");
     }
-    at::Tensor out;
+    at::Tensor out = Where::given(c, given, {T, n_q, 128}, at::kHalf), ws;
+    if (space) ws = *space;
     int rc = 0;
     {
         const Unlocked other_threads_run;
-        out = w.out(c, given, {T, n_q, 128}, at::kHalf);
+        if (!out.defined()) out = w.make({T, n_q, 128}, at::kHalf);
         if (launch) {
-            const at::Tensor ws = space ? *space : w.make({need}, at::kByte);
+            if (!ws.defined()) ws = w.make({need}, at::kByte);
             rc = p_prefill(ptr(q), T > 1 ? q.stride(0) : n_q * 128ll, ptr<int32_t>(rows), ptr<int32_t>(pos), ptr<int32_t>(slot), ns, T, n_q,
                            n_kv, ptr<int32_t>(tables), n_slots, max_blocks, ptr(kv), n_blocks, ptr(out), ptr(ws), ws.numel(),
                            ptr<int32_t>(status), w.stream());

@@ -47,3 +47,20 @@ def test_an_operator_gives_up_the_interpreter(name):
         stop[0] = True
         t.join()
     assert seen > first
+
+
+def test_a_callers_outputs_keep_their_count():
+    """Outputs that the caller passes are handed back: the same tensors, with no reference lost or kept."""
+    import qwen3_dense_decoder_gb300 as q3
+    q3.build()
+    kv, tab, row = torch.zeros(4, 2, 8, 2560, dtype=torch.uint8), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(0, dtype=torch.int32)
+    one, q = torch.zeros(1, dtype=torch.int32), torch.zeros(0, 32, 128, dtype=torch.float16)
+    out = torch.zeros(0, 32, 128, dtype=torch.float16)
+    before = sys.getrefcount(out)
+    for _ in range(100):
+        assert q3.op_kv4_decode_attention(q, row, row, tab, kv, out=out) is out
+        assert q3.op_kv4_prefill_attention(q, one, row, tab, kv, out=out) is out
+        for bad in (torch.zeros(1, 32, 128, dtype=torch.float16), out.double()):
+            with pytest.raises(ValueError):
+                q3.op_kv4_decode_attention(q, row, row, tab, kv, out=bad)
+    assert sys.getrefcount(out) == before

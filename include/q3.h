@@ -538,6 +538,58 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
                          int top_k, float* logprob_dev, float* entropy_dev, int32_t* top_ids_dev,
                          float* top_logprob_dev, int32_t* status_dev, void* stream);
 
+/* ---- Operators of 8-bit integer rows ----
+ * The projections of a layer whose weights and activations are 8-bit integers,
+ * and what stands between them.  Conventions as those of the 4-bit cache's
+ * operators above: nothing is allocated, calls are asynchronous on stream and
+ * may be captured, *status_dev collects what a kernel finds, zero rows launch
+ * nothing.  The Kipp pages have no counterpart ("Kipp Model Support", section
+ * "Quantization (Q8_0)", packs weights alone, with a scale for each 32).
+ *
+ * A row y of K values (1 <= K <= 131,071) is held as K int8 codes and one f32
+ * scale: scale = max |y| / 127, code = round-half-even(y / scale), in [-127,
+ * 127]; a row of zeros has scale 0 and zero codes.  y is an FP32 value and the
+ * division a product with an FP32 reciprocal: where y / scale lies within 2^-13
+ * of a half, a code may be the neighbour.  A row that holds an infinity or a NaN has a NaN for its
+ * scale and zero codes (so that every product with it is NaN) and sets
+ * Q3_STATUS_F16_RANGE.  codes_dev: rows code_stride bytes apart (a multiple of
+ * 16, at least K), 16-byte aligned; bytes past K are neither written nor read.
+ * scales_dev: f32 [T].  values_dev: [T][K] of values_type (f32, fp16 or bf16),
+ * or NULL, receives scale * code.  Inputs: f32, fp16 or bf16 rows, stride
+ * elements apart, of any alignment of the type (rows that begin on 16-byte
+ * boundaries are read faster).
+ *
+ * q3_op_i8_quantize: y = x.  Tokens of an activation, or the output channels of
+ * a weight matrix.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_i8_quantize(const void* x_dev, int type, int64_t stride, int T, int K, int8_t* codes_dev, int64_t code_stride,
+                      float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
+
+/* q3_op_i8_norm: y = s / sqrt(mean s^2 + eps) * gain with s = x, or with
+ * delta_dev the rounding of x + delta to x's type, which goes to sum_dev (rows
+ * sum_stride elements apart; sum_dev may be x_dev, with its stride).  Without
+ * delta_dev sum_dev is NULL.  delta has a type of its own.  gain_dev: bf16 [K];
+ * eps finite and at least 0.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_i8_norm(const void* x_dev, int type, int64_t stride, const void* delta_dev, int delta_type, int64_t delta_stride,
+                  void* sum_dev, int64_t sum_stride, const void* gain_dev, float eps, int T, int K, int8_t* codes_dev,
+                  int64_t code_stride, float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
+
+/* q3_op_i8_swiglu: y[f] = silu(x[f]) * x[F + f] of rows of 2 F values (gate, then
+ * up), silu(z) = z / (1 + e^-z).  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, int8_t* codes_dev, int64_t code_stride,
+                    float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
+
+/* q3_op_i8_matmul: out[t][m] = (sum_k x[t][k] w[m][k]) x_scale[t] w_scale[m].
+ * The sum is the exact whole number whatever T and the split of the work, so a
+ * token's row does not depend on the tokens beside it; it is rounded to FP32,
+ * multiplied by x_scale, then by w_scale, and rounded to out_type (f32, fp16 or
+ * bf16).  x_dev: T rows of K codes, w_dev: M rows (1 <= M), as above; any int8 is
+ * a code here, -128 among them.  out_dev: rows out_stride elements apart (>= M).
+ * Status: Q3_STATUS_F16_RANGE (a result in fp16 is not a finite fp16 number),
+ * Q3_STATUS_TIMEOUT.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,
+                    const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
+                    int32_t* status_dev, void* stream);
+
 /* Split-K matmul that allocates nothing (the Kipp pages have no counterpart;
  * this entry point serves callers that cannot call cudaMalloc where they need
  * the product: a host framework that owns all device memory through its own

@@ -114,6 +114,10 @@ def lib():
         L.q3_op_kv4_prefill_attention.argtypes = [vp, i64, vp, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, vp, i64, vp, vp]
         L.q3_session_score.argtypes = [vp, vp, i, i, vp, i, vp, vp, vp, vp]
         L.q3_op_token_logprobs.argtypes = [vp, i, i64, i, i, vp, i, vp, vp, vp, vp, vp, vp]
+        L.q3_op_i8_quantize.argtypes = [vp, i, i64, i, i, vp, i64, vp, vp, i, vp, vp]
+        L.q3_op_i8_norm.argtypes = [vp, i, i64, vp, i, i64, vp, i64, vp, f, i, i, vp, i64, vp, vp, i, vp, vp]
+        L.q3_op_i8_swiglu.argtypes = [vp, i, i64, i, i, vp, i64, vp, vp, i, vp, vp]
+        L.q3_op_i8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i, i, i, vp, i, i64, vp, vp]
         _lib = L
     return _lib
 
@@ -326,7 +330,8 @@ def _op(name: str):
             raise RuntimeError(f"the operators' extension module cannot be loaded (qwen3_dense_decoder_gb300.build() makes it): {e}") from e
         address = [C.cast(f, C.c_void_p).value for f in (L.q3_op_kv4_append, L.q3_op_kv4_decode_attention,
                                                          L.q3_op_kv4_prefill_attention, L.q3_kv4_prefill_workspace,
-                                                         L.q3_op_token_logprobs)]
+                                                         L.q3_op_token_logprobs, L.q3_op_i8_quantize, L.q3_op_i8_norm,
+                                                         L.q3_op_i8_swiglu, L.q3_op_i8_matmul)]
         _ops.init(_check, *address)
         _native = _ops
     return getattr(_native, name)
@@ -417,6 +422,48 @@ def op_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None,
     in order, lowest index first among equals (int32 [N, top_k]), with their
     log probabilities (f32 [N, top_k])."""
     return _op("token_logprobs")(logits, targets, top_k, status, stream)
+
+
+# ---------------------------------------------------------------- rows in 8-bit integers
+# A row of values is held as int8 codes in [-127, 127] and one f32 scale, max
+# |row| / 127.  Codes are int8 [T, K] whose rows begin on 16-byte boundaries:
+# where K is not a multiple of 16, those made here are a view of wider rows.
+
+def op_i8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                   values: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Rows x [T, K] (f32, fp16 or bf16; rows may be strided) as 8-bit integers:
+    (codes int8 [T, K], scales f32 [T]).  The tokens of an activation, or the
+    output channels of a weight matrix.  values: f32, fp16 or bf16 [T, K], if
+    given, receives the values that the codes stand for."""
+    return _op("i8_quantize")(x, codes, scales, values, status, stream)
+
+
+def op_i8_norm(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, delta: torch.Tensor | None = None,
+               sum_out: torch.Tensor | None = None, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+               values: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """The RMS norm of rows x [T, K] (f32, fp16 or bf16; rows may be strided), or
+    of x + delta, with bf16 gains [K], as 8-bit integers: (codes, scales, sum).
+    sum is x where there is no delta, else x + delta rounded to x's type, which
+    is what the norm is taken of; sum_out receives it and may be x itself.
+    values as in op_i8_quantize."""
+    return _op("i8_norm")(x, gain, eps, delta, sum_out, codes, scales, values, status, stream)
+
+
+def op_i8_swiglu(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 values: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """silu(gate) * up of rows x [T, 2 F] (gate, then up; f32, fp16 or bf16; rows
+    may be strided) as 8-bit integers: (codes int8 [T, F], scales f32 [T]).
+    values as in op_i8_quantize."""
+    return _op("i8_swiglu")(x, codes, scales, values, status, stream)
+
+
+def op_i8_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                 out: torch.Tensor | None = None, dtype: torch.dtype | None = None, status: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """out[t][m] = (sum_k x[t][k] w[m][k]) x_scales[t] w_scales[m] over int8 codes
+    x [T, K] and w [M, K], the sum a whole number: [T, M] in dtype (f32, fp16 or
+    bf16; fp16 unless out says otherwise).  The rows of out may be strided."""
+    return _op("i8_matmul")(x, x_scales, w, w_scales, out, dtype, status, stream)
 
 
 class Model:

@@ -18,6 +18,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -30,6 +31,10 @@ decltype(&q3_op_kv4_decode_attention) p_decode;
 decltype(&q3_op_kv4_prefill_attention) p_prefill;
 decltype(&q3_kv4_prefill_workspace) p_workspace;
 decltype(&q3_op_token_logprobs) p_logprobs;
+decltype(&q3_op_i8_quantize) p_i8_quantize;
+decltype(&q3_op_i8_norm) p_i8_norm;
+decltype(&q3_op_i8_swiglu) p_i8_swiglu;
+decltype(&q3_op_i8_matmul) p_i8_matmul;
 PyObject* g_check;
 
 struct Refusal { std::string what; };        // becomes a ValueError
@@ -339,12 +344,197 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
     Q3_END
 }
 
+// ---------------------------------------------------------------- 8-bit integer rows
+
+// rows of f32, fp16 or bf16 values
+int i8_values(const Args& c, const char* what, const at::Tensor& t)
+{
+    const int type = type_of(t);
+    if (type < 0 || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1)) c.refuse(std::string(what) + " must be f32, fp16 or bf16 rows, each contiguous");
+    return type;
+}
+// elements between rows; one row has no next
+int64_t row_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+// int8 rows that begin on 16-byte boundaries
+void i8_codes(const Args& c, const char* what, const at::Tensor& t)
+{
+    if (t.scalar_type() != at::kChar || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) % 16) ||
+        reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+        c.refuse(std::string(what) + " must be int8 rows that begin on 16-byte boundaries");
+}
+int64_t code_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : (t.size(1) + 15) / 16 * 16; }
+
+void f32(const Args& c, const char* what, const at::Tensor& t, int64_t n)
+{
+    if (t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != n || !t.is_contiguous())
+        c.refuse(std::string(what) + " must be contiguous f32 [" + std::to_string(n) + "]");
+}
+
+// codes, scales and values of the three writers, checked or made
+struct I8Out {
+    at::Tensor codes, scales;
+    const at::Tensor* values;
+    int T, K;
+
+    I8Out(const Args& c, int T, int K, const at::Tensor* codes_given, const at::Tensor* scales_given, const at::Tensor* values, const at::Tensor* status)
+        : values(values), T(T), K(K)
+    {
+        if (K < 1) c.refuse("rows must have at least one value");
+        if (codes_given) {
+            i8_codes(c, "codes", *codes_given);
+            if (codes_given->size(0) != T || codes_given->size(1) != K) c.refuse("codes must be [" + std::to_string(T) + ", " + std::to_string(K) + "]");
+            codes = *codes_given;
+        }
+        if (scales_given) {
+            f32(c, "scales", *scales_given, T);
+            scales = *scales_given;
+        }
+        if (values && (type_of(*values) < 0 || values->sizes() != at::IntArrayRef({T, K}) || !values->is_contiguous()))
+            c.refuse("values must be contiguous f32, fp16 or bf16 [" + std::to_string(T) + ", " + std::to_string(K) + "]");
+        if (status) int32(c, "status", *status, {1});
+    }
+    void make(const Where& w) {                  // no tensor of the caller's is touched
+        if (!codes.defined()) {
+            codes = w.make({T, (K + 15ll) / 16 * 16}, at::kChar);
+            if (K % 16) codes = codes.narrow(1, 0, K);
+        }
+        if (!scales.defined()) scales = w.make({T}, at::kFloat);
+    }
+    int values_type() const { return values ? type_of(*values) : 0; }
+};
+
+PyObject* i8_pair(const I8Out& o, const at::Tensor* third = nullptr)
+{
+    PyObject* r = PyTuple_New(third ? 3 : 2);
+    if (!r) throw Raised{};
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(o.codes));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(o.scales));
+    if (third) PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(*third));
+    return r;
+}
+
+// (x, codes, scales, values, status, stream)
+PyObject* i8_rows(const char* name, PyObject* const* a, Py_ssize_t n, int parts, decltype(p_i8_quantize) entry)
+{
+    const Args c(name, a, n, 6);
+    const at::Tensor& x = c.tensor(0);
+    const at::Tensor *codes = c.maybe(1), *scales = c.maybe(2), *values = c.maybe(3), *status = c.maybe(4);
+    const int type = i8_values(c, "x", x), T = c.size(x, 0), width = c.size(x, 1);
+    if (width % parts) c.refuse("x must be [T, 2 F], gate then up");
+    const int K = width / parts;
+    I8Out o(c, T, K, codes, scales, values, status);
+    const Where w(c, {&x, codes, scales, values, status}, a[5], T > 0);
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        o.make(w);
+        if (T > 0)
+            rc = entry(ptr(x), type, row_stride(x), T, K, ptr<int8_t>(o.codes), code_stride(o.codes), ptr<float>(o.scales), ptr(values),
+                       o.values_type(), ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
+    return i8_pair(o);
+}
+
+PyObject* i8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    Q3_BEGIN
+    return i8_rows("op_i8_quantize", a, n, 1, p_i8_quantize);
+    Q3_END
+}
+
+PyObject* i8_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    Q3_BEGIN
+    return i8_rows("op_i8_swiglu", a, n, 2, p_i8_swiglu);
+    Q3_END
+}
+
+// (x, gain, eps, delta, sum_out, codes, scales, values, status, stream)
+PyObject* i8_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    Q3_BEGIN
+    const Args c("op_i8_norm", a, n, 10);
+    const at::Tensor &x = c.tensor(0), &gain = c.tensor(1);
+    const double eps = PyFloat_AsDouble(a[2]);
+    if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+    const at::Tensor *delta = c.maybe(3), *sum_given = c.maybe(4), *codes = c.maybe(5), *scales = c.maybe(6), *values = c.maybe(7),
+                     *status = c.maybe(8);
+    const int type = i8_values(c, "x", x), T = c.size(x, 0), K = c.size(x, 1);
+    if (gain.scalar_type() != at::kBFloat16 || gain.dim() != 1 || gain.size(0) != K || !gain.is_contiguous())
+        c.refuse("gain must be contiguous bf16 [" + std::to_string(K) + "]");
+    const int delta_type = delta ? i8_values(c, "delta", *delta) : 0;
+    if (delta && delta->sizes() != x.sizes()) c.refuse("delta must be " + text(x.sizes()));
+    if (sum_given && !delta) c.refuse("sum_out is for calls with delta");
+    if (sum_given && (i8_values(c, "sum_out", *sum_given) != type || sum_given->sizes() != x.sizes())) c.refuse("sum_out must be of x's type and size");
+    I8Out o(c, T, K, codes, scales, values, status);
+    const Where w(c, {&x, &gain, delta, sum_given, codes, scales, values, status}, a[9], T > 0);
+    at::Tensor sum;
+    if (!delta) sum = x;
+    else if (sum_given) sum = *sum_given;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        o.make(w);
+        if (!sum.defined()) sum = w.make({T, K}, x.scalar_type());
+        if (T > 0)
+            rc = p_i8_norm(ptr(x), type, row_stride(x), ptr(delta), delta_type, delta ? row_stride(*delta) : 0, delta ? ptr(sum) : nullptr,
+                           delta ? row_stride(sum) : 0, ptr(gain), (float)eps, T, K, ptr<int8_t>(o.codes), code_stride(o.codes),
+                           ptr<float>(o.scales), ptr(values), o.values_type(), ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
+    return i8_pair(o, &sum);
+    Q3_END
+}
+
+// (x, x_scales, w, w_scales, out, dtype, status, stream)
+PyObject* i8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    Q3_BEGIN
+    const Args c("op_i8_matmul", a, n, 8);
+    const at::Tensor &x = c.tensor(0), &xs = c.tensor(1), &wt = c.tensor(2), &ws = c.tensor(3);
+    const at::Tensor *given = c.maybe(4), *status = c.maybe(6);
+    i8_codes(c, "x", x);
+    i8_codes(c, "w", wt);
+    const int T = c.size(x, 0), K = c.size(x, 1), M = c.size(wt, 0);
+    if (wt.size(1) != K) c.refuse("w must be [M, " + std::to_string(K) + "]");
+    f32(c, "x_scales", xs, T);
+    f32(c, "w_scales", ws, M);
+    at::ScalarType type = at::kHalf;
+    if (a[5] != Py_None) {
+        if (!THPDtype_Check(a[5])) c.refuse("dtype must be a torch.dtype");
+        type = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
+    }
+    if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16) c.refuse("dtype must be f32, fp16 or bf16");
+    if (given) {
+        i8_values(c, "out", *given);
+        if (given->size(0) != T || given->size(1) != M || (a[5] != Py_None && given->scalar_type() != type))
+            c.refuse("out must be [" + std::to_string(T) + ", " + std::to_string(M) + "], of dtype where that is given");
+    }
+    if (status) int32(c, "status", *status, {1});
+    const Where w(c, {&x, &xs, &wt, &ws, given, status}, a[7], T > 0);
+    at::Tensor out;
+    if (given) out = *given;
+    int rc = 0;
+    {
+        const Unlocked other_threads_run;
+        if (!out.defined()) out = w.make({T, M}, type);
+        if (T > 0)
+            rc = p_i8_matmul(ptr<int8_t>(x), code_stride(x), ptr<float>(xs), ptr<int8_t>(wt), code_stride(wt), ptr<float>(ws), T, M, K, ptr(out),
+                             type_of(out), row_stride(out), ptr<int32_t>(status), w.stream());
+    }
+    check(rc);
+    return THPVariable_Wrap(out);
+    Q3_END
+}
+
 // (check, addresses of the entry points)
 PyObject* init(PyObject*, PyObject* args)
 {
     PyObject* f;
-    unsigned long long p[5];
-    if (!PyArg_ParseTuple(args, "OKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4])) return nullptr;
+    unsigned long long p[9];
+    if (!PyArg_ParseTuple(args, "OKKKKKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8])) return nullptr;
     Py_INCREF(f);
     Py_XDECREF(g_check);
     g_check = f;
@@ -353,11 +543,16 @@ PyObject* init(PyObject*, PyObject* args)
     p_prefill = reinterpret_cast<decltype(p_prefill)>(p[2]);
     p_workspace = reinterpret_cast<decltype(p_workspace)>(p[3]);
     p_logprobs = reinterpret_cast<decltype(p_logprobs)>(p[4]);
+    p_i8_quantize = reinterpret_cast<decltype(p_i8_quantize)>(p[5]);
+    p_i8_norm = reinterpret_cast<decltype(p_i8_norm)>(p[6]);
+    p_i8_swiglu = reinterpret_cast<decltype(p_i8_swiglu)>(p[7]);
+    p_i8_matmul = reinterpret_cast<decltype(p_i8_matmul)>(p[8]);
     Py_RETURN_NONE;
 }
 
 #define Q3_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {Q3_FAST(kv4_append), Q3_FAST(kv4_decode_attention), Q3_FAST(kv4_prefill_attention), Q3_FAST(token_logprobs),
+                         Q3_FAST(i8_quantize), Q3_FAST(i8_norm), Q3_FAST(i8_swiglu), Q3_FAST(i8_matmul),
                          {"init", init, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -423,6 +423,48 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const Launch& L, const LogprobArgs& a, int type);
 
+// ---------------------------------------------------------------- 8-bit integer rows and their product
+// T rows of K values to codes and scales: x, the norm of x + delta, or SwiGLU
+// of rows [gate K, up K].
+struct I8RowArgs {
+    const void* x;             // [T] rows, x_stride elements apart
+    int64_t x_stride;
+    const void* delta;         // norm: added to x, or null
+    int delta_type;
+    int64_t delta_stride;
+    void* sum;                 // norm with delta: x + delta in x's type; may be x
+    int64_t sum_stride;
+    const __nv_bfloat16* gain; // norm: [K]
+    float eps;
+    int T, K;
+    int8_t* codes;             // [T] rows, code_stride bytes apart
+    int64_t code_stride;
+    float* scales;             // [T]
+    void* values;              // [T][K] code * scale, or null
+    int values_type;
+    int values_vec;            // set by the launcher: rows of values begin on 16-byte boundaries
+    int* status;               // or null
+};
+cudaError_t launch_i8_quantize(const Launch& L, const I8RowArgs& a, int type);
+cudaError_t launch_i8_norm(const Launch& L, const I8RowArgs& a, int type);
+cudaError_t launch_i8_swiglu(const Launch& L, const I8RowArgs& a, int type);
+
+// out[t][m] = (sum_k x[t][k] w[m][k]) xs[t] ws[m]
+struct I8MatmulArgs {
+    const int8_t* x;           // [T] rows of K codes, x_stride bytes apart
+    int64_t x_stride;
+    const float* xs;           // [T]
+    const int8_t* w;           // [M] rows of K codes, w_stride bytes apart
+    int64_t w_stride;
+    const float* ws;           // [M]
+    int T, M, K;
+    void* out;                 // [T] rows of M, out_stride elements apart
+    int out_type;
+    int64_t out_stride;
+    int* status;               // or null
+};
+cudaError_t launch_i8_matvec(const Launch& L, const I8MatmulArgs& a);
+
 // Q8_0: canonical blocks -> (int8 plane, fp16 scale plane); planes -> fp16
 // tensor-core operand; bf16 -> canonical blocks.
 cudaError_t launch_q8_split(cudaStream_t s, const uint8_t* blocks, int64_t nblocks, int8_t* qs,

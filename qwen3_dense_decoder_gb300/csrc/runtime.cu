@@ -2506,4 +2506,110 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
     return Q3_OK;
 }
 
+// ---------------------------------------------------------------- operators of 8-bit integer rows
+namespace {
+
+constexpr int I8_MAX_K = 131071;             // 128 * 128 * K stays below 2^31
+
+bool i8_type_ok(int type) { return type >= Q3_TYPE_F32 && type <= Q3_TYPE_BF16; }
+bool i8_rows_ok(const void* p, int64_t stride, int64_t width, int type)
+{
+    return p && stride >= width && !(reinterpret_cast<uintptr_t>(p) & (type == Q3_TYPE_F32 ? 3 : 1));
+}
+bool i8_codes_ok(const void* p, int64_t stride, int K) { return p && aligned16(p) && stride >= K && stride % 16 == 0; }
+bool aligned4(const void* p) { return !(reinterpret_cast<uintptr_t>(p) & 3); }
+
+// the outputs that the three writers share
+int i8_outputs(const char* name, I8RowArgs& a, int T, int K, int8_t* codes, int64_t code_stride, float* scales, void* values,
+               int values_type, int32_t* status)
+{
+    if (T < 0 || K < 1 || K > I8_MAX_K) return fail(Q3_ERR_INVALID_ARG, "%s: T rows of 1 to %d values", name, I8_MAX_K);
+    if (!i8_codes_ok(codes, code_stride, K) || !scales || !aligned4(scales))
+        return fail(Q3_ERR_INVALID_ARG, "%s: codes begin on 16-byte boundaries, rows a multiple of 16 bytes apart", name);
+    if (values && (!i8_type_ok(values_type) || !i8_rows_ok(values, K, K, values_type)))
+        return fail(Q3_ERR_INVALID_ARG, "%s: values of an unknown type or not aligned to it", name);
+    a.T = T; a.K = K;
+    a.codes = codes; a.code_stride = code_stride; a.scales = scales;
+    a.values = values; a.values_type = values_type; a.status = status;
+    return Q3_OK;
+}
+
+}  // namespace
+
+int q3_op_i8_quantize(const void* x_dev, int type, int64_t stride, int T, int K, int8_t* codes_dev, int64_t code_stride,
+                      float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream)
+{
+    if (!i8_type_ok(type) || !i8_rows_ok(x_dev, stride, K, type))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_quantize: x of an unknown type, not aligned to it or with a short stride");
+    I8RowArgs a{};
+    const int rc = i8_outputs("op_i8_quantize", a, T, K, codes_dev, code_stride, scales_dev, values_dev, values_type, status_dev);
+    if (rc != Q3_OK || T == 0) return rc;
+    a.x = x_dev; a.x_stride = stride;
+    const cudaError_t e = launch_i8_quantize(op_launch(stream), a, type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_quantize: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_op_i8_norm(const void* x_dev, int type, int64_t stride, const void* delta_dev, int delta_type, int64_t delta_stride,
+                  void* sum_dev, int64_t sum_stride, const void* gain_dev, float eps, int T, int K, int8_t* codes_dev,
+                  int64_t code_stride, float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream)
+{
+    if (!i8_type_ok(type) || !i8_rows_ok(x_dev, stride, K, type))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_norm: x of an unknown type, not aligned to it or with a short stride");
+    if (delta_dev && (!i8_type_ok(delta_type) || !i8_rows_ok(delta_dev, delta_stride, K, delta_type) ||
+                      !i8_rows_ok(sum_dev, sum_stride, K, type) || (sum_dev == x_dev && T > 1 && sum_stride != stride)))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_norm: delta and its sum: of an unknown type, not aligned to it, with a short stride or missing");
+    if (!delta_dev && sum_dev) return fail(Q3_ERR_INVALID_ARG, "op_i8_norm: a sum without delta");
+    if (!gain_dev || (reinterpret_cast<uintptr_t>(gain_dev) & 1) || !(eps >= 0.0f) || !(eps < INFINITY))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_norm: bf16 gains and a finite eps of at least 0");
+    I8RowArgs a{};
+    const int rc = i8_outputs("op_i8_norm", a, T, K, codes_dev, code_stride, scales_dev, values_dev, values_type, status_dev);
+    if (rc != Q3_OK || T == 0) return rc;
+    a.x = x_dev; a.x_stride = stride;
+    a.delta = delta_dev; a.delta_type = delta_type; a.delta_stride = delta_stride;
+    a.sum = sum_dev; a.sum_stride = sum_stride;
+    a.gain = static_cast<const bf16*>(gain_dev); a.eps = eps;
+    const cudaError_t e = launch_i8_norm(op_launch(stream), a, type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_norm: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, int8_t* codes_dev, int64_t code_stride,
+                    float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream)
+{
+    if (!i8_type_ok(type) || !i8_rows_ok(x_dev, stride, 2ll * F, type))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_swiglu: x of an unknown type, not aligned to it or with a short stride");
+    I8RowArgs a{};
+    const int rc = i8_outputs("op_i8_swiglu", a, T, F, codes_dev, code_stride, scales_dev, values_dev, values_type, status_dev);
+    if (rc != Q3_OK || T == 0) return rc;
+    a.x = x_dev; a.x_stride = stride;
+    const cudaError_t e = launch_i8_swiglu(op_launch(stream), a, type);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_swiglu: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
+int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,
+                    const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
+                    int32_t* status_dev, void* stream)
+{
+    if (T < 0 || M < 1 || K < 1 || K > I8_MAX_K)
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: T rows, at least one channel, 1 to %d inputs", I8_MAX_K);
+    if (!i8_codes_ok(x_dev, x_stride, K) || !i8_codes_ok(w_dev, w_stride, K))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: codes begin on 16-byte boundaries, rows a multiple of 16 bytes apart");
+    if (!x_scales_dev || !w_scales_dev || !aligned4(x_scales_dev) || !aligned4(w_scales_dev))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: f32 scales of x and w");
+    if (!i8_type_ok(out_type) || !i8_rows_ok(out_dev, out_stride, M, out_type))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: out of an unknown type, not aligned to it or with a short stride");
+    if (T == 0) return Q3_OK;
+    I8MatmulArgs a{};
+    a.x = x_dev; a.x_stride = x_stride; a.xs = x_scales_dev;
+    a.w = w_dev; a.w_stride = w_stride; a.ws = w_scales_dev;
+    a.T = T; a.M = M; a.K = K;
+    a.out = out_dev; a.out_type = out_type; a.out_stride = out_stride;
+    a.status = status_dev;
+    const cudaError_t e = launch_i8_matvec(op_launch(stream), a);
+    if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_matmul: %s", cudaGetErrorString(e));
+    return Q3_OK;
+}
+
 }  // extern "C"

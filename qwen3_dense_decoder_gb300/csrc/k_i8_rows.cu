@@ -54,11 +54,11 @@ Q3_DEV void load8(const X* p, int tid, int n, int i, int K, float (&v)[8])
         for (int e = 0; e < 8; ++e) v[e] = to_f(w.v[e]);
         return;
     }
+    X w[8];                                     // unconditional loads, so that all eight are under way together
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int k = place<VEC>(tid, n, i, e);
-        v[e] = k < K ? to_f(p[k]) : 0.f;
-    }
+    for (int e = 0; e < 8; ++e) w[e] = p[min(place<VEC>(tid, n, i, e), K - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = place<VEC>(tid, n, i, e) < K ? to_f(w[e]) : 0.f;
 }
 
 template <typename X, bool VEC>

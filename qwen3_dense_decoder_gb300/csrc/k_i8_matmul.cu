@@ -1,0 +1,539 @@
+// k_i8_matmul.cu -- out[t][m] = (sum_k x[t][k] w[m][k]) xs[t] ws[m] over 8-bit
+// codes on tcgen05, for more than a few rows of x.
+//
+// sm_103a has no integer kind of tcgen05.mma.  An int8 code is an fp16 number,
+// and FP32 sums of products of two are exact up to 2^24: 1,024 products of 128 x
+// 128.  So kind::f16 sums chunks of 1,024 inputs in tensor memory, and the
+// epilogue's warps add the chunks as 32-bit integers in registers: the exact
+// whole number, at the 16-bit rate, from 8-bit operands in memory.
+//
+// A CTA (or with CG == 2 a pair of CTAs, each with its own 128 channels and half
+// of the tokens) takes a tile of 128 CG channels by bn tokens:
+//   TMA      int8 tiles of 128 channels and of the tokens by 128 inputs into a ring
+//   warps 0..3  expand the channels' codes to fp16 in tensor memory (operand A; a
+//               thread owns a TMEM lane, a channel), 64 inputs a step
+//   warps 4..7  expand the tokens' codes to fp16 in shared memory (operand B)
+//   one thread issues the products (of a pair, the first CTA's for both)
+//   warps 8..15 add chunks, then scale and store
+// Weights pass through shared memory once as bytes and never as fp16.  With
+// fewer tiles than SMs a cluster of CTAs shares a tile's inputs (splits) and joins
+// the whole-number sums through distributed shared memory: the same number.
+#include <cooperative_groups.h>
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace q3 {
+
+namespace {
+
+constexpr int THREADS = 640;
+constexpr int BM = 128;                          // channels of a CTA
+constexpr int STAGE_K = 128, STEP_K = 64;        // inputs of a ring stage, of an expanded step
+constexpr int CHUNK = 8;                         // stages that FP32 sums exactly: 1,024 inputs
+constexpr int NC = 4;                            // expanded steps under way
+constexpr int MAX_NS = 8;
+constexpr int A_RAW = BM * STAGE_K;
+constexpr uint32_t TMEM_COLS = 512, T_A = TMEM_COLS - NC * 32;
+constexpr int TMA_WARP = 16, MMA_WARP = 17;
+// registers of a thread by warpgroup; 640 threads launch with 96
+constexpr int R_EXPAND = 72, R_EPILOGUE = 144, R_ISSUE = 48, R_LAUNCH = 96;
+static_assert(2 * R_EXPAND + 2 * R_EPILOGUE + R_ISSUE <= 5 * R_LAUNCH, "registers");
+
+constexpr size_t MAX_SMEM = 227 * 1024;
+constexpr int I8_SMS = 152;
+
+struct I8GemmArgs {
+    I8MatmulArgs a;
+    int bn, splits, ns;              // tokens of a tile, CTAs that share its inputs, ring stages
+    int m_tiles, n_tiles;
+};
+
+struct Bars {
+    uint64_t raw_full[MAX_NS], raw_empty[MAX_NS];
+    uint64_t half_full[NC], half_empty[NC];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// the rings (B's rows: rows_b tokens), the barriers and what alignment may take
+constexpr size_t smem_bytes(int rows_b, int ns) {
+    return (size_t)ns * (A_RAW + rows_b * STAGE_K) + NC * (size_t)rows_b * STEP_K * 2 + sizeof(Bars) + 1024;
+}
+
+template <int R> Q3_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
+template <int R> Q3_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
+
+// Bounded wait (in line: a call would keep the warpgroups from registers of their own)
+Q3_DEV bool wait_long(uint64_t* bar, uint32_t parity, int* abort, int* status) {
+    uint64_t t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 512; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*(volatile int*)abort) return false;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > Q3_WAIT_LIMIT_NS) {
+            if (status) set_status(status, Q3_STATUS_TIMEOUT);
+            *(volatile int*)abort = 1;
+            return false;
+        }
+    }
+}
+// What ends a role's copies or products on its way out, bounded too
+Q3_DEV void wait_last(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity) && global_ns() - t0 < Q3_WAIT_LIMIT_NS) {}
+}
+// By a whole warp, of one mind about the outcome
+Q3_DEV bool wait_warp(uint64_t* bar, uint32_t parity, Bars& b, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_long(bar, parity, &b.abort, status));
+}
+// arrive on CTA 0's barrier of the pair
+template <int CG> Q3_DEV void arrive_first(uint64_t* bar) {
+    if (CG == 1) {
+        mbar_arrive(bar);
+    } else {
+        asm volatile("{\n\t.reg .b32 a;\n\t"
+                     "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+                     "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}"
+                     :: "r"(smem_u32(bar)) : "memory");
+    }
+}
+// D[tmem] (+)= A[tmem] B[smem], of one CTA or of a pair
+template <int CG> Q3_DEV void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if (CG == 1) {
+        tc_mma_f16_ts(d, a, b, idesc, add);
+    } else {
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                     :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    }
+}
+// arrive, on both CTAs' barriers of a pair, once the products issued so far are done
+template <int CG> Q3_DEV void commit(uint64_t* bar) {
+    if (CG == 1) {
+        tc_commit(bar);
+    } else {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+    }
+}
+template <int CG> Q3_DEV void alloc(uint32_t* dst) {
+    if (CG == 1) {
+        tmem_alloc(dst, TMEM_COLS);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(dst)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG> Q3_DEV void dealloc(uint32_t t) {
+    if (CG == 1) tmem_dealloc(t, TMEM_COLS);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(t), "r"(TMEM_COLS) : "memory");
+}
+
+// Four codes as two pairs of fp16: a byte with its sign bit flipped, under 0x64,
+// is the fp16 1,024 + 128 + code
+Q3_DEV void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t f = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    const uint32_t l = __byte_perm(f, 0x64646464u, 0x4140), h = __byte_perm(f, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), bias), b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+Q3_DEV void expand16(const uint4& w, uint32_t* r) {
+    expand4(w.x, r[0], r[1]);
+    expand4(w.y, r[2], r[3]);
+    expand4(w.z, r[4], r[5]);
+    expand4(w.w, r[6], r[7]);
+}
+
+// A place in a ring of n: the slot, the parity of its use, whether it is the first use
+struct Ring {
+    uint32_t n, slot = 0, phase = 0;
+    bool first = true;
+    Q3_DEV explicit Ring(uint32_t n) : n(n) {}
+    Q3_DEV void next() {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+            first = false;
+        }
+    }
+};
+
+Q3_DEV uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+Q3_DEV void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <typename O> Q3_DEV void put(O* p, float v, bool& bad);
+template <> Q3_DEV void put<float>(float* p, float v, bool&) { *p = v; }
+template <> Q3_DEV void put<__half>(__half* p, float v, bool& bad) { *p = to_f16(v, bad); }
+template <> Q3_DEV void put<__nv_bfloat16>(__nv_bfloat16* p, float v, bool&) { *p = __float2bfloat16_rn(v); }
+
+// A thread's sums of one channel, columns first .. of `n` tokens from t0: scaled
+// and stored
+template <typename O, int ACC>
+Q3_DEV void store_sums(const I8MatmulArgs& a, const int (&acc)[ACC], const float (&xs)[ACC / 32], int64_t m, int t0, int n, float ws, bool& bad)
+{
+    const bool live = m < a.M;
+    O* p = static_cast<O*>(a.out) + (int64_t)t0 * a.out_stride + m;
+#pragma unroll
+    for (int j = 0; j < ACC; ++j) {
+        const float x = __shfl_sync(0xffffffffu, xs[j / 32], j % 32);
+        if (j < n && live) put<O>(p, (float)acc[j] * x * ws, bad);
+        p += a.out_stride;
+    }
+}
+
+template <int CG>
+__global__ void __launch_bounds__(THREADS, 1)
+i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const I8GemmArgs p)
+{
+    constexpr int ACC = CG == 2 ? 96 : 64;       // tokens of an epilogue warp
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const I8MatmulArgs& a = p.a;
+    const int rows_b = p.bn / CG;                // tokens of this CTA's B operand
+    const int stage_bytes = A_RAW + rows_b * STAGE_K, step_bytes = rows_b * STEP_K * 2;
+    uint8_t* half = smem + p.ns * stage_bytes;   // operand B in fp16, NC steps
+    Bars& b = *reinterpret_cast<Bars*>(half + NC * step_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int size = CG == 2 ? 2 : p.splits;     // CTAs of a cluster
+    const int rank = size > 1 ? (int)(blockIdx.x % size) : 0;
+    int* status = a.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.ns; ++s) {
+            mbar_init(&b.raw_full[s], 1);
+            mbar_init(&b.raw_empty[s], 8);
+        }
+        for (int c = 0; c < NC; ++c) {
+            mbar_init(&b.half_full[c], 8 * CG);
+            mbar_init(&b.half_empty[c], 1);
+        }
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(&b.acc_full[c], 1);
+            mbar_init(&b.acc_empty[c], 8 * CG);
+        }
+        mbar_init(&b.drain, 1);
+        b.abort = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tw);
+        prefetch_tmap(&tx);
+    }
+    if (warp == MMA_WARP) alloc<CG>(&b.tmem);
+    tc_fence_before();
+    __syncthreads();
+    if (size > 1) cg::this_cluster().sync();     // every CTA's barriers are there
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    grid_dep_wait();
+
+    // units of work: (weight tile, token tile), token tiles first; a split cluster
+    // has one and shares its stages
+    const int kt = (a.K + STAGE_K - 1) / STAGE_K;
+    const int split = CG == 1 && p.splits > 1 ? rank : 0, splits = CG == 1 ? p.splits : 1;
+    const int s0 = (int)((int64_t)kt * split / splits), s1 = (int)((int64_t)kt * (split + 1) / splits);
+    const int units = p.m_tiles * p.n_tiles, first = blockIdx.x / size, stride = gridDim.x / size;
+    const int stages = s1 - s0, chunks = (stages + CHUNK - 1) / CHUNK;
+
+    if (warp < 8) {
+        // ---------------- expanding: A into tensor memory (warps 0..3), B into shared memory (4..7)
+        reg_dec<R_EXPAND>();
+        const bool is_a = warp < 4;
+        const int row = (warp & 3) * 32 + lane;
+        const bool live = is_a || row < rows_b;
+        const uint32_t swz = (uint32_t)(row & 7);
+        const uint32_t src0 = smem_u32(smem) + (is_a ? 0 : A_RAW) + row * 128;
+        const uint32_t dst0 = smem_u32(half) + row * 128;
+        const uint32_t ta0 = tmem + ((uint32_t)(warp & 3) * 32 << 16) + T_A;
+        Ring raw(p.ns), half_at(NC);
+        bool ok = true;
+        for (int u = first; u < units && ok; u += stride) {
+            for (int s = 0; s < stages && ok; ++s, raw.next()) {
+                if (!(ok = wait_warp(&b.raw_full[raw.slot], raw.phase, b, status))) break;
+                const uint32_t src = src0 + raw.slot * stage_bytes;
+                uint4 w[8];
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = lds16(src + ((j ^ swz) << 4));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h, half_at.next()) {
+                    const uint32_t c = half_at.slot;
+                    if (!(ok = half_at.first || wait_warp(&b.half_empty[c], half_at.phase ^ 1, b, status))) break;
+                    if (is_a) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t r[16];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) expand16(w[4 * h + 2 * i + j], r + 8 * j);
+                            tmem_st_32x32b_x16(ta0 + c * 32 + i * 16, r);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    } else {
+                        if (live) {
+                            const uint32_t dst = dst0 + c * step_bytes;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t r[8];
+                                expand16(w[4 * h + j], r);
+                                sts16(dst + (((2 * j) ^ swz) << 4), r[0], r[1], r[2], r[3]);
+                                sts16(dst + (((2 * j + 1) ^ swz) << 4), r[4], r[5], r[6], r[7]);
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive_first<CG>(&b.half_full[c]);
+                        if (h == 0) mbar_arrive(&b.raw_empty[raw.slot]);
+                    }
+                }
+            }
+        }
+        // the products' last arrivals on this CTA's barriers
+        for (int i = 0; i < NC && ok; ++i, half_at.next())
+            if (!half_at.first) wait_warp(&b.half_empty[half_at.slot], half_at.phase ^ 1, b, status);
+    } else if (warp < TMA_WARP) {
+        // ---------------- epilogue: quadrant warp % 4 of the lanes, half the columns
+        reg_inc<R_EPILOGUE>();
+        const int part = (warp - 8) >> 2, cols = p.bn / 2;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) * 32 << 16);
+        Ring acc_at(2);
+        bool ok = true, bad = false;
+        for (int u = first; u < units && ok; u += stride) {
+            const int nt = u % p.n_tiles, mt = u / p.n_tiles;
+            const int64_t m = (int64_t)mt * (BM * CG) + (CG == 2 ? rank * BM : 0) + (warp & 3) * 32 + lane;
+            const int t0 = nt * p.bn + part * cols;
+            int acc[ACC];
+#pragma unroll
+            for (int j = 0; j < ACC; ++j) acc[j] = 0;
+            for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
+                const uint32_t d = acc_at.slot;
+                if (!(ok = wait_warp(&b.acc_full[d], acc_at.phase, b, status))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < ACC / 16; ++g) {
+                    if (g * 16 < cols) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(lanes + d * p.bn + part * cols + g * 16, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[g * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first<CG>(&b.acc_empty[d]);
+            }
+            if (!ok) break;
+            if (CG == 1 && splits > 1) {
+                // this CTA's share of the sums, [token][channel], where its operands were
+                int* red = reinterpret_cast<int*>(smem);
+#pragma unroll
+                for (int j = 0; j < ACC; ++j)
+                    if (j < cols) red[(part * cols + j) * BM + (warp & 3) * 32 + lane] = acc[j];
+                break;
+            }
+            float xs[ACC / 32];
+#pragma unroll
+            for (int i = 0; i < ACC / 32; ++i) {
+                const int t = t0 + i * 32 + lane;
+                xs[i] = i * 32 + lane < cols && t < a.T ? a.xs[t] : 0.f;
+            }
+            const float ws = m < a.M ? a.ws[m] : 0.f;
+            const int n = min(cols, a.T - t0);
+            switch (a.out_type) {
+            case Q3_TYPE_F32: store_sums<float, ACC>(a, acc, xs, m, t0, n, ws, bad); break;
+            case Q3_TYPE_F16: store_sums<__half, ACC>(a, acc, xs, m, t0, n, ws, bad); break;
+            default: store_sums<__nv_bfloat16, ACC>(a, acc, xs, m, t0, n, ws, bad);
+            }
+        }
+        if (bad && status) set_status(status, Q3_STATUS_F16_RANGE);
+    } else {
+        reg_dec<R_ISSUE>();
+        if (warp == TMA_WARP) {
+            Ring raw(p.ns);
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride) {
+                const int nt = u % p.n_tiles, mt = u / p.n_tiles;
+                const int m0 = mt * (BM * CG) + (CG == 2 ? rank * BM : 0), n0 = nt * p.bn + (CG == 2 ? rank * rows_b : 0);
+                for (int s = s0; s < s1; ++s, raw.next()) {
+                    if (!(ok = raw.first || wait_warp(&b.raw_empty[raw.slot], raw.phase ^ 1, b, status))) break;
+                    uint8_t* dst = smem + raw.slot * stage_bytes;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&b.raw_full[raw.slot], stage_bytes);
+                        tma_load_2d(dst, &tw, &b.raw_full[raw.slot], s * STAGE_K, m0);
+                        tma_load_2d(dst + A_RAW, &tx, &b.raw_full[raw.slot], s * STAGE_K, n0);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok)                             // copies still under way end before the CTA does
+                for (int i = 0; i < p.ns; ++i, raw.next())
+                    if (!raw.first) wait_last(&b.raw_full[raw.slot], raw.phase ^ 1);
+        } else if (warp == MMA_WARP && (CG == 1 || rank == 0)) {
+            const uint32_t idesc = idesc_f16_f32(BM * CG, 0) | ((uint32_t)(p.bn >> 3) << 17);
+            Ring half_at(NC), acc_at(2);
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride) {
+                for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
+                    if (!(ok = acc_at.first || wait_warp(&b.acc_empty[acc_at.slot], acc_at.phase ^ 1, b, status))) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + acc_at.slot * p.bn;
+                    const int steps = 2 * min(CHUNK, stages - c * CHUNK);
+                    for (int k = 0; k < steps; ++k, half_at.next()) {
+                        if (!(ok = wait_warp(&b.half_full[half_at.slot], half_at.phase, b, status))) break;
+                        tc_fence_after();
+                        const uint64_t desc = smem_desc_sw128(smem_u32(half) + half_at.slot * step_bytes);
+                        const uint32_t ta = tmem + T_A + half_at.slot * 32;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int j = 0; j < STEP_K / 16; ++j) mma<CG>(d, ta + j * 8, desc + j * 2, idesc, k > 0 || j > 0);
+                            commit<CG>(&b.half_empty[half_at.slot]);
+                            if (k + 1 == steps) commit<CG>(&b.acc_full[acc_at.slot]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) {                           // as do products
+                if (elect_one()) commit<CG>(&b.drain);
+                __syncwarp();
+                wait_last(&b.drain, 0);
+            }
+        }
+        __syncwarp();
+    }
+    // The roles have ended and all warps of a warpgroup are here before its registers
+    // change again; what follows is for all warps alike.
+    __syncthreads();
+    if (CG == 1) {
+        if (warp >= TMA_WARP) reg_inc<R_EXPAND>();
+        else if (warp >= 8) reg_dec<R_EXPAND>();
+    }
+    if (CG == 1 && splits > 1) {
+        // the cluster's sums, a share of the tokens each
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        if (first < units && !b.abort) {
+            const int nt = first % p.n_tiles, mt = first / p.n_tiles;
+            const int c0 = p.bn * rank / splits, c1 = p.bn * (rank + 1) / splits;
+            bool bad = false;
+            for (int i = c0 * 32 + threadIdx.x; i < c1 * 32; i += THREADS) {
+                const int col = i >> 5, t = nt * p.bn + col;
+                const int64_t m = (int64_t)mt * BM + (i & 31) * 4;
+                if (t >= a.T || m >= a.M) continue;
+                int4 s = make_int4(0, 0, 0, 0);
+                for (int r = 0; r < splits; ++r) {
+                    const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(reinterpret_cast<int*>(smem), r) + i * 4);
+                    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+                }
+                const int sums[4] = {s.x, s.y, s.z, s.w};
+                const float xs = a.xs[t];
+                for (int e = 0; e < 4; ++e) {
+                    if (m + e >= a.M) break;
+                    const float v = (float)sums[e] * xs * a.ws[m + e];
+                    const int64_t at = (int64_t)t * a.out_stride + m + e;
+                    switch (a.out_type) {
+                    case Q3_TYPE_F32: put(static_cast<float*>(a.out) + at, v, bad); break;
+                    case Q3_TYPE_F16: put(static_cast<__half*>(a.out) + at, v, bad); break;
+                    default: put(static_cast<__nv_bfloat16*>(a.out) + at, v, bad);
+                    }
+                }
+            }
+            if (bad && status) set_status(status, Q3_STATUS_F16_RANGE);
+        }
+    }
+    if (size > 1) cg::this_cluster().sync();     // no CTA's memory is in use by another
+    if (warp == MMA_WARP) dealloc<CG>(tmem);
+}
+
+template <int CG>
+cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8GemmArgs& p)
+{
+    // the attribute and the registers that the warpgroups' split counts on, once a device
+    static std::atomic<int> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, i8_gemm_kernel<CG>)) != cudaSuccess) return e;
+        if (at.numRegs < R_LAUNCH) return cudaErrorLaunchOutOfResources;
+        if ((e = cudaFuncSetAttribute(i8_gemm_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MAX_SMEM)) != cudaSuccess) return e;
+        ready[dev].store(1, std::memory_order_release);
+    }
+    const int size = CG == 2 ? 2 : p.splits, units = p.m_tiles * p.n_tiles;
+    const int ctas = CG == 1 && p.splits > 1 ? units : std::min(units, I8_SMS / size);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * size));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes(p.bn / CG, p.ns);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = L.pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = size > 1 ? 2 : 1;
+    if (L.counter) ++*L.counter;
+    return cudaLaunchKernelEx(&cfg, i8_gemm_kernel<CG>, tw, tx, p);
+}
+
+}  // namespace
+
+// How a product is shared out: a pair of CTAs for many tokens; else 128 channels a
+// CTA, and with fewer tiles than SMs a cluster for each.
+I8Plan i8_plan(int T, int M, int K)
+{
+    I8Plan q{};
+    const int kt = (K + STAGE_K - 1) / STAGE_K;
+    q.cg = T > 256 ? 2 : 1;
+    q.bn = q.cg == 2 ? 192 : std::min(128, (T + 15) / 16 * 16);
+    const int tiles = (M + 127) / 128 * ((T + q.bn - 1) / q.bn);
+    q.splits = 1;
+    if (q.cg == 1)
+        while (q.splits < 8 && tiles * (q.splits + 1) <= I8_SMS && kt / (q.splits + 1) >= 4) ++q.splits;
+    q.ns = 2;
+    while (q.ns < MAX_NS && smem_bytes(q.bn / q.cg, q.ns + 1) <= MAX_SMEM) ++q.ns;
+    return q;
+}
+
+cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q)
+{
+    // what tcgen05.mma takes: 16 k tokens for 128 channels, 32 k for a pair's 256
+    if (q.bn % (16 * q.cg) || q.bn < 16 * q.cg || q.bn > (q.cg == 2 ? 192 : 128)) return cudaErrorInvalidValue;
+    I8GemmArgs p{};
+    p.a = a;
+    p.bn = q.bn; p.splits = q.splits; p.ns = q.ns;
+    p.m_tiles = (a.M + 128 * q.cg - 1) / (128 * q.cg);
+    p.n_tiles = (a.T + q.bn - 1) / q.bn;
+    return q.cg == 2 ? launch_cg<2>(L, tw, tx, p) : launch_cg<1>(L, tw, tx, p);
+}
+
+}  // namespace q3

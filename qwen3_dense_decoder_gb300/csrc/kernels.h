@@ -463,7 +463,15 @@ struct I8MatmulArgs {
     int64_t out_stride;
     int* status;               // or null
 };
+// For at most this many rows of x; beyond, on tcgen05.
+constexpr int I8_MATVEC_ROWS = 8;
 cudaError_t launch_i8_matvec(const Launch& L, const I8MatmulArgs& a);
+// CTAs of a tile (2: a pair with 256 channels), its tokens, CTAs that
+// share its inputs, ring stages.  tw: w in boxes of 128 rows by 128 inputs; tx: x in
+// boxes of bn / cg rows.
+struct I8Plan { int cg, bn, splits, ns; };
+I8Plan i8_plan(int T, int M, int K);
+cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q);
 
 // Q8_0: canonical blocks -> (int8 plane, fp16 scale plane); planes -> fp16
 // tensor-core operand; bf16 -> canonical blocks.

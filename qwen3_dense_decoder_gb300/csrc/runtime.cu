@@ -125,6 +125,20 @@ bool tmap_q16(CUtensorMap* m, const void* ptr, uint64_t T, uint64_t n_q, int64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of 8-bit codes, stride bytes apart, in boxes of 128 codes by box_rows rows.
+bool tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int64_t stride, uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {(cuuint64_t)stride};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t elem[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 struct Q8Planes {
@@ -2607,7 +2621,16 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
     a.T = T; a.M = M; a.K = K;
     a.out = out_dev; a.out_type = out_type; a.out_stride = out_stride;
     a.status = status_dev;
-    const cudaError_t e = launch_i8_matvec(op_launch(stream), a);
+    cudaError_t e;
+    if (T <= I8_MATVEC_ROWS) {
+        e = launch_i8_matvec(op_launch(stream), a);
+    } else {
+        const I8Plan q = i8_plan(T, M, K);
+        CUtensorMap tw, tx;
+        if (!tmap_i8(&tw, w_dev, M, K, w_stride, 128) || !tmap_i8(&tx, x_dev, T, K, x_stride, q.bn / q.cg))
+            return fail(Q3_ERR_CUDA, "op_i8_matmul: tensor map encoding failed");
+        e = launch_i8_gemm(op_launch(stream), tw, tx, a, q);
+    }
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_matmul: %s", cudaGetErrorString(e));
     return Q3_OK;
 }

@@ -10,9 +10,9 @@
 // A CTA (or with CG == 2 a pair of CTAs, each with its own 128 channels and half
 // of the tokens) takes a tile of 128 CG channels by bn tokens:
 //   TMA      int8 tiles of 128 channels and of the tokens by 128 inputs into a ring
-//   warps 0..3  expand the channels' codes to fp16 in tensor memory (operand A; a
-//               thread owns a TMEM lane, a channel), 64 inputs a step
-//   warps 4..7  expand the tokens' codes to fp16 in shared memory (operand B)
+//   warps 0..3, 4..7  expand every other stage to fp16: the tokens' codes in shared
+//               memory (operand B), then the channels' in tensor memory (operand A;
+//               a thread owns a TMEM lane, a channel)
 //   one thread issues the products (of a pair, the first CTA's for both)
 //   warps 8..15 add chunks, then scale and store
 // Weights pass through shared memory once as bytes and never as fp16.  With
@@ -35,12 +35,12 @@ namespace {
 
 constexpr int THREADS = 640;
 constexpr int BM = 128;                          // channels of a CTA
-constexpr int STAGE_K = 128, STEP_K = 64;        // inputs of a ring stage, of an expanded step
+constexpr int STAGE_K = 128;                     // inputs of a stage
 constexpr int CHUNK = 8;                         // stages that FP32 sums exactly: 1,024 inputs
-constexpr int NC = 4;                            // expanded steps under way
+constexpr int NA = 2, NB = 3;                    // expanded stages: A's and B's
 constexpr int MAX_NS = 8;
 constexpr int A_RAW = BM * STAGE_K;
-constexpr uint32_t TMEM_COLS = 512, T_A = TMEM_COLS - NC * 32;
+constexpr uint32_t TMEM_COLS = 512, A_COLS = STAGE_K / 2, T_A = TMEM_COLS - NA * A_COLS;
 constexpr int TMA_WARP = 16, MMA_WARP = 17;
 // registers of a thread by warpgroup; 640 threads launch with 96
 constexpr int R_EXPAND = 72, R_EPILOGUE = 144, R_ISSUE = 48, R_LAUNCH = 96;
@@ -57,7 +57,7 @@ struct I8GemmArgs {
 
 struct Bars {
     uint64_t raw_full[MAX_NS], raw_empty[MAX_NS];
-    uint64_t half_full[NC], half_empty[NC];
+    uint64_t full[NA], a_empty[NA], b_empty[NB];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
@@ -65,7 +65,7 @@ struct Bars {
 
 // the rings (B's rows: rows_b tokens), the barriers and what alignment may take
 constexpr size_t smem_bytes(int rows_b, int ns) {
-    return (size_t)ns * (A_RAW + rows_b * STAGE_K) + NC * (size_t)rows_b * STEP_K * 2 + sizeof(Bars) + 1024;
+    return (size_t)ns * (A_RAW + rows_b * STAGE_K) + NB * (size_t)rows_b * STAGE_K * 2 + sizeof(Bars) + 1024;
 }
 
 template <int R> Q3_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
@@ -212,9 +212,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const I8MatmulArgs& a = p.a;
     const int rows_b = p.bn / CG;                // tokens of this CTA's B operand
-    const int stage_bytes = A_RAW + rows_b * STAGE_K, step_bytes = rows_b * STEP_K * 2;
-    uint8_t* half = smem + p.ns * stage_bytes;   // operand B in fp16, NC steps
-    Bars& b = *reinterpret_cast<Bars*>(half + NC * step_bytes);
+    const int stage_bytes = A_RAW + rows_b * STAGE_K, half_bytes = rows_b * STAGE_K * 2;
+    uint8_t* half = smem + p.ns * stage_bytes;   // operand B in fp16: NB stages, each 64 inputs and 64 more
+    Bars& b = *reinterpret_cast<Bars*>(half + NB * half_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int size = CG == 2 ? 2 : p.splits;     // CTAs of a cluster
     const int rank = size > 1 ? (int)(blockIdx.x % size) : 0;
@@ -223,12 +223,13 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.ns; ++s) {
             mbar_init(&b.raw_full[s], 1);
-            mbar_init(&b.raw_empty[s], 8);
+            mbar_init(&b.raw_empty[s], 4);
         }
-        for (int c = 0; c < NC; ++c) {
-            mbar_init(&b.half_full[c], 8 * CG);
-            mbar_init(&b.half_empty[c], 1);
+        for (int c = 0; c < NA; ++c) {
+            mbar_init(&b.full[c], 4 * CG);
+            mbar_init(&b.a_empty[c], 1);
         }
+        for (int c = 0; c < NB; ++c) mbar_init(&b.b_empty[c], 1);
         for (int c = 0; c < 2; ++c) {
             mbar_init(&b.acc_full[c], 1);
             mbar_init(&b.acc_empty[c], 8 * CG);
@@ -256,65 +257,70 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const int stages = s1 - s0, chunks = (stages + CHUNK - 1) / CHUNK;
 
     if (warp < 8) {
-        // ---------------- expanding: A into tensor memory (warps 0..3), B into shared memory (4..7)
+        // ---------------- expanding: a warpgroup takes every other stage
         reg_dec<R_EXPAND>();
-        const bool is_a = warp < 4;
-        const int row = (warp & 3) * 32 + lane;
-        const bool live = is_a || row < rows_b;
+        const int mine = warp >> 2, row = (warp & 3) * 32 + lane;
+        const bool live = row < rows_b;
         const uint32_t swz = (uint32_t)(row & 7);
-        const uint32_t src0 = smem_u32(smem) + (is_a ? 0 : A_RAW) + row * 128;
-        const uint32_t dst0 = smem_u32(half) + row * 128;
-        const uint32_t ta0 = tmem + ((uint32_t)(warp & 3) * 32 << 16) + T_A;
-        Ring raw(p.ns), half_at(NC);
+        const uint32_t src0 = smem_u32(smem) + row * 128, dst0 = smem_u32(half) + row * 128;
+        const uint32_t ta = tmem + ((uint32_t)(warp & 3) * 32 << 16) + T_A + mine * A_COLS;
+        Ring raw(p.ns), a_at(NA), b_at(NB);
         bool ok = true;
         for (int u = first; u < units && ok; u += stride) {
-            for (int s = 0; s < stages && ok; ++s, raw.next()) {
+            for (int s = 0; s < stages && ok; ++s, raw.next(), a_at.next(), b_at.next()) {
+                if ((int)a_at.slot != mine) continue;
                 if (!(ok = wait_warp(&b.raw_full[raw.slot], raw.phase, b, status))) break;
                 const uint32_t src = src0 + raw.slot * stage_bytes;
-                uint4 w[8];
-                if (live) {
+                uint4 w[2][4];
+                auto load = [&](uint4 (&v)[4], uint32_t from, int h) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = lds16(src + ((j ^ swz) << 4));
+                    for (int j = 0; j < 4; ++j) v[j] = lds16(from + (((h * 4 + j) ^ swz) << 4));
+                };
+                if (live) load(w[0], src + A_RAW, 0);
+                if (!(ok = b_at.first || wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status))) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 0) { if (live) load(w[1], src + A_RAW, 1); }
+                    else load(w[0], src, 0);
+                    if (live) {
+                        const uint32_t dst = dst0 + b_at.slot * half_bytes + h * (half_bytes / 2);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t r[8];
+                            expand16(w[h][j], r);
+                            sts16(dst + (((2 * j) ^ swz) << 4), r[0], r[1], r[2], r[3]);
+                            sts16(dst + (((2 * j + 1) ^ swz) << 4), r[4], r[5], r[6], r[7]);
+                        }
+                    }
                 }
+                if (!(ok = a_at.first || wait_warp(&b.a_empty[mine], a_at.phase ^ 1, b, status))) break;
+                tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h, half_at.next()) {
-                    const uint32_t c = half_at.slot;
-                    if (!(ok = half_at.first || wait_warp(&b.half_empty[c], half_at.phase ^ 1, b, status))) break;
-                    if (is_a) {
-                        tc_fence_after();
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 0) load(w[1], src, 1);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t r[16];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) expand16(w[4 * h + 2 * i + j], r + 8 * j);
-                            tmem_st_32x32b_x16(ta0 + c * 32 + i * 16, r);
-                        }
-                        tmem_st_wait();
-                        tc_fence_before();
-                    } else {
-                        if (live) {
-                            const uint32_t dst = dst0 + c * step_bytes;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t r[8];
-                                expand16(w[4 * h + j], r);
-                                sts16(dst + (((2 * j) ^ swz) << 4), r[0], r[1], r[2], r[3]);
-                                sts16(dst + (((2 * j + 1) ^ swz) << 4), r[4], r[5], r[6], r[7]);
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t r[16];
+                        expand16(w[h][2 * i], r);
+                        expand16(w[h][2 * i + 1], r + 8);
+                        tmem_st_32x32b_x16(ta + h * 32 + i * 16, r);
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        arrive_first<CG>(&b.half_full[c]);
-                        if (h == 0) mbar_arrive(&b.raw_empty[raw.slot]);
-                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    arrive_first<CG>(&b.full[mine]);
+                    mbar_arrive(&b.raw_empty[raw.slot]);
                 }
             }
         }
         // the products' last arrivals on this CTA's barriers
-        for (int i = 0; i < NC && ok; ++i, half_at.next())
-            if (!half_at.first) wait_warp(&b.half_empty[half_at.slot], half_at.phase ^ 1, b, status);
+        for (int i = 0; i < NA && ok; ++i, a_at.next())
+            if (!a_at.first) wait_warp(&b.a_empty[a_at.slot], a_at.phase ^ 1, b, status);
+        for (int i = 0; i < NB && ok; ++i, b_at.next())
+            if (!b_at.first) wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status);
     } else if (warp < TMA_WARP) {
         // ---------------- epilogue: quadrant warp % 4 of the lanes, half the columns
         reg_inc<R_EPILOGUE>();
@@ -395,24 +401,26 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                     if (!raw.first) wait_last(&b.raw_full[raw.slot], raw.phase ^ 1);
         } else if (warp == MMA_WARP && (CG == 1 || rank == 0)) {
             const uint32_t idesc = idesc_f16_f32(BM * CG, 0) | ((uint32_t)(p.bn >> 3) << 17);
-            Ring half_at(NC), acc_at(2);
+            Ring a_at(NA), b_at(NB), acc_at(2);
             bool ok = true;
             for (int u = first; u < units && ok; u += stride) {
                 for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
                     if (!(ok = acc_at.first || wait_warp(&b.acc_empty[acc_at.slot], acc_at.phase ^ 1, b, status))) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc_at.slot * p.bn;
-                    const int steps = 2 * min(CHUNK, stages - c * CHUNK);
-                    for (int k = 0; k < steps; ++k, half_at.next()) {
-                        if (!(ok = wait_warp(&b.half_full[half_at.slot], half_at.phase, b, status))) break;
+                    const int n = min(CHUNK, stages - c * CHUNK);
+                    for (int k = 0; k < n; ++k, a_at.next(), b_at.next()) {
+                        if (!(ok = wait_warp(&b.full[a_at.slot], a_at.phase, b, status))) break;
                         tc_fence_after();
-                        const uint64_t desc = smem_desc_sw128(smem_u32(half) + half_at.slot * step_bytes);
-                        const uint32_t ta = tmem + T_A + half_at.slot * 32;
+                        const uint64_t desc = smem_desc_sw128(smem_u32(half) + b_at.slot * half_bytes);
+                        const uint32_t ta = tmem + T_A + a_at.slot * A_COLS, next64 = half_bytes >> 5;
                         if (elect_one()) {
 #pragma unroll
-                            for (int j = 0; j < STEP_K / 16; ++j) mma<CG>(d, ta + j * 8, desc + j * 2, idesc, k > 0 || j > 0);
-                            commit<CG>(&b.half_empty[half_at.slot]);
-                            if (k + 1 == steps) commit<CG>(&b.acc_full[acc_at.slot]);
+                            for (int j = 0; j < STAGE_K / 16; ++j)
+                                mma<CG>(d, ta + j * 8, desc + (j & 3) * 2 + (j >> 2) * next64, idesc, k > 0 || j > 0);
+                            commit<CG>(&b.a_empty[a_at.slot]);
+                            commit<CG>(&b.b_empty[b_at.slot]);
+                            if (k + 1 == n) commit<CG>(&b.acc_full[acc_at.slot]);
                         }
                         __syncwarp();
                     }

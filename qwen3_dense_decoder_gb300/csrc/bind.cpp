@@ -35,6 +35,7 @@ decltype(&q3_op_i8_quantize) p_i8_quantize;
 decltype(&q3_op_i8_norm) p_i8_norm;
 decltype(&q3_op_i8_swiglu) p_i8_swiglu;
 decltype(&q3_op_i8_matmul) p_i8_matmul;
+decltype(&q3_i8_matmul_workspace) p_i8_workspace;
 PyObject* g_check;
 
 struct Refusal { std::string what; };        // becomes a ValueError
@@ -488,13 +489,13 @@ PyObject* i8_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
     Q3_END
 }
 
-// (x, x_scales, w, w_scales, out, dtype, status, stream)
+// (x, x_scales, w, w_scales, out, dtype, workspace, status, stream)
 PyObject* i8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     Q3_BEGIN
-    const Args c("op_i8_matmul", a, n, 8);
+    const Args c("op_i8_matmul", a, n, 9);
     const at::Tensor &x = c.tensor(0), &xs = c.tensor(1), &wt = c.tensor(2), &ws = c.tensor(3);
-    const at::Tensor *given = c.maybe(4), *status = c.maybe(6);
+    const at::Tensor *given = c.maybe(4), *space = c.maybe(6), *status = c.maybe(7);
     i8_codes(c, "x", x);
     i8_codes(c, "w", wt);
     const int T = c.size(x, 0), K = c.size(x, 1), M = c.size(wt, 0);
@@ -513,16 +514,25 @@ PyObject* i8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
             c.refuse("out must be [" + std::to_string(T) + ", " + std::to_string(M) + "], of dtype where that is given");
     }
     if (status) int32(c, "status", *status, {1});
-    const Where w(c, {&x, &xs, &wt, &ws, given, status}, a[7], T > 0);
-    at::Tensor out;
+    const Where w(c, {&x, &xs, &wt, &ws, given, space, status}, a[8], T > 0);
+    int64_t need = 0;
+    if (T > 0) {
+        check(p_i8_workspace(T, M, K, &need));
+        if (space && (space->scalar_type() != at::kByte || !space->is_contiguous() || space->numel() < need))
+            c.refuse("workspace must be contiguous uint8, at least " + std::to_string(need) + " bytes");
+    }
+    at::Tensor out, room;
     if (given) out = *given;
+    if (space) room = *space;
     int rc = 0;
     {
         const Unlocked other_threads_run;
         if (!out.defined()) out = w.make({T, M}, type);
-        if (T > 0)
+        if (T > 0) {
+            if (need && !room.defined()) room = w.make({need}, at::kByte);
             rc = p_i8_matmul(ptr<int8_t>(x), code_stride(x), ptr<float>(xs), ptr<int8_t>(wt), code_stride(wt), ptr<float>(ws), T, M, K, ptr(out),
-                             type_of(out), row_stride(out), ptr<int32_t>(status), w.stream());
+                             type_of(out), row_stride(out), need ? ptr(room) : nullptr, need ? room.numel() : 0, ptr<int32_t>(status), w.stream());
+        }
     }
     check(rc);
     return THPVariable_Wrap(out);
@@ -533,8 +543,8 @@ PyObject* i8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyObject* init(PyObject*, PyObject* args)
 {
     PyObject* f;
-    unsigned long long p[9];
-    if (!PyArg_ParseTuple(args, "OKKKKKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8])) return nullptr;
+    unsigned long long p[10];
+    if (!PyArg_ParseTuple(args, "OKKKKKKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8], &p[9])) return nullptr;
     Py_INCREF(f);
     Py_XDECREF(g_check);
     g_check = f;
@@ -547,6 +557,7 @@ PyObject* init(PyObject*, PyObject* args)
     p_i8_norm = reinterpret_cast<decltype(p_i8_norm)>(p[6]);
     p_i8_swiglu = reinterpret_cast<decltype(p_i8_swiglu)>(p[7]);
     p_i8_matmul = reinterpret_cast<decltype(p_i8_matmul)>(p[8]);
+    p_i8_workspace = reinterpret_cast<decltype(p_i8_workspace)>(p[9]);
     Py_RETURN_NONE;
 }
 

@@ -12,7 +12,8 @@
 //   TMA      int8 tiles of 128 channels and of the tokens by 128 inputs into a ring
 //   warps 0..3, 4..7  expand every other stage to fp16: the tokens' codes in shared
 //               memory (operand B), then the channels' in tensor memory (operand A;
-//               a thread owns a TMEM lane, a channel)
+//               a thread owns a TMEM lane, a channel).  For pairs a kernel before
+//               this one has expanded the tokens' codes, once for all channel tiles
 //   one thread issues the products (of a pair, the first CTA's for both)
 //   warps 8..15 add chunks, then scale and store
 // Weights pass through shared memory once as bytes and never as fp16.  With
@@ -37,8 +38,8 @@ constexpr int THREADS = 640;
 constexpr int BM = 128;                          // channels of a CTA
 constexpr int STAGE_K = 128;                     // inputs of a stage
 constexpr int CHUNK = 8;                         // stages that FP32 sums exactly: 1,024 inputs
-constexpr int NA = 2, NB = 3;                    // expanded stages: A's and B's
-constexpr int MAX_NS = 8;
+constexpr int NA = 2;                            // A's expanded stages
+constexpr int MAX_NS = 8;                        // of either ring
 constexpr int A_RAW = BM * STAGE_K;
 constexpr uint32_t TMEM_COLS = 512, A_COLS = STAGE_K / 2, T_A = TMEM_COLS - NA * A_COLS;
 constexpr int TMA_WARP = 16, MMA_WARP = 17;
@@ -51,21 +52,24 @@ constexpr int I8_SMS = 152;
 
 struct I8GemmArgs {
     I8MatmulArgs a;
-    int bn, splits, ns;              // tokens of a tile, CTAs that share its inputs, ring stages
+    int bn, splits, ns, nb;          // tokens of a tile, CTAs that share its inputs, ring stages: codes, B in fp16
     int m_tiles, n_tiles;
 };
 
 struct Bars {
     uint64_t raw_full[MAX_NS], raw_empty[MAX_NS];
-    uint64_t full[NA], a_empty[NA], b_empty[NB];
+    uint64_t full[NA], a_empty[NA], b_empty[MAX_NS];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
 };
 
-// the rings (B's rows: rows_b tokens), the barriers and what alignment may take
-constexpr size_t smem_bytes(int rows_b, int ns) {
-    return (size_t)ns * (A_RAW + rows_b * STAGE_K) + NB * (size_t)rows_b * STAGE_K * 2 + sizeof(Bars) + 1024;
+// bytes of a stage of the ring of codes and of B's in fp16; all of it with the
+// barriers and what alignment may take
+constexpr int raw_bytes(int cg, int bn) { return A_RAW + (cg == 1 ? bn * STAGE_K : 0); }
+constexpr int half_bytes_of(int cg, int bn) { return bn / cg * STAGE_K * 2; }
+constexpr size_t smem_bytes(int cg, int bn, int ns, int nb) {
+    return (size_t)ns * raw_bytes(cg, bn) + (size_t)nb * half_bytes_of(cg, bn) + sizeof(Bars) + 1024;
 }
 
 template <int R> Q3_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
@@ -203,6 +207,28 @@ Q3_DEV void store_sums(const I8MatmulArgs& a, const int (&acc)[ACC], const float
     }
 }
 
+// x's codes as fp16 rows, Kp apart: operand B of the pairs
+__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t* x, int64_t stride, int K, __half* out, int64_t Kp)
+{
+    grid_dep_wait();
+    grid_dep_launch();                           // the product's set-up overlaps this
+    const int k = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
+    if (k >= K) return;
+    const int64_t t = blockIdx.x;
+    uint32_t r[8];
+    if (k + 16 <= K) {
+        expand16(ldg_nc_v4(x + t * stride + k), r);
+    } else {
+        uint32_t w[4] = {};
+        for (int e = 0; e < 16; ++e)
+            if (k + e < K) w[e >> 2] |= (uint32_t)(uint8_t)x[t * stride + k + e] << (8 * (e & 3));
+        expand16(make_uint4(w[0], w[1], w[2], w[3]), r);
+    }
+    uint4* o = reinterpret_cast<uint4*>(out + t * Kp + k);
+    o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
 template <int CG>
 __global__ void __launch_bounds__(THREADS, 1)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const I8GemmArgs p)
@@ -212,9 +238,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const I8MatmulArgs& a = p.a;
     const int rows_b = p.bn / CG;                // tokens of this CTA's B operand
-    const int stage_bytes = A_RAW + rows_b * STAGE_K, half_bytes = rows_b * STAGE_K * 2;
-    uint8_t* half = smem + p.ns * stage_bytes;   // operand B in fp16: NB stages, each 64 inputs and 64 more
-    Bars& b = *reinterpret_cast<Bars*>(half + NB * half_bytes);
+    const int stage_bytes = raw_bytes(CG, p.bn), half_bytes = half_bytes_of(CG, p.bn);
+    uint8_t* half = smem + p.ns * stage_bytes;   // operand B in fp16: nb stages, each 64 inputs and 64 more
+    Bars& b = *reinterpret_cast<Bars*>(half + p.nb * half_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int size = CG == 2 ? 2 : p.splits;     // CTAs of a cluster
     const int rank = size > 1 ? (int)(blockIdx.x % size) : 0;
@@ -229,7 +255,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             mbar_init(&b.full[c], 4 * CG);
             mbar_init(&b.a_empty[c], 1);
         }
-        for (int c = 0; c < NB; ++c) mbar_init(&b.b_empty[c], 1);
+        for (int c = 0; c < p.nb; ++c) mbar_init(&b.b_empty[c], 1);
         for (int c = 0; c < 2; ++c) {
             mbar_init(&b.acc_full[c], 1);
             mbar_init(&b.acc_empty[c], 8 * CG);
@@ -264,7 +290,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
         const uint32_t swz = (uint32_t)(row & 7);
         const uint32_t src0 = smem_u32(smem) + row * 128, dst0 = smem_u32(half) + row * 128;
         const uint32_t ta = tmem + ((uint32_t)(warp & 3) * 32 << 16) + T_A + mine * A_COLS;
-        Ring raw(p.ns), a_at(NA), b_at(NB);
+        Ring raw(p.ns), a_at(NA), b_at(p.nb);
         bool ok = true;
         for (int u = first; u < units && ok; u += stride) {
             for (int s = 0; s < stages && ok; ++s, raw.next(), a_at.next(), b_at.next()) {
@@ -276,10 +302,11 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = lds16(from + (((h * 4 + j) ^ swz) << 4));
                 };
-                if (live) load(w[0], src + A_RAW, 0);
-                if (!(ok = b_at.first || wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status))) break;
+                if (CG == 2) load(w[0], src, 0);
+                else if (live) load(w[0], src + A_RAW, 0);
+                if (CG == 1 && !(ok = b_at.first || wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status))) break;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < (CG == 1 ? 2 : 0); ++h) {
                     if (h == 0) { if (live) load(w[1], src + A_RAW, 1); }
                     else load(w[0], src, 0);
                     if (live) {
@@ -306,7 +333,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                         tmem_st_32x32b_x16(ta + h * 32 + i * 16, r);
                     }
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (CG == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -319,7 +346,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
         // the products' last arrivals on this CTA's barriers
         for (int i = 0; i < NA && ok; ++i, a_at.next())
             if (!a_at.first) wait_warp(&b.a_empty[a_at.slot], a_at.phase ^ 1, b, status);
-        for (int i = 0; i < NB && ok; ++i, b_at.next())
+        for (int i = 0; i < (CG == 1 ? p.nb : 0) && ok; ++i, b_at.next())
             if (!b_at.first) wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status);
     } else if (warp < TMA_WARP) {
         // ---------------- epilogue: quadrant warp % 4 of the lanes, half the columns
@@ -380,28 +407,38 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     } else {
         reg_dec<R_ISSUE>();
         if (warp == TMA_WARP) {
-            Ring raw(p.ns);
+            Ring raw(p.ns), b_at(p.nb);
             bool ok = true;
             for (int u = first; u < units && ok; u += stride) {
                 const int nt = u % p.n_tiles, mt = u / p.n_tiles;
                 const int m0 = mt * (BM * CG) + (CG == 2 ? rank * BM : 0), n0 = nt * p.bn + (CG == 2 ? rank * rows_b : 0);
-                for (int s = s0; s < s1; ++s, raw.next()) {
+                for (int s = s0; s < s1; ++s, raw.next(), b_at.next()) {
                     if (!(ok = raw.first || wait_warp(&b.raw_empty[raw.slot], raw.phase ^ 1, b, status))) break;
+                    if (CG == 2 && !(ok = b_at.first || wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status))) break;
                     uint8_t* dst = smem + raw.slot * stage_bytes;
+                    uint64_t* bar = &b.raw_full[raw.slot];
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&b.raw_full[raw.slot], stage_bytes);
-                        tma_load_2d(dst, &tw, &b.raw_full[raw.slot], s * STAGE_K, m0);
-                        tma_load_2d(dst + A_RAW, &tx, &b.raw_full[raw.slot], s * STAGE_K, n0);
+                        mbar_arrive_expect_tx(bar, CG == 1 ? stage_bytes : stage_bytes + half_bytes);
+                        tma_load_2d(dst, &tw, bar, s * STAGE_K, m0);
+                        if (CG == 1) {
+                            tma_load_2d(dst + A_RAW, &tx, bar, s * STAGE_K, n0);
+                        } else {
+                            uint8_t* to = half + b_at.slot * half_bytes;
+                            tma_load_2d(to, &tx, bar, s * STAGE_K, n0);
+                            tma_load_2d(to + half_bytes / 2, &tx, bar, s * STAGE_K + 64, n0);
+                        }
                     }
                     __syncwarp();
                 }
             }
+            for (int i = 0; i < (CG == 2 ? p.nb : 0) && ok; ++i, b_at.next())      // the products' last arrivals
+                if (!b_at.first) wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status);
             if (!ok)                             // copies still under way end before the CTA does
                 for (int i = 0; i < p.ns; ++i, raw.next())
                     if (!raw.first) wait_last(&b.raw_full[raw.slot], raw.phase ^ 1);
         } else if (warp == MMA_WARP && (CG == 1 || rank == 0)) {
             const uint32_t idesc = idesc_f16_f32(BM * CG, 0) | ((uint32_t)(p.bn >> 3) << 17);
-            Ring a_at(NA), b_at(NB), acc_at(2);
+            Ring a_at(NA), b_at(p.nb), acc_at(2);
             bool ok = true;
             for (int u = first; u < units && ok; u += stride) {
                 for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
@@ -499,7 +536,7 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * size));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes(p.bn / CG, p.ns);
+    cfg.dynamicSmemBytes = smem_bytes(CG, p.bn, p.ns, p.nb);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -527,9 +564,28 @@ I8Plan i8_plan(int T, int M, int K)
     q.splits = 1;
     if (q.cg == 1)
         while (q.splits < 8 && tiles * (q.splits + 1) <= I8_SMS && kt / (q.splits + 1) >= 4) ++q.splits;
-    q.ns = 2;
-    while (q.ns < MAX_NS && smem_bytes(q.bn / q.cg, q.ns + 1) <= MAX_SMEM) ++q.ns;
+    q.ns = q.nb = 3;
+    for (bool more = true; more;) {
+        more = false;
+        if (q.cg == 2 && q.nb < MAX_NS && smem_bytes(q.cg, q.bn, q.ns, q.nb + 1) <= MAX_SMEM) ++q.nb, more = true;
+        if (q.ns < MAX_NS && smem_bytes(q.cg, q.bn, q.ns + 1, q.nb) <= MAX_SMEM) ++q.ns, more = true;
+    }
     return q;
+}
+
+cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, __half* out, int64_t Kp)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.K + 4095) / 4096));
+    cfg.blockDim = dim3(256);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = L.pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (L.counter) ++*L.counter;
+    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, a.x, a.x_stride, a.K, out, Kp);
 }
 
 cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q)
@@ -538,7 +594,7 @@ cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtenso
     if (q.bn % (16 * q.cg) || q.bn < 16 * q.cg || q.bn > (q.cg == 2 ? 192 : 128)) return cudaErrorInvalidValue;
     I8GemmArgs p{};
     p.a = a;
-    p.bn = q.bn; p.splits = q.splits; p.ns = q.ns;
+    p.bn = q.bn; p.splits = q.splits; p.ns = q.ns; p.nb = q.nb;
     p.m_tiles = (a.M + 128 * q.cg - 1) / (128 * q.cg);
     p.n_tiles = (a.T + q.bn - 1) / q.bn;
     return q.cg == 2 ? launch_cg<2>(L, tw, tx, p) : launch_cg<1>(L, tw, tx, p);

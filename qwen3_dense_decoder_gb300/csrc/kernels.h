@@ -466,11 +466,14 @@ struct I8MatmulArgs {
 // For at most this many rows of x; beyond, on tcgen05.
 constexpr int I8_MATVEC_ROWS = 8;
 cudaError_t launch_i8_matvec(const Launch& L, const I8MatmulArgs& a);
-// CTAs of a tile (2: a pair with 256 channels), its tokens, CTAs that
-// share its inputs, ring stages.  tw: w in boxes of 128 rows by 128 inputs; tx: x in
-// boxes of bn / cg rows.
-struct I8Plan { int cg, bn, splits, ns; };
+// CTAs of a tile (2: a pair with 256 channels), its tokens, CTAs that share its
+// inputs, stages of the rings.  tw: w in boxes of 128 rows by 128 inputs; tx: x in
+// boxes of bn rows by 128 inputs, or for pairs x's fp16 copy (rows of i8_copy_row(K))
+// in boxes of bn / 2 rows by 64.
+struct I8Plan { int cg, bn, splits, ns, nb; };
 I8Plan i8_plan(int T, int M, int K);
+inline int64_t i8_copy_row(int K) { return (K + 15ll) / 16 * 16; }
+cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, __half* out, int64_t Kp);
 cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q);
 
 // Q8_0: canonical blocks -> (int8 plane, fp16 scale plane); planes -> fp16

@@ -139,6 +139,20 @@ bool tmap_i8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The fp16 copy of such rows, stride elements apart, in boxes of 64 by box_rows rows.
+bool tmap_i8_copy(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, int64_t stride, uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t elem[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 struct Q8Planes {
@@ -2602,9 +2616,24 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
     return Q3_OK;
 }
 
+namespace {
+int64_t i8_workspace(int T, int M, int K)
+{
+    if (T <= I8_MATVEC_ROWS || i8_plan(T, M, K).cg == 1) return 0;
+    return (int64_t)T * i8_copy_row(K) * 2;
+}
+}  // namespace
+
+int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes)
+{
+    if (!bytes || T < 0 || M < 1 || K < 1 || K > I8_MAX_K) return fail(Q3_ERR_INVALID_ARG, "i8_matmul_workspace: bad argument");
+    *bytes = i8_workspace(T, M, K);
+    return Q3_OK;
+}
+
 int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,
                     const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
-                    int32_t* status_dev, void* stream)
+                    void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* stream)
 {
     if (T < 0 || M < 1 || K < 1 || K > I8_MAX_K)
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: T rows, at least one channel, 1 to %d inputs", I8_MAX_K);
@@ -2614,6 +2643,9 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: f32 scales of x and w");
     if (!i8_type_ok(out_type) || !i8_rows_ok(out_dev, out_stride, M, out_type))
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: out of an unknown type, not aligned to it or with a short stride");
+    const int64_t need = i8_workspace(T, M, K);
+    if (need && (!workspace_dev || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: workspace of %lld bytes, 256-byte aligned", (long long)need);
     if (T == 0) return Q3_OK;
     I8MatmulArgs a{};
     a.x = x_dev; a.x_stride = x_stride; a.xs = x_scales_dev;
@@ -2621,15 +2653,18 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
     a.T = T; a.M = M; a.K = K;
     a.out = out_dev; a.out_type = out_type; a.out_stride = out_stride;
     a.status = status_dev;
-    cudaError_t e;
+    const Launch L = op_launch(stream);
+    cudaError_t e = cudaSuccess;
     if (T <= I8_MATVEC_ROWS) {
-        e = launch_i8_matvec(op_launch(stream), a);
+        e = launch_i8_matvec(L, a);
     } else {
         const I8Plan q = i8_plan(T, M, K);
         CUtensorMap tw, tx;
-        if (!tmap_i8(&tw, w_dev, M, K, w_stride, 128) || !tmap_i8(&tx, x_dev, T, K, x_stride, q.bn / q.cg))
-            return fail(Q3_ERR_CUDA, "op_i8_matmul: tensor map encoding failed");
-        e = launch_i8_gemm(op_launch(stream), tw, tx, a, q);
+        const bool ok = tmap_i8(&tw, w_dev, M, K, w_stride, 128) &&
+                        (q.cg == 2 ? tmap_i8_copy(&tx, workspace_dev, T, K, i8_copy_row(K), q.bn / 2) : tmap_i8(&tx, x_dev, T, K, x_stride, q.bn));
+        if (!ok) return fail(Q3_ERR_CUDA, "op_i8_matmul: tensor map encoding failed");
+        if (q.cg == 2) e = launch_i8_expand(L, a, static_cast<f16*>(workspace_dev), i8_copy_row(K));
+        if (e == cudaSuccess) e = launch_i8_gemm(L, tw, tx, a, q);
     }
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_matmul: %s", cudaGetErrorString(e));
     return Q3_OK;

@@ -35,7 +35,8 @@ def _swiglu(L, **kw):
 
 
 def _matmul(L, **kw):
-    a = dict(x=P, x_stride=112, xs=P, w=P, w_stride=112, ws=P, T=4, M=7, K=100, out=P, out_type=1, out_stride=7, status=None)
+    a = dict(x=P, x_stride=112, xs=P, w=P, w_stride=112, ws=P, T=4, M=7, K=100, out=P, out_type=1, out_stride=7, ws_dev=None, ws_bytes=0,
+             status=None)
     a.update(kw)
     return L.q3_op_i8_matmul(*a.values(), None)
 
@@ -71,6 +72,19 @@ def test_swiglu_refuses(L, bad):
 def test_matmul_refuses(L, bad):
     assert _matmul(L, **bad) == -1
     assert L.q3_last_error()
+
+
+def test_matmul_workspace(L):
+    import qwen3_dense_decoder_gb300 as q3
+    assert [q3.i8_matmul_workspace(t, 7, 100) for t in (0, 1, 8, 9, 64)] == [0] * 5
+    need = q3.i8_matmul_workspace(4096, 4096, 1000)
+    assert need >= 4096 * 1000 * 2
+    big = dict(T=4096, M=4096, K=1000, x_stride=1008, w_stride=1008, out_stride=4096)
+    for bad in (dict(), dict(ws_dev=P, ws_bytes=need - 1), dict(ws_dev=P + 16, ws_bytes=need)):
+        assert _matmul(L, **big, **bad) == -1
+    for bad in ((-1, 7, 100), (9, 0, 100), (9, 7, 0), (9, 7, 131072)):
+        with pytest.raises(q3.Q3Error):
+            q3.i8_matmul_workspace(*bad)
 
 
 def test_nothing_to_do_is_no_error(L):

@@ -38,10 +38,10 @@ constexpr int THREADS = 640;
 constexpr int BM = 128;                          // channels of a CTA
 constexpr int STAGE_K = 128;                     // inputs of a stage
 constexpr int CHUNK = 8;                         // stages that FP32 sums exactly: 1,024 inputs
-constexpr int NA = 2;                            // A's expanded stages
+constexpr int MAX_NA = 4;                        // A's expanded stages
 constexpr int MAX_NS = 8;                        // of either ring
 constexpr int A_RAW = BM * STAGE_K;
-constexpr uint32_t TMEM_COLS = 512, A_COLS = STAGE_K / 2, T_A = TMEM_COLS - NA * A_COLS;
+constexpr uint32_t TMEM_COLS = 512, A_COLS = STAGE_K / 2;
 constexpr int TMA_WARP = 16, MMA_WARP = 17;
 // registers of a thread by warpgroup; 640 threads launch with 96
 constexpr int R_EXPAND = 72, R_EPILOGUE = 144, R_ISSUE = 48, R_LAUNCH = 96;
@@ -58,7 +58,7 @@ struct I8GemmArgs {
 
 struct Bars {
     uint64_t raw_full[MAX_NS], raw_empty[MAX_NS];
-    uint64_t full[NA], a_empty[NA], b_empty[MAX_NS];
+    uint64_t full[MAX_NA], a_empty[MAX_NA], b_empty[MAX_NS];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
@@ -71,6 +71,10 @@ constexpr int half_bytes_of(int cg, int bn) { return bn / cg * STAGE_K * 2; }
 constexpr size_t smem_bytes(int cg, int bn, int ns, int nb) {
     return (size_t)ns * raw_bytes(cg, bn) + (size_t)nb * half_bytes_of(cg, bn) + sizeof(Bars) + 1024;
 }
+
+// A's stages in what two accumulators leave of tensor memory: with two (bn 192) the
+// expanding waits for the products, with three (160) it does not
+constexpr __host__ __device__ int a_stages(int bn) { return bn > 160 ? 2 : bn > 128 ? 3 : MAX_NA; }
 
 template <int R> Q3_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
 template <int R> Q3_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
@@ -244,6 +248,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int size = CG == 2 ? 2 : p.splits;     // CTAs of a cluster
     const int rank = size > 1 ? (int)(blockIdx.x % size) : 0;
+    const int na = a_stages(p.bn);
+    const uint32_t t_a = TMEM_COLS - na * A_COLS;    // tensor memory: two accumulators, then A's stages
     int* status = a.status;
 
     if (threadIdx.x == 0) {
@@ -251,7 +257,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             mbar_init(&b.raw_full[s], 1);
             mbar_init(&b.raw_empty[s], 4);
         }
-        for (int c = 0; c < NA; ++c) {
+        for (int c = 0; c < MAX_NA; ++c) {
             mbar_init(&b.full[c], 4 * CG);
             mbar_init(&b.a_empty[c], 1);
         }
@@ -289,12 +295,13 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
         const bool live = row < rows_b;
         const uint32_t swz = (uint32_t)(row & 7);
         const uint32_t src0 = smem_u32(smem) + row * 128, dst0 = smem_u32(half) + row * 128;
-        const uint32_t ta = tmem + ((uint32_t)(warp & 3) * 32 << 16) + T_A + mine * A_COLS;
-        Ring raw(p.ns), a_at(NA), b_at(p.nb);
+        const uint32_t ta0 = tmem + ((uint32_t)(warp & 3) * 32 << 16) + t_a;
+        Ring raw(p.ns), a_at(na), b_at(p.nb);
+        int turn = 0;
         bool ok = true;
         for (int u = first; u < units && ok; u += stride) {
-            for (int s = 0; s < stages && ok; ++s, raw.next(), a_at.next(), b_at.next()) {
-                if ((int)a_at.slot != mine) continue;
+            for (int s = 0; s < stages && ok; ++s, turn ^= 1, raw.next(), a_at.next(), b_at.next()) {
+                if (turn != mine) continue;
                 if (!(ok = wait_warp(&b.raw_full[raw.slot], raw.phase, b, status))) break;
                 const uint32_t src = src0 + raw.slot * stage_bytes;
                 uint4 w[2][4];
@@ -320,8 +327,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                         }
                     }
                 }
-                if (!(ok = a_at.first || wait_warp(&b.a_empty[mine], a_at.phase ^ 1, b, status))) break;
+                if (!(ok = a_at.first || wait_warp(&b.a_empty[a_at.slot], a_at.phase ^ 1, b, status))) break;
                 tc_fence_after();
+                const uint32_t ta = ta0 + a_at.slot * A_COLS;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 0) load(w[1], src, 1);
@@ -338,13 +346,13 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive_first<CG>(&b.full[mine]);
+                    arrive_first<CG>(&b.full[a_at.slot]);
                     mbar_arrive(&b.raw_empty[raw.slot]);
                 }
             }
         }
         // the products' last arrivals on this CTA's barriers
-        for (int i = 0; i < NA && ok; ++i, a_at.next())
+        for (int i = 0; i < na && ok; ++i, a_at.next())
             if (!a_at.first) wait_warp(&b.a_empty[a_at.slot], a_at.phase ^ 1, b, status);
         for (int i = 0; i < (CG == 1 ? p.nb : 0) && ok; ++i, b_at.next())
             if (!b_at.first) wait_warp(&b.b_empty[b_at.slot], b_at.phase ^ 1, b, status);
@@ -438,7 +446,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                     if (!raw.first) wait_last(&b.raw_full[raw.slot], raw.phase ^ 1);
         } else if (warp == MMA_WARP && (CG == 1 || rank == 0)) {
             const uint32_t idesc = idesc_f16_f32(BM * CG, 0) | ((uint32_t)(p.bn >> 3) << 17);
-            Ring a_at(NA), b_at(p.nb), acc_at(2);
+            Ring a_at(na), b_at(p.nb), acc_at(2);
             bool ok = true;
             for (int u = first; u < units && ok; u += stride) {
                 for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
@@ -450,7 +458,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                         if (!(ok = wait_warp(&b.full[a_at.slot], a_at.phase, b, status))) break;
                         tc_fence_after();
                         const uint64_t desc = smem_desc_sw128(smem_u32(half) + b_at.slot * half_bytes);
-                        const uint32_t ta = tmem + T_A + a_at.slot * A_COLS, next64 = half_bytes >> 5;
+                        const uint32_t ta = tmem + t_a + a_at.slot * A_COLS, next64 = half_bytes >> 5;
                         if (elect_one()) {
 #pragma unroll
                             for (int j = 0; j < STAGE_K / 16; ++j)

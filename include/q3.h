@@ -591,8 +591,9 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
 int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,
                     const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
                     void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* stream);
-/* Bytes of workspace for these sizes: 0 for few tokens, else an fp16 copy of x, T
- * rows of round_up(K, 16).  Host only.  Errors: Q3_ERR_INVALID_ARG. */
+/* Bytes of workspace for these sizes: 0 for few tokens, else an fp16 copy of x (T
+ * rows of round_up(K, 16)) and 4 bytes for each 1,024 of its codes.  Host only.
+ * Errors: Q3_ERR_INVALID_ARG. */
 int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes);
 
 /* Split-K matmul that allocates nothing (the Kipp pages have no counterpart;

@@ -5,7 +5,10 @@
 // and FP32 sums of products of two are exact up to 2^24: 1,024 products of 128 x
 // 128.  So kind::f16 sums chunks of 1,024 inputs in tensor memory, and the
 // epilogue's warps add the chunks as 32-bit integers in registers: the exact
-// whole number, at the 16-bit rate, from 8-bit operands in memory.
+// whole number, at the 16-bit rate, from 8-bit operands in memory.  Reading a chunk
+// slows the products beside it (2,048 rows by 19,456 x 2,560: 147 us with three
+// chunks a tile, 115 with one), so pairs sum longer ones where the tokens allow it:
+// no partial sum exceeds 128 sum |x|, known for every token and 1,024 inputs.
 //
 // A CTA (or with CG == 2 a pair of CTAs, each with its own 128 channels and half
 // of the tokens) takes a tile of 128 CG channels by bn tokens:
@@ -42,7 +45,8 @@ constexpr int MAX_NA = 4;                        // A's expanded stages
 constexpr int MAX_NS = 8;                        // of either ring
 constexpr int A_RAW = BM * STAGE_K;
 constexpr uint32_t TMEM_COLS = 512, A_COLS = STAGE_K / 2;
-constexpr int TMA_WARP = 16, MMA_WARP = 17;
+constexpr int CHUNK_K = CHUNK * STAGE_K;
+constexpr int TMA_WARP = 16, MMA_WARP = 17, PLAN_WARP = 18;
 // registers of a thread by warpgroup; 640 threads launch with 96
 constexpr int R_EXPAND = 72, R_EPILOGUE = 144, R_ISSUE = 48, R_LAUNCH = 96;
 static_assert(2 * R_EXPAND + 2 * R_EPILOGUE + R_ISSUE <= 5 * R_LAUNCH, "registers");
@@ -54,12 +58,15 @@ struct I8GemmArgs {
     I8MatmulArgs a;
     int bn, splits, ns, nb;          // tokens of a tile, CTAs that share its inputs, ring stages: codes, B in fp16
     int m_tiles, n_tiles;
+    const int* l1;                   // pairs: [1,024 inputs][T] sum |x|
 };
 
 struct Bars {
     uint64_t raw_full[MAX_NS], raw_empty[MAX_NS];
     uint64_t full[MAX_NA], a_empty[MAX_NA], b_empty[MAX_NS];
     uint64_t acc_full[2], acc_empty[2], drain;
+    uint64_t plan_full[2], plan_empty[2];
+    uint32_t plan[2][4];                     // bit i: a chunk ends with input 1,024 (i + 1); two units
     uint32_t tmem;
     int abort;
 };
@@ -196,8 +203,7 @@ template <> Q3_DEV void put<float>(float* p, float v, bool&) { *p = v; }
 template <> Q3_DEV void put<__half>(__half* p, float v, bool& bad) { *p = to_f16(v, bad); }
 template <> Q3_DEV void put<__nv_bfloat16>(__nv_bfloat16* p, float v, bool&) { *p = __float2bfloat16_rn(v); }
 
-// A thread's sums of one channel, columns first .. of `n` tokens from t0: scaled
-// and stored
+// A thread's sums of one channel and `n` tokens from t0 (FP32), scaled and stored
 template <typename O, int ACC>
 Q3_DEV void store_sums(const I8MatmulArgs& a, const int (&acc)[ACC], const float (&xs)[ACC / 32], int64_t m, int t0, int n, float ws, bool& bad)
 {
@@ -206,31 +212,45 @@ Q3_DEV void store_sums(const I8MatmulArgs& a, const int (&acc)[ACC], const float
 #pragma unroll
     for (int j = 0; j < ACC; ++j) {
         const float x = __shfl_sync(0xffffffffu, xs[j / 32], j % 32);
-        if (j < n && live) put<O>(p, (float)acc[j] * x * ws, bad);
+        if (j < n && live) put<O>(p, __int_as_float(acc[j]) * x * ws, bad);
         p += a.out_stride;
     }
 }
 
-// x's codes as fp16 rows, Kp apart: operand B of the pairs
-__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t* x, int64_t stride, int K, __half* out, int64_t Kp)
+// x's codes as fp16 rows, Kp apart, operand B of the pairs, and sum |x| of every
+// 1,024 of a row (l1: [1,024 inputs][T])
+__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t* x, int64_t stride, int T, int K, __half* out, int64_t Kp, int* l1)
 {
+    __shared__ int part[8];
     grid_dep_wait();
     grid_dep_launch();                           // the product's set-up overlaps this
-    const int k = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
-    if (k >= K) return;
     const int64_t t = blockIdx.x;
-    uint32_t r[8];
+    const int k = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
+    const int8_t* row = x + t * stride;
+    uint4 w = make_uint4(0, 0, 0, 0);
     if (k + 16 <= K) {
-        expand16(ldg_nc_v4(x + t * stride + k), r);
+        w = ldg_nc_v4(row + k);
     } else {
-        uint32_t w[4] = {};
+        uint32_t* v = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (k + e < K) w[e >> 2] |= (uint32_t)(uint8_t)x[t * stride + k + e] << (8 * (e & 3));
-        expand16(make_uint4(w[0], w[1], w[2], w[3]), r);
+            if (k + e < K) v[e >> 2] |= (uint32_t)(uint8_t)row[k + e] << (8 * (e & 3));
     }
-    uint4* o = reinterpret_cast<uint4*>(out + t * Kp + k);
-    o[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    uint32_t r[8];
+    expand16(w, r);
+    if (k < K) {
+        uint4* o = reinterpret_cast<uint4*>(out + t * Kp + k);
+        o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+    __half2 sum = __float2half2_rn(0.f);         // at most 1,024 a half: exact
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = __hadd2(sum, __habs2(*reinterpret_cast<const __half2*>(&r[i])));
+    const int warp_sum = __reduce_add_sync(0xffffffffu, (int)(__low2float(sum) + __high2float(sum)));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = warp_sum;
+    __syncthreads();
+    const int c = (int)blockIdx.y * 4 + (int)threadIdx.x;
+    if (threadIdx.x < 4 && c * CHUNK_K < K) l1[(int64_t)c * T + t] = part[2 * threadIdx.x] + part[2 * threadIdx.x + 1];
 }
 
 template <int CG>
@@ -266,6 +286,10 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             mbar_init(&b.acc_full[c], 1);
             mbar_init(&b.acc_empty[c], 8 * CG);
         }
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(&b.plan_full[c], 1);
+            mbar_init(&b.plan_empty[c], rank == 0 ? 9 : 8);      // the epilogue's warps and the products'
+        }
         mbar_init(&b.drain, 1);
         b.abort = 0;
         fence_barrier_init();
@@ -286,7 +310,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     const int split = CG == 1 && p.splits > 1 ? rank : 0, splits = CG == 1 ? p.splits : 1;
     const int s0 = (int)((int64_t)kt * split / splits), s1 = (int)((int64_t)kt * (split + 1) / splits);
     const int units = p.m_tiles * p.n_tiles, first = blockIdx.x / size, stride = gridDim.x / size;
-    const int stages = s1 - s0, chunks = (stages + CHUNK - 1) / CHUNK;
+    const int stages = s1 - s0, most = (stages + CHUNK - 1) / CHUNK;
+    const bool planned = CG == 2 && most > 1;    // else chunks of CHUNK stages
 
     if (warp < 8) {
         // ---------------- expanding: a warpgroup takes every other stage
@@ -361,27 +386,49 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
         reg_inc<R_EPILOGUE>();
         const int part = (warp - 8) >> 2, cols = p.bn / 2;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) * 32 << 16);
-        Ring acc_at(2);
+        Ring acc_at(2), plan_at(2);
         bool ok = true, bad = false;
         for (int u = first; u < units && ok; u += stride) {
             const int nt = u % p.n_tiles, mt = u / p.n_tiles;
             const int64_t m = (int64_t)mt * (BM * CG) + (CG == 2 ? rank * BM : 0) + (warp & 3) * 32 + lane;
             const int t0 = nt * p.bn + part * cols;
+            int chunks = most;
+            if (planned) {
+                if (!(ok = wait_warp(&b.plan_full[plan_at.slot], plan_at.phase, b, status))) break;
+                chunks = 1;
+                for (int i = 0; i < most; i += 32) chunks += i + 1 < most ? __popc(b.plan[plan_at.slot][i >> 5]) : 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.plan_empty[plan_at.slot]);
+                plan_at.next();
+            }
+            // the first chunk as the FP32 that it is, whole numbers from the second on
             int acc[ACC];
+            if (chunks == 0)
 #pragma unroll
-            for (int j = 0; j < ACC; ++j) acc[j] = 0;
+                for (int j = 0; j < ACC; ++j) acc[j] = 0;
             for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
                 const uint32_t d = acc_at.slot;
                 if (!(ok = wait_warp(&b.acc_full[d], acc_at.phase, b, status))) break;
                 tc_fence_after();
+                const uint32_t from = lanes + d * p.bn + part * cols;
+                if (c == 0) {
 #pragma unroll
-                for (int g = 0; g < ACC / 16; ++g) {
-                    if (g * 16 < cols) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(lanes + d * p.bn + part * cols + g * 16, r);
-                        tmem_ld_wait();
+                    for (int g = 0; g < ACC / 16; ++g)
+                        if (g * 16 < cols) tmem_ld_32x32b_x16(from + g * 16, *reinterpret_cast<uint32_t(*)[16]>(acc + g * 16));
+                    tmem_ld_wait();
+                } else {
+                    if (c == 1)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[g * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+                        for (int j = 0; j < ACC; ++j) acc[j] = __float2int_rn(__int_as_float(acc[j]));
+#pragma unroll
+                    for (int g = 0; g < ACC / 16; ++g) {
+                        if (g * 16 < cols) {
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(from + g * 16, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[g * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+                        }
                     }
                 }
                 tc_fence_before();
@@ -394,9 +441,12 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                 int* red = reinterpret_cast<int*>(smem);
 #pragma unroll
                 for (int j = 0; j < ACC; ++j)
-                    if (j < cols) red[(part * cols + j) * BM + (warp & 3) * 32 + lane] = acc[j];
+                    if (j < cols) red[(part * cols + j) * BM + (warp & 3) * 32 + lane] = chunks == 1 ? __float2int_rn(__int_as_float(acc[j])) : acc[j];
                 break;
             }
+            if (chunks > 1)
+#pragma unroll
+                for (int j = 0; j < ACC; ++j) acc[j] = __float_as_int((float)acc[j]);
             float xs[ACC / 32];
 #pragma unroll
             for (int i = 0; i < ACC / 32; ++i) {
@@ -406,9 +456,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
             const float ws = m < a.M ? a.ws[m] : 0.f;
             const int n = min(cols, a.T - t0);
             switch (a.out_type) {
-            case Q3_TYPE_F32: store_sums<float, ACC>(a, acc, xs, m, t0, n, ws, bad); break;
-            case Q3_TYPE_F16: store_sums<__half, ACC>(a, acc, xs, m, t0, n, ws, bad); break;
-            default: store_sums<__nv_bfloat16, ACC>(a, acc, xs, m, t0, n, ws, bad);
+            case Q3_TYPE_F32: store_sums<float>(a, acc, xs, m, t0, n, ws, bad); break;
+            case Q3_TYPE_F16: store_sums<__half>(a, acc, xs, m, t0, n, ws, bad); break;
+            default: store_sums<__nv_bfloat16>(a, acc, xs, m, t0, n, ws, bad);
             }
         }
         if (bad && status) set_status(status, Q3_STATUS_F16_RANGE);
@@ -446,14 +496,19 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                     if (!raw.first) wait_last(&b.raw_full[raw.slot], raw.phase ^ 1);
         } else if (warp == MMA_WARP && (CG == 1 || rank == 0)) {
             const uint32_t idesc = idesc_f16_f32(BM * CG, 0) | ((uint32_t)(p.bn >> 3) << 17);
-            Ring a_at(na), b_at(p.nb), acc_at(2);
+            Ring a_at(na), b_at(p.nb), acc_at(2), plan_at(2);
             bool ok = true;
             for (int u = first; u < units && ok; u += stride) {
-                for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
+                if (planned && !(ok = wait_warp(&b.plan_full[plan_at.slot], plan_at.phase, b, status))) break;
+                for (int at = 0; at < stages && ok; acc_at.next()) {
+                    int end = at / CHUNK;                // the chunk's last 1,024 inputs
+                    if (planned)
+                        while (end + 1 < most && !(b.plan[plan_at.slot][end >> 5] >> (end & 31) & 1)) ++end;
+                    const int n = min((end + 1) * CHUNK, stages) - at;
+                    at += n;
                     if (!(ok = acc_at.first || wait_warp(&b.acc_empty[acc_at.slot], acc_at.phase ^ 1, b, status))) break;
                     tc_fence_after();
                     const uint32_t d = tmem + acc_at.slot * p.bn;
-                    const int n = min(CHUNK, stages - c * CHUNK);
                     for (int k = 0; k < n; ++k, a_at.next(), b_at.next()) {
                         if (!(ok = wait_warp(&b.full[a_at.slot], a_at.phase, b, status))) break;
                         tc_fence_after();
@@ -470,11 +525,50 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                         __syncwarp();
                     }
                 }
+                if (planned && ok) {
+                    if (lane == 0) mbar_arrive(&b.plan_empty[plan_at.slot]);
+                    plan_at.next();
+                }
             }
             if (!ok) {                           // as do products
                 if (elect_one()) commit<CG>(&b.drain);
                 __syncwarp();
                 wait_last(&b.drain, 0);
+            }
+        }
+        else if (warp == PLAN_WARP && planned) {
+            // where each unit's chunks end: as late as 128 sum |x| of every token stays
+            // within 2^24
+            Ring plan_at(2);
+            bool ok = true;
+            for (int u = first; u < units && ok; u += stride, plan_at.next()) {
+                if (!(ok = plan_at.first || wait_warp(&b.plan_empty[plan_at.slot], plan_at.phase ^ 1, b, status))) break;
+                const int t0 = u % p.n_tiles * p.bn, t1 = min(t0 + p.bn, a.T);
+                uint32_t* plan = b.plan[plan_at.slot];
+                uint32_t bits = 0;
+                int sum = 0;
+                for (int c0 = 0; c0 < most; c0 += 4) {
+                    int m[4] = {0, 0, 0, 0};
+                    for (int t = t0 + lane; t < t1; t += 32)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m[i] = max(m[i], p.l1[(int64_t)min(c0 + i, most - 1) * a.T + t]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = c0 + i, v = (int)__reduce_max_sync(0xffffffffu, (uint32_t)m[i]);
+                        if (c >= most) break;
+                        if (c > 0 && sum + v > (1 << 24) / 128) {
+                            bits |= 1u << ((c - 1) & 31);      // the chunk before ends with c - 1
+                            sum = 0;
+                        }
+                        sum += v;
+                        if (c > 0 && ((c & 31) == 0 || c + 1 == most)) {
+                            if (lane == 0) plan[(c - 1) >> 5] = bits;
+                            bits = 0;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.plan_full[plan_at.slot]);
             }
         }
         __syncwarp();
@@ -581,7 +675,7 @@ I8Plan i8_plan(int T, int M, int K)
     return q;
 }
 
-cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, __half* out, int64_t Kp)
+cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, void* workspace)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.K + 4095) / 4096));
@@ -593,15 +687,17 @@ cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, __half* out
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (L.counter) ++*L.counter;
-    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, a.x, a.x_stride, a.K, out, Kp);
+    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, a.x, a.x_stride, a.T, a.K, static_cast<__half*>(workspace), i8_copy_row(a.K),
+                              i8_sums(workspace, a.T, a.K));
 }
 
-cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q)
+cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q, void* workspace)
 {
     // what tcgen05.mma takes: 16 k tokens for 128 channels, 32 k for a pair's 256
     if (q.bn % (16 * q.cg) || q.bn < 16 * q.cg || q.bn > (q.cg == 2 ? 192 : 128)) return cudaErrorInvalidValue;
     I8GemmArgs p{};
     p.a = a;
+    if (q.cg == 2) p.l1 = i8_sums(workspace, a.T, a.K);
     p.bn = q.bn; p.splits = q.splits; p.ns = q.ns; p.nb = q.nb;
     p.m_tiles = (a.M + 128 * q.cg - 1) / (128 * q.cg);
     p.n_tiles = (a.T + q.bn - 1) / q.bn;

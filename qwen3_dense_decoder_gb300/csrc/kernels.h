@@ -472,9 +472,12 @@ cudaError_t launch_i8_matvec(const Launch& L, const I8MatmulArgs& a);
 // in boxes of bn / 2 rows by 64.
 struct I8Plan { int cg, bn, splits, ns, nb; };
 I8Plan i8_plan(int T, int M, int K);
+// A pair's workspace: x's copy, then sum |x| of every 1,024 inputs of a token, [..][T]
 inline int64_t i8_copy_row(int K) { return (K + 15ll) / 16 * 16; }
-cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, __half* out, int64_t Kp);
-cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q);
+inline int64_t i8_copy_bytes(int T, int K) { return (T * i8_copy_row(K) * 2 + 255) / 256 * 256; }
+inline int* i8_sums(void* workspace, int T, int K) { return reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + i8_copy_bytes(T, K)); }
+cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, void* workspace);
+cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtensorMap& tx, const I8MatmulArgs& a, const I8Plan& q, void* workspace);
 
 // Q8_0: canonical blocks -> (int8 plane, fp16 scale plane); planes -> fp16
 // tensor-core operand; bf16 -> canonical blocks.

@@ -2620,7 +2620,7 @@ namespace {
 int64_t i8_workspace(int T, int M, int K)
 {
     if (T <= I8_MATVEC_ROWS || i8_plan(T, M, K).cg == 1) return 0;
-    return (int64_t)T * i8_copy_row(K) * 2;
+    return i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int);
 }
 }  // namespace
 
@@ -2663,8 +2663,8 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
         const bool ok = tmap_i8(&tw, w_dev, M, K, w_stride, 128) &&
                         (q.cg == 2 ? tmap_i8_copy(&tx, workspace_dev, T, K, i8_copy_row(K), q.bn / 2) : tmap_i8(&tx, x_dev, T, K, x_stride, q.bn));
         if (!ok) return fail(Q3_ERR_CUDA, "op_i8_matmul: tensor map encoding failed");
-        if (q.cg == 2) e = launch_i8_expand(L, a, static_cast<f16*>(workspace_dev), i8_copy_row(K));
-        if (e == cudaSuccess) e = launch_i8_gemm(L, tw, tx, a, q);
+        if (q.cg == 2) e = launch_i8_expand(L, a, workspace_dev);
+        if (e == cudaSuccess) e = launch_i8_gemm(L, tw, tx, a, q, workspace_dev);
     }
     if (e != cudaSuccess) return fail(Q3_ERR_CUDA, "op_i8_matmul: %s", cudaGetErrorString(e));
     return Q3_OK;

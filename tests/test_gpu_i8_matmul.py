@@ -161,3 +161,29 @@ def test_calls_in_a_row_that_feed_one_another(q3):
         for _ in range(5):
             got = q3.op_i8_matmul(*q3.op_i8_quantize(got), wc, ws) * 0.03125
         assert torch.equal(got, want), t
+
+
+@pytest.mark.parametrize("k", [1024, 2048, 2049, 32768, 33 * 1024 + 5, 131071])
+@pytest.mark.parametrize("size", [1, 8, 33, 127])
+def test_sums_of_tokens_of_different_sizes(q3, k, size):
+    """Long sums where the codes are small, short ones where some tokens' are not; the weights all of one sign and largest."""
+    x = rows(400, k, size, lo=-size, hi=size)
+    x[7] = 127
+    x[199, : k // 2] = -128
+    x[200:210, k // 3:] = 127
+    w = rows(260, k, 5, lo=100, hi=127)
+    w[::2] = -128
+    check(q3, x, w, torch.float32)
+
+
+def test_sums_at_the_largest_that_fp32_holds(q3):
+    """sum |x| of 1,024 inputs at 2^17 / n: n chunks in one sum reach 2^24 exactly, one more code would pass it."""
+    for n in (1, 2, 4, 32, 33, 64):
+        k = 70 * 1024
+        x = torch.zeros(300, k, dtype=torch.int8, device="cuda")
+        full = 131072 // n // 128                                # codes of -128 in each 1,024
+        x.view(300, 70, 1024)[:, :, :full] = -128
+        x[::3].view(100, 70, 1024)[:, ::2, 1023] = 1
+        w = torch.full((260, k), -128, dtype=torch.int8, device="cuda")
+        w[1::2] = 127
+        check(q3, x, w, torch.float32)

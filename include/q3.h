@@ -553,7 +553,8 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
  * of a half, a code may be the neighbour.  A row that holds an infinity or a NaN has a NaN for its
  * scale and zero codes (so that every product with it is NaN) and sets
  * Q3_STATUS_F16_RANGE.  codes_dev: rows code_stride bytes apart (a multiple of
- * 16, at least K), 16-byte aligned; bytes past K are neither written nor read.
+ * 16, at least K), 16-byte aligned; bytes between K and the next row are not
+ * written and have no effect.
  * scales_dev: f32 [T].  values_dev: [T][K] of values_type (f32, fp16 or bf16),
  * or NULL, receives scale * code.  Inputs: f32, fp16 or bf16 rows, stride
  * elements apart, of any alignment of the type (rows that begin on 16-byte

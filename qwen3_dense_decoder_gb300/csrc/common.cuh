@@ -187,6 +187,18 @@ Q3_DEV uint2 kvq_dequant4(uint32_t w, __half d) {
     return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
+// ---------------------------------------------------------------- 8-bit integer codes
+// Four codes as two pairs of fp16: a byte with its sign bit flipped, under 0x64,
+// is the fp16 1,024 + 128 + code
+Q3_DEV void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t f = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    const uint32_t l = __byte_perm(f, 0x64646464u, 0x4140), h = __byte_perm(f, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), bias), b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // ---------------------------------------------------------------- PDL
 // Programmatic dependent launch: a kernel may start while its predecessor
 // drains; it must call grid_dep_wait() before touching what the predecessor

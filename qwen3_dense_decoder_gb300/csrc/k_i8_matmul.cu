@@ -157,17 +157,6 @@ template <int CG> Q3_DEV void dealloc(uint32_t t) {
     else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(t), "r"(TMEM_COLS) : "memory");
 }
 
-// Four codes as two pairs of fp16: a byte with its sign bit flipped, under 0x64,
-// is the fp16 1,024 + 128 + code
-Q3_DEV void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t f = w ^ 0x80808080u;
-    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
-    const uint32_t l = __byte_perm(f, 0x64646464u, 0x4140), h = __byte_perm(f, 0x64646464u, 0x4342);
-    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), bias), b = __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
-    lo = *reinterpret_cast<const uint32_t*>(&a);
-    hi = *reinterpret_cast<const uint32_t*>(&b);
-}
-
 Q3_DEV void expand16(const uint4& w, uint32_t* r) {
     expand4(w.x, r[0], r[1]);
     expand4(w.y, r[2], r[3]);
@@ -299,7 +288,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
     if (warp == MMA_WARP) alloc<CG>(&b.tmem);
     tc_fence_before();
     __syncthreads();
-    if (size > 1) cg::this_cluster().sync();     // every CTA's barriers are there
+    if (CG == 2) cg::this_cluster().sync();      // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = b.tmem;
     grid_dep_wait();
@@ -592,11 +581,14 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                 const int col = i >> 5, t = nt * p.bn + col;
                 const int64_t m = (int64_t)mt * BM + (i & 31) * 4;
                 if (t >= a.T || m >= a.M) continue;
-                int4 s = make_int4(0, 0, 0, 0);
-                for (int r = 0; r < splits; ++r) {
-                    const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(reinterpret_cast<int*>(smem), r) + i * 4);
-                    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-                }
+                int4 v[8];                       // all shares' loads together
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < splits) v[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(reinterpret_cast<int*>(smem), r) + i * 4);
+                int4 s = v[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < splits) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
                 const int sums[4] = {s.x, s.y, s.z, s.w};
                 const float xs = a.xs[t];
                 for (int e = 0; e < 4; ++e) {
@@ -659,6 +651,7 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
 I8Plan i8_plan(int T, int M, int K)
 {
     I8Plan q{};
+    if (T <= 16 || (T <= I8_FEW_ROWS && (int64_t)M * K <= 16 << 20)) return q;
     const int kt = (K + STAGE_K - 1) / STAGE_K;
     q.cg = T > 256 ? 2 : 1;
     q.bn = q.cg == 2 ? 192 : std::min(128, (T + 15) / 16 * 16);

@@ -463,10 +463,10 @@ struct I8MatmulArgs {
     int64_t out_stride;
     int* status;               // or null
 };
-// For at most this many rows of x; beyond, on tcgen05.
-constexpr int I8_MATVEC_ROWS = 8;
-cudaError_t launch_i8_matvec(const Launch& L, const I8MatmulArgs& a);
-// CTAs of a tile (2: a pair with 256 channels), its tokens, CTAs that share its
+// For at most I8_FEW_ROWS rows of x
+constexpr int I8_FEW_ROWS = 32;
+cudaError_t launch_i8_few(const Launch& L, const I8MatmulArgs& a);
+// CTAs of a tile (2: a pair with 256 channels; 0: launch_i8_few's), its tokens, CTAs that share its
 // inputs, stages of the rings.  tw: w in boxes of 128 rows by 128 inputs; tx: x in
 // boxes of bn rows by 128 inputs, or for pairs x's fp16 copy (rows of i8_copy_row(K))
 // in boxes of bn / 2 rows by 64.

@@ -2619,7 +2619,7 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
 namespace {
 int64_t i8_workspace(int T, int M, int K)
 {
-    if (T <= I8_MATVEC_ROWS || i8_plan(T, M, K).cg == 1) return 0;
+    if (T == 0 || i8_plan(T, M, K).cg != 2) return 0;
     return i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int);
 }
 }  // namespace
@@ -2655,10 +2655,10 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
     a.status = status_dev;
     const Launch L = op_launch(stream);
     cudaError_t e = cudaSuccess;
-    if (T <= I8_MATVEC_ROWS) {
-        e = launch_i8_matvec(L, a);
+    const I8Plan q = i8_plan(T, M, K);
+    if (q.cg == 0) {
+        e = launch_i8_few(L, a);
     } else {
-        const I8Plan q = i8_plan(T, M, K);
         CUtensorMap tw, tx;
         const bool ok = tmap_i8(&tw, w_dev, M, K, w_stride, 128) &&
                         (q.cg == 2 ? tmap_i8_copy(&tx, workspace_dev, T, K, i8_copy_row(K), q.bn / 2) : tmap_i8(&tx, x_dev, T, K, x_stride, q.bn));

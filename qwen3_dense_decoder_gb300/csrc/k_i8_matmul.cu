@@ -646,19 +646,43 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
 
 }  // namespace
 
-// How a product is shared out: a pair of CTAs for many tokens; else 128 channels a
-// CTA, and with fewer tiles than SMs a cluster for each.
+// How a product is shared out: the quickest by what was measured (us, device time;
+// 2,048 x 1,024 to 19,456 x 2,560 and 5,120 x 17,408, 32 to 2,048 tokens, within 15 %):
+//  - a wave of tiles takes its stages, 0.56 us and 0.6 ns a token each for one CTA,
+//    0.28 us and 0.4 ns for a pair, or 0.33 and 2 ns for the tokens beyond 128;
+//  - setting up takes 6.5 us and 10 ns a token, joining a cluster's sums 1.5 us and
+//    12 ns a token more; a pair 9 us, and the expansion before it 1 us and its bytes.
+// Few tokens take launch_i8_few's: 2.5 us and up, but its expansion of x, a warp's own,
+// grows with the tokens (32 by 19,456 x 2,560: 23.8 us, by 2,560 x 4,096 8.6; in pairs
+// or a cluster 16 and 10).
 I8Plan i8_plan(int T, int M, int K)
 {
     I8Plan q{};
     if (T <= 16 || (T <= I8_FEW_ROWS && (int64_t)M * K <= 16 << 20)) return q;
-    const int kt = (K + STAGE_K - 1) / STAGE_K;
-    q.cg = T > 256 ? 2 : 1;
-    q.bn = q.cg == 2 ? 192 : std::min(128, (T + 15) / 16 * 16);
-    const int tiles = (M + 127) / 128 * ((T + q.bn - 1) / q.bn);
-    q.splits = 1;
-    if (q.cg == 1)
-        while (q.splits < 8 && tiles * (q.splits + 1) <= I8_SMS && kt / (q.splits + 1) >= 4) ++q.splits;
+    const int64_t kt = (K + STAGE_K - 1) / STAGE_K, m_tiles = (M + 127ll) / 128, m_pairs = (M + 255ll) / 256;
+    double best = 1e30;
+    auto take = [&](double us, int cg, int bn, int splits) {
+        if (us >= best) return;
+        best = us;
+        q.cg = cg; q.bn = bn; q.splits = splits;
+    };
+    for (int bn = 32; bn <= 192; bn += 32) {
+        const int64_t waves = (m_pairs * ((T + bn - 1) / bn) + I8_SMS / 2 - 1) / (I8_SMS / 2);
+        const double stage = bn <= 128 ? 0.28 + 0.0004 * bn : 0.33 + 0.002 * (bn - 128);
+        take(10 + 7.5e-7 * T * K + waves * kt * stage, 2, bn, 1);
+    }
+    // token tiles of equal width
+    for (int n = (T + 127) / 128; n <= (T + 127) / 128 + 2; ++n) {
+        const int bn = ((T + n - 1) / n + 15) / 16 * 16;
+        const int64_t tiles = m_tiles * ((T + bn - 1) / bn);
+        for (int splits = 1; splits <= 8; ++splits) {
+            // clusters in one wave: as many as eight GPCs of 18 SMs hold (20 of seven CTAs
+            // took 29 us where 20 of six took 16)
+            if (splits > 1 && (tiles > 8 * (18 / splits) || kt < 2 * splits)) break;
+            const int64_t waves = (tiles + I8_SMS - 1) / I8_SMS;
+            take(6.5 + 0.01 * bn + waves * ((kt + splits - 1) / splits) * (0.56 + 0.0006 * bn) + (splits > 1 ? 1.5 + 0.012 * bn : 0), 1, bn, splits);
+        }
+    }
     q.ns = q.nb = 3;
     for (bool more = true; more;) {
         more = false;

@@ -16,6 +16,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -161,6 +162,10 @@ public:
     }
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
         return at::empty(shape, at::TensorOptions().dtype(type).device(device_));
+    }
+    // rows of k elements, `stride` apart
+    at::Tensor rows(int64_t t, int64_t k, int64_t stride, at::ScalarType type) const {
+        return at::empty_strided({t, k}, {stride, 1}, at::TensorOptions().dtype(type).device(device_));
     }
     // a caller's tensor, checked, or none yet
     static at::Tensor given(const Args& c, const at::Tensor* t, at::IntArrayRef shape, at::ScalarType type) {
@@ -397,8 +402,7 @@ struct I8Out {
     }
     void make(const Where& w) {                  // no tensor of the caller's is touched
         if (!codes.defined()) {
-            codes = w.make({T, (K + 15ll) / 16 * 16}, at::kChar);
-            if (K % 16) codes = codes.narrow(1, 0, K);
+            codes = w.rows(T, K, (K + 15ll) / 16 * 16, at::kChar);
         }
         if (!scales.defined()) scales = w.make({T}, at::kFloat);
     }

@@ -671,14 +671,15 @@ I8Plan i8_plan(int T, int M, int K)
         const double stage = bn <= 128 ? 0.28 + 0.0004 * bn : 0.33 + 0.002 * (bn - 128);
         take(10 + 7.5e-7 * T * K + waves * kt * stage, 2, bn, 1);
     }
-    // token tiles of equal width
+    // token tiles of equal width; clusters of one CTA an SM in one wave, a little under
+    // cudaOccupancyMaxActiveClusters' numbers (76, 46, 36, 28, 23, 15 and 15: with 20 of
+    // seven CTAs 64 by 2,560 x 9,728 took 29 us, with 20 of six 16)
+    constexpr int MOST_CLUSTERS[9] = {0, I8_SMS, 74, 44, 34, 26, 22, 14, 14};
     for (int n = (T + 127) / 128; n <= (T + 127) / 128 + 2; ++n) {
         const int bn = ((T + n - 1) / n + 15) / 16 * 16;
         const int64_t tiles = m_tiles * ((T + bn - 1) / bn);
         for (int splits = 1; splits <= 8; ++splits) {
-            // clusters in one wave: as many as eight GPCs of 18 SMs hold (20 of seven CTAs
-            // took 29 us where 20 of six took 16)
-            if (splits > 1 && (tiles > 8 * (18 / splits) || kt < 2 * splits)) break;
+            if (splits > 1 && (tiles > MOST_CLUSTERS[splits] || kt < 2 * splits)) break;
             const int64_t waves = (tiles + I8_SMS - 1) / I8_SMS;
             take(6.5 + 0.01 * bn + waves * ((kt + splits - 1) / splits) * (0.56 + 0.0006 * bn) + (splits > 1 ? 1.5 + 0.012 * bn : 0), 1, bn, splits);
         }

@@ -548,13 +548,13 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
  *
  * A row y of K values (1 <= K <= 131,071) is held as K int8 codes and one f32
  * scale: scale = max |y| / 127, code = round-half-even(y / scale), in [-127,
- * 127]; a row of zeros has scale 0 and zero codes.  y is an FP32 value and the
- * division a product with an FP32 reciprocal: where y / scale lies within 2^-13
- * of a half, a code may be the neighbour.  A row that holds an infinity or a NaN has a NaN for its
- * scale and zero codes (so that every product with it is NaN) and sets
- * Q3_STATUS_F16_RANGE.  codes_dev: rows code_stride bytes apart (a multiple of
- * 16, at least K), 16-byte aligned; bytes between K and the next row are not
- * written and have no effect.
+ * 127]; a row of zeros has scale 0 and zero codes.  Codes of fp16 and bf16 values
+ * are these; of others, whose y is an FP32 value, a code may be the neighbour
+ * where y / scale lies within 2^-13 of a half.  A row that holds an infinity or a
+ * NaN has a NaN for its scale and zero codes (so that every product with it is
+ * NaN) and sets Q3_STATUS_F16_RANGE.  codes_dev: rows code_stride bytes apart (a
+ * multiple of 16, at least K), 16-byte aligned; bytes between K and the next row
+ * are not written and have no effect.
  * scales_dev: f32 [T].  values_dev: [T][K] of values_type (f32, fp16 or bf16),
  * or NULL, receives scale * code.  Inputs: f32, fp16 or bf16 rows, stride
  * elements apart, of any alignment of the type (rows that begin on 16-byte

@@ -128,6 +128,21 @@ def test_halves_go_to_even_and_columns_beside_stay(q3, k):
     assert bool((base[:, :16] == 99).all()) and bool((base[:, 16 + k:] == 99).all())
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t,k,gap", [(700, 256, 0), (50, 5120, 0), (9, 333, 1), (3, 17408, 0), (2, 40001, 1)])
+def test_codes_of_16_bit_values_are_the_definitions(q3, t, k, gap, dtype):
+    """127 x and code * max are whole multiples of one power of two below 2^53: the remainder is exact, and a half goes to even."""
+    x = wide(t, k, TYPES[dtype], gap, t + k)
+    codes, _ = q3.op_i8_quantize(x)
+    v, c = f64(x), f64(codes)
+    top = np.abs(v).max(1, keepdims=True)
+    d = 2 * np.abs(127 * v - c * top)
+    assert np.all(d <= top)
+    half = d == top
+    assert half.any() or k < 1000
+    assert np.all(c[half] % 2 == 0)
+
+
 @pytest.mark.parametrize("k", [24, 1000, 5120, 16389])
 def test_rows_of_zeros_and_of_what_is_no_number(q3, k):
     x = torch.randn(8, k, device="cuda")

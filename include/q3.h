@@ -546,7 +546,8 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
  * nothing.  The Kipp pages have no counterpart ("Kipp Model Support", section
  * "Quantization (Q8_0)", packs weights alone, with a scale for each 32).
  *
- * A row y of K values (1 <= K <= 131,071) is held as K int8 codes and one f32
+ * A row y of K values (1 <= K <= 131,071; at most 2^30 rows or channels) is held
+ * as K int8 codes and one f32
  * scale: scale = max |y| / 127, code = round-half-even(y / scale), in [-127,
  * 127]; a row of zeros has scale 0 and zero codes.  Codes of fp16 and bf16 values
  * are these; of others, whose y is an FP32 value, a code may be the neighbour

@@ -2538,6 +2538,7 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
 namespace {
 
 constexpr int I8_MAX_K = 131071;             // 128 * 128 * K stays below 2^31
+constexpr int I8_MAX_ROWS = 1 << 30;         // tokens and channels: numbers of tiles stay well below 2^31
 
 bool i8_type_ok(int type) { return type >= Q3_TYPE_F32 && type <= Q3_TYPE_BF16; }
 bool i8_rows_ok(const void* p, int64_t stride, int64_t width, int type)
@@ -2551,7 +2552,8 @@ bool aligned4(const void* p) { return !(reinterpret_cast<uintptr_t>(p) & 3); }
 int i8_outputs(const char* name, I8RowArgs& a, int T, int K, int8_t* codes, int64_t code_stride, float* scales, void* values,
                int values_type, int32_t* status)
 {
-    if (T < 0 || K < 1 || K > I8_MAX_K) return fail(Q3_ERR_INVALID_ARG, "%s: T rows of 1 to %d values", name, I8_MAX_K);
+    if (T < 0 || T > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
+        return fail(Q3_ERR_INVALID_ARG, "%s: at most 2^30 rows of 1 to %d values", name, I8_MAX_K);
     if (!i8_codes_ok(codes, code_stride, K) || !scales || !aligned4(scales))
         return fail(Q3_ERR_INVALID_ARG, "%s: codes begin on 16-byte boundaries, rows a multiple of 16 bytes apart", name);
     if (values && (!i8_type_ok(values_type) || !i8_rows_ok(values, K, K, values_type)))
@@ -2626,7 +2628,8 @@ int64_t i8_workspace(int T, int M, int K)
 
 int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes)
 {
-    if (!bytes || T < 0 || M < 1 || K < 1 || K > I8_MAX_K) return fail(Q3_ERR_INVALID_ARG, "i8_matmul_workspace: bad argument");
+    if (!bytes || T < 0 || T > I8_MAX_ROWS || M < 1 || M > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
+        return fail(Q3_ERR_INVALID_ARG, "i8_matmul_workspace: bad argument");
     *bytes = i8_workspace(T, M, K);
     return Q3_OK;
 }
@@ -2635,8 +2638,8 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
                     const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
                     void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* stream)
 {
-    if (T < 0 || M < 1 || K < 1 || K > I8_MAX_K)
-        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: T rows, at least one channel, 1 to %d inputs", I8_MAX_K);
+    if (T < 0 || T > I8_MAX_ROWS || M < 1 || M > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
+        return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: at most 2^30 tokens, 1 to 2^30 channels, 1 to %d inputs", I8_MAX_K);
     if (!i8_codes_ok(x_dev, x_stride, K) || !i8_codes_ok(w_dev, w_stride, K))
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: codes begin on 16-byte boundaries, rows a multiple of 16 bytes apart");
     if (!x_scales_dev || !w_scales_dev || !aligned4(x_scales_dev) || !aligned4(w_scales_dev))

@@ -187,3 +187,47 @@ def test_sums_at_the_largest_that_fp32_holds(q3):
         w = torch.full((260, k), -128, dtype=torch.int8, device="cuda")
         w[1::2] = 127
         check(q3, x, w, torch.float32)
+
+
+def test_outputs_and_codes_beyond_2_31_elements(q3):
+    t, m, k = 70000, 32768, 64
+    x, w = rows(t, k, 1), rows(m, k, 2)
+    xs, ws = scales(t, 3, 2.0 ** -7), scales(m, 4, 2.0 ** -9)
+    out = q3.op_i8_matmul(x, xs, w, ws, dtype=torch.bfloat16)
+    at = torch.tensor([0, 1, 191, 192, 65535, 65536, 69900, t - 1], device="cuda")
+    assert torch.equal(out[at], reference(x[at], xs[at], w, ws, torch.bfloat16))
+    del out
+    # the channels' rows lie beyond 2^31 bytes
+    wide = torch.empty(m * 8, 16384, dtype=torch.int8, device="cuda")[:, :k]
+    wide[-300:] = w[:300]
+    wide[:300] = w[300:600]
+    for n in (9, 40, 300):
+        x, xs = rows(n, k, 6), scales(n, 7, 2.0 ** -7)
+        big = scales(m * 8, 8, 2.0 ** -9)
+        got = q3.op_i8_matmul(x, xs, wide, big, dtype=torch.float32)
+        assert torch.equal(got[:, -300:], reference(x, xs, w[:300], big[-300:], torch.float32))
+        assert torch.equal(got[:, :300], reference(x, xs, w[300:600], big[:300], torch.float32))
+
+
+@pytest.mark.parametrize("t", [1, 40, 300])
+def test_the_first_call_of_a_process_may_be_captured(t):
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import torch, qwen3_dense_decoder_gb300 as q3
+x = torch.randn({t}, 512, device="cuda").half(); w = torch.randint(-127, 128, (700, 512), device="cuda", dtype=torch.int8)
+ws = torch.rand(700, device="cuda"); g = torch.ones(512, device="cuda").bfloat16()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    c, s, _ = q3.op_i8_norm(x, g)
+    y = q3.op_i8_matmul(c, s, w, ws, dtype=torch.float32)
+    z = q3.op_i8_swiglu(y)
+graph.replay()
+torch.cuda.synchronize()
+want = (c.double() @ w.double().T).float() * s.unsqueeze(1) * ws
+assert torch.equal(y, want) and z[0].abs().amax() == 127
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -222,3 +222,15 @@ def test_another_stream_and_a_captured_call(q3):
     want = q3.op_i8_norm(x, gain, delta=d)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(torch.equal(a, b) for a, b in zip(act, q3.op_i8_swiglu(want[2])))
+
+
+def test_rows_beyond_2_31_elements(q3):
+    x = torch.empty(300000, 8192, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 262143, 262144, 262145, 299999]
+    x.zero_()
+    x[at] = torch.randn(len(at), 8192, device="cuda").bfloat16()
+    codes, scales = q3.op_i8_quantize(x)
+    check(f64(x[at]), codes[at], scales[at], None)
+    assert int((scales != 0).sum()) == len(at)
+    codes, scales = q3.op_i8_swiglu(x, codes=codes[:, :4096], scales=scales)
+    check(swiglu64(f64(x[at])), codes[at], scales[at], None)

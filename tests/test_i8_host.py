@@ -41,7 +41,7 @@ def _matmul(L, **kw):
     return L.q3_op_i8_matmul(*a.values(), None)
 
 
-ROWS = [dict(x=None), dict(x=P + 2), dict(type=1, x=P + 1), dict(type=3), dict(type=-1), dict(stride=99), dict(T=-1), dict(K=0),
+ROWS = [dict(x=None), dict(x=P + 2), dict(type=1, x=P + 1), dict(type=3), dict(type=-1), dict(stride=99), dict(T=-1), dict(T=(1 << 30) + 1), dict(K=0),
         dict(K=131072, stride=1 << 20, code_stride=1 << 20), dict(codes=None), dict(codes=ODD), dict(code_stride=96), dict(code_stride=108),
         dict(scales=None), dict(scales=P + 2), dict(values=P + 2), dict(values=P + 1, values_type=1), dict(values=P, values_type=3)]
 
@@ -66,7 +66,7 @@ def test_swiglu_refuses(L, bad):
 
 @pytest.mark.parametrize("bad", [
     dict(x=None), dict(x=ODD), dict(x_stride=96), dict(x_stride=104), dict(xs=None), dict(xs=P + 2), dict(w=None), dict(w=ODD),
-    dict(w_stride=96), dict(w_stride=104), dict(ws=None), dict(ws=P + 1), dict(T=-1), dict(M=0), dict(K=0),
+    dict(w_stride=96), dict(w_stride=104), dict(ws=None), dict(ws=P + 1), dict(T=-1), dict(T=(1 << 30) + 1), dict(M=0), dict(M=(1 << 30) + 1, out_stride=1 << 31), dict(K=0),
     dict(K=131072, x_stride=1 << 20, w_stride=1 << 20), dict(out=None), dict(out=P + 1), dict(out=P + 2, out_type=0), dict(out_type=3),
     dict(out_stride=6)], ids=str)
 def test_matmul_refuses(L, bad):

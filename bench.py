@@ -71,7 +71,7 @@ def parse():
                     help="measure the other named shapes instead (one JSON line each; 0.6b, 8b-q8_0 "
                          "and 14b if none given; 14b-kvq8 is the 14B workload over the Q8_0 K/V cache)")
     ap.add_argument("--ncu-case", choices=("decode-4layer", "gemm-gateup", "attn-prefill", "attn-decode-b32",
-                                           "attn-decode-kvq8-b32", "gemv-a4", "prefill-2layer", "kv4-scoring"),
+                                           "attn-decode-kvq8-b32", "gemv-a4", "prefill-2layer", "kv4-scoring", "i8-rows"),
                     default=None,
                     help="run only a small case sized for an ncu capture (a few GB on the device) and exit")
     return ap.parse_args()
@@ -182,6 +182,27 @@ def ncu_case(name: str):
             q3.op_kv4_prefill_attention(q, ints([0, 512]), ints([10240]), tables, kv)
             q3.op_kv4_decode_attention(q[:8], ends, ints(list(range(8))), tables, kv)
             q3.op_token_logprobs(logits, zero, 5)
+        torch.cuda.synchronize()
+    elif name == "i8-rows":
+        # the operators of 8-bit integer rows, three rounds: 8,192 bf16 rows of
+        # 5,120 quantised, the norm of 2,048 rows of 5,120 with a residual's
+        # addition, SwiGLU of 2,048 rows of 9,728, and the products of 2,048
+        # rows with 19,456 x 2,560 (pairs), of 64 with 2,560 x 9,728 (clusters)
+        # and of 7 with 5,120 x 17,408
+        g = torch.Generator(device="cuda")
+        g.manual_seed(10)
+        rows = lambda t, k: torch.randn(t, k, device="cuda", generator=g)  # noqa: E731
+        wide = rows(8192, 5120).bfloat16()
+        x, delta, gain = rows(2048, 5120).bfloat16(), rows(2048, 5120).bfloat16(), torch.ones(5120, dtype=torch.bfloat16, device="cuda")
+        gate_up = rows(2048, 2 * 9728).half()
+        products = [(*q3.op_i8_quantize(rows(t, k)), *q3.op_i8_quantize(rows(m, k)))
+                    for t, m, k in ((2048, 19456, 2560), (64, 2560, 9728), (7, 5120, 17408))]
+        for _ in range(3):
+            q3.op_i8_quantize(wide)
+            q3.op_i8_norm(x, gain, delta=delta)
+            q3.op_i8_swiglu(gate_up)
+            for p in products:
+                q3.op_i8_matmul(*p)
         torch.cuda.synchronize()
     elif name == "gemv-a4":
         # the gate/up projection of a Qwen3-4B AFFINE4_GS32 decode step as one

@@ -207,39 +207,46 @@ Q3_DEV void store_sums(const I8MatmulArgs& a, const int (&acc)[ACC], const float
 }
 
 // x's codes as fp16 rows, Kp apart, operand B of the pairs, and sum |x| of every
-// 1,024 of a row (l1: [1,024 inputs][T])
+// 1,024 of a row (l1: [1,024 inputs][T]), a warp's each
 __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t* x, int64_t stride, int T, int K, __half* out, int64_t Kp, int* l1)
 {
-    __shared__ int part[8];
     grid_dep_wait();
     grid_dep_launch();                           // the product's set-up overlaps this
-    const int64_t t = blockIdx.x;
-    const int k = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
+    const int lane = threadIdx.x & 31, chunks = (K + CHUNK_K - 1) / CHUNK_K;
+    const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = task / chunks;
+    if (t >= T) return;
+    const int c = (int)(task % chunks);
     const int8_t* row = x + t * stride;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (k + 16 <= K) {
-        w = ldg_nc_v4(row + k);
-    } else {
-        uint32_t* v = reinterpret_cast<uint32_t*>(&w);
+    uint4 w[2];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (k + e < K) v[e >> 2] |= (uint32_t)(uint8_t)row[k + e] << (8 * (e & 3));
-    }
-    uint32_t r[8];
-    expand16(w, r);
-    if (k < K) {
-        uint4* o = reinterpret_cast<uint4*>(out + t * Kp + k);
-        o[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        o[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
-    __half2 sum = __float2half2_rn(0.f);         // at most 1,024 a half: exact
+    for (int h = 0; h < 2; ++h) {
+        const int k = c * CHUNK_K + h * 512 + lane * 16;
+        w[h] = make_uint4(0, 0, 0, 0);
+        if (k + 16 <= K) {
+            w[h] = ldg_nc_v4(row + k);
+        } else {
+            uint32_t* v = reinterpret_cast<uint32_t*>(&w[h]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = __hadd2(sum, __habs2(*reinterpret_cast<const __half2*>(&r[i])));
-    const int warp_sum = __reduce_add_sync(0xffffffffu, (int)(__low2float(sum) + __high2float(sum)));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = warp_sum;
-    __syncthreads();
-    const int c = (int)blockIdx.y * 4 + (int)threadIdx.x;
-    if (threadIdx.x < 4 && c * CHUNK_K < K) l1[(int64_t)c * T + t] = part[2 * threadIdx.x] + part[2 * threadIdx.x + 1];
+            for (int e = 0; e < 16; ++e)
+                if (k + e < K) v[e >> 2] |= (uint32_t)(uint8_t)row[k + e] << (8 * (e & 3));
+        }
+    }
+    __half2 sum = __float2half2_rn(0.f);         // at most 16 x 128 a half: exact
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int k = c * CHUNK_K + h * 512 + lane * 16;
+        uint32_t r[8];
+        expand16(w[h], r);
+        if (k < K) {
+            uint4* o = reinterpret_cast<uint4*>(out + t * Kp + k);
+            o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+            o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __hadd2(sum, __habs2(*reinterpret_cast<const __half2*>(&r[i])));
+    }
+    const int whole = __reduce_add_sync(0xffffffffu, (int)(__low2float(sum) + __high2float(sum)));
+    if (lane == 0) l1[(int64_t)c * T + t] = whole;
 }
 
 template <int CG>
@@ -696,7 +703,8 @@ I8Plan i8_plan(int T, int M, int K)
 cudaError_t launch_i8_expand(const Launch& L, const I8MatmulArgs& a, void* workspace)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.K + 4095) / 4096));
+    const int64_t tasks = (int64_t)a.T * ((a.K + CHUNK_K - 1) / CHUNK_K);
+    cfg.gridDim = dim3((unsigned)((tasks + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[1];

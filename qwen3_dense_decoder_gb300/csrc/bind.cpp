@@ -14,9 +14,11 @@
 #include <optional>
 #include <string>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -160,12 +162,18 @@ public:
         for (const at::Tensor* t : tensors)
             if (t) t->record_stream(*other_);
     }
+    // On the call's device straight from its allocator, for the current stream: by way
+    // of the dispatcher a call that makes two outputs takes 4.6 us of host time, not 3.8.
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-        return at::empty(shape, at::TensorOptions().dtype(type).device(device_));
+        if (!guard_) return at::empty(shape, at::TensorOptions().dtype(type).device(device_));
+        return at::Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                    type, std::nullopt));
     }
     // rows of k elements, `stride` apart
     at::Tensor rows(int64_t t, int64_t k, int64_t stride, at::ScalarType type) const {
-        return at::empty_strided({t, k}, {stride, 1}, at::TensorOptions().dtype(type).device(device_));
+        if (!guard_) return at::empty_strided({t, k}, {stride, 1}, at::TensorOptions().dtype(type).device(device_));
+        return at::Tensor(at::detail::empty_strided_generic({t, k}, {stride, 1}, c10::cuda::CUDACachingAllocator::get(),
+                                                            c10::DispatchKeySet(c10::DispatchKey::CUDA), type));
     }
     // a caller's tensor, checked, or none yet
     static at::Tensor given(const Args& c, const at::Tensor* t, at::IntArrayRef shape, at::ScalarType type) {

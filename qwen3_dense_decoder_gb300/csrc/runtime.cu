@@ -2619,10 +2619,9 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
 }
 
 namespace {
-int64_t i8_workspace(int T, int M, int K)
+int64_t i8_workspace(const I8Plan& q, int T, int K)
 {
-    if (T == 0 || i8_plan(T, M, K).cg != 2) return 0;
-    return i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int);
+    return q.cg == 2 ? i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int) : 0;
 }
 }  // namespace
 
@@ -2630,7 +2629,7 @@ int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes)
 {
     if (!bytes || T < 0 || T > I8_MAX_ROWS || M < 1 || M > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
         return fail(Q3_ERR_INVALID_ARG, "i8_matmul_workspace: bad argument");
-    *bytes = i8_workspace(T, M, K);
+    *bytes = T ? i8_workspace(i8_plan(T, M, K), T, K) : 0;
     return Q3_OK;
 }
 
@@ -2646,10 +2645,11 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: f32 scales of x and w");
     if (!i8_type_ok(out_type) || !i8_rows_ok(out_dev, out_stride, M, out_type))
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: out of an unknown type, not aligned to it or with a short stride");
-    const int64_t need = i8_workspace(T, M, K);
+    if (T == 0) return Q3_OK;
+    const I8Plan q = i8_plan(T, M, K);
+    const int64_t need = i8_workspace(q, T, K);
     if (need && (!workspace_dev || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace_dev) & 255)))
         return fail(Q3_ERR_INVALID_ARG, "op_i8_matmul: workspace of %lld bytes, 256-byte aligned", (long long)need);
-    if (T == 0) return Q3_OK;
     I8MatmulArgs a{};
     a.x = x_dev; a.x_stride = x_stride; a.xs = x_scales_dev;
     a.w = w_dev; a.w_stride = w_stride; a.ws = w_scales_dev;
@@ -2658,7 +2658,6 @@ int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales
     a.status = status_dev;
     const Launch L = op_launch(stream);
     cudaError_t e = cudaSuccess;
-    const I8Plan q = i8_plan(T, M, K);
     if (q.cg == 0) {
         e = launch_i8_few(L, a);
     } else {

@@ -45,13 +45,16 @@ Q3_DEV Words load32_end(const int8_t* row, int k, int K)
 {
     Words w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t b[4];
+    for (int i = 0; i < 8; ++i) w.v[i] = k + 4 * i + 4 <= K ? *reinterpret_cast<const uint32_t*>(row + k + 4 * i) : 0u;
+    const int at = K & ~3;                       // the word that K cuts
+    if (at >= k && at < k + 32 && at < K) {
+        uint32_t b = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = (uint32_t)(uint8_t)row[min(k + 4 * i + e, K - 1)];
-        w.v[i] = 0;
+        for (int e = 0; e < 3; ++e)
+            if (at + e < K) b |= (uint32_t)(uint8_t)row[at + e] << (8 * e);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w.v[i] |= k + 4 * i + e < K ? b[e] << (8 * e) : 0;
+        for (int i = 0; i < 8; ++i)
+            if (k + 4 * i == at) w.v[i] = b;
     }
     return w;
 }

@@ -85,8 +85,8 @@ Q3_DEV void store8(X* p, int tid, int n, int i, int K, const float (&v)[8], bool
 // e^-b = 2^t (1 + r ln 2) with t the rounded product b log2(1/e) and r what that
 // leaves: 2^-22 of the value or less, by ex2.approx.  Below -64 e^-64 is taken out
 // and multiplied into z first, so that FP32 holds every step as long as it holds
-// the result.  IEEE expf and division took 46.6 us where this takes 35 (2,048 rows
-// of 9,728 fp16).
+// the result.  IEEE expf and division take 35.6 us where this takes 30.7 (2,048
+// rows of 9,728 fp16).
 Q3_DEV float silu(float z)
 {
     constexpr double LOG2E = 1.44269504088896340736;
@@ -285,7 +285,7 @@ Q3_DEV void emit(const I8RowArgs& a, int64_t r, int tid, int n, int i, const flo
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float q = y[e] * inv;
-        // (SwiGLU's y lie nowhere in particular: 31.4 us without, 33.5 with, 2,048 rows of 9,728)
+        // (SwiGLU's y lie nowhere in particular: 30.7 us without, 32.7 with, 2,048 rows of 9,728)
         const float c = (OP == SWIGLU ? q : fmaf(fmaf(-q, top, 127.0f * y[e]), one, q)) + MAGIC;
         bits[e] = __float_as_uint(c);
         code[e] = c - MAGIC;
@@ -507,7 +507,8 @@ cudaError_t launch_one(const Launch& L, K kernel, const I8RowArgs& a, int grid, 
 int threads_for(int K, int V) { return ((K + 8 * V - 1) / (8 * V) + 31) / 32 * 32; }
 
 // One wave of CTAs, 640 threads an SM: what 96 registers a thread let reside
-// (two waves' worth of 2,048 rows of 5,120 take 22.4 us, one 17.9).
+// (two waves' worth: the norm of 2,048 rows of 5,120 20.8 us, one 19.2; SwiGLU of
+// 2,048 of 9,728 31.8 and 30.6; 34,816 rows of 5,120 quantised 139 and 141).
 template <typename X, int OP, int V, int DELTA>
 cudaError_t launch_v(const Launch& L, const I8RowArgs& a)
 {
@@ -518,9 +519,10 @@ cudaError_t launch_v(const Launch& L, const I8RowArgs& a)
 }
 
 // Eights a thread: fewer threads a row leave more rows' bytes under way between
-// barriers (34,816 bf16 rows of 5,120: 149 us with two, 138 with four), but the
-// norm's and SwiGLU's two operands then fill the registers (2,048 rows of 5,120:
-// 17.9 us with two, 24.8 with four; one row of 2,560: 2.4 and 4.7).
+// barriers (34,816 bf16 rows of 5,120: 151 us with two, 141 with four), but the
+// norm's two operands and gains then fill the registers (2,048 rows of 5,120: 19.2 us
+// with two, 22.7 with four; one row of 2,560: 2.5 and 4.6).  SwiGLU differs less (32
+// rows of 9,728: 3.1 and 3.5; 2,048: 30.7 and 29.9).
 template <typename X, int OP, int DELTA>
 cudaError_t launch_rows(const Launch& L, const I8RowArgs& a)
 {

@@ -661,7 +661,7 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
 //    12 ns a token more; a pair 9 us, and the expansion before it 1 us and its bytes.
 // Few tokens take launch_i8_few's: 2.5 us and up, but its expansion of x, a warp's own,
 // grows with the tokens (32 by 19,456 x 2,560: 23.8 us, by 2,560 x 4,096 8.6; in pairs
-// or a cluster 16 and 10).
+// or a cluster 18 and 10).
 I8Plan i8_plan(int T, int M, int K)
 {
     I8Plan q{};

@@ -186,6 +186,36 @@ def test_values_near_the_ends_of_fp32(q3, k, size):
             assert np.all(np.abs(f64(codes) * f64(scales)[:, None] - y) <= np.abs(y).max(1, keepdims=True) / 127 + 1e-44)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("k", [2047, 2560, 5120, 20000])
+def test_rare_rows_among_others_and_in_place(q3, k, dtype):
+    """Enough rows that a CTA takes several: some near the ends of FP32, of zeros or no numbers; the sum in x's place."""
+    t = 1000
+    g = torch.Generator(device="cuda").manual_seed(k)
+    x = torch.randn(t, k, generator=g, device="cuda")
+    delta = torch.randn(t, k, generator=g, device="cuda")
+    if dtype != "f16":
+        for rows in (x, delta):
+            rows[::3] *= 1e-25
+            rows[1::7] *= 1e20
+    x[5::11] = delta[5::11] = 0
+    x[9::50, k - 1] = float("nan")
+    x, delta = x.to(TYPES[dtype]), delta.to(TYPES[dtype])
+    gain = (1 + 0.3 * torch.randn(k, generator=g, device="cuda")).bfloat16()
+    codes, scales, total = q3.op_i8_norm(x, gain, delta=delta)
+    assert torch.equal(total.nan_to_num(7.0), (x + delta).nan_to_num(7.0))
+    good = ~torch.isnan(total).any(1)
+    assert torch.equal(torch.isnan(scales), ~good)
+    check(norm64(f64(total[good]), f64(gain), 1e-6), codes[good], scales[good], None)
+    c, s = q3.op_i8_quantize(x)
+    check(f64(x[good]), c[good], s[good], None)
+    assert torch.equal(torch.isnan(s), ~good) and not c[~good].any()
+    c, s, same = q3.op_i8_norm(x, gain, delta=delta, sum_out=x)
+    assert same is x or same.data_ptr() == x.data_ptr()
+    assert torch.equal(c, codes) and torch.equal(s.nan_to_num(7.0), scales.nan_to_num(7.0))
+    assert torch.equal(x.nan_to_num(7.0), total.nan_to_num(7.0))
+
+
 def test_swiglu_of_gates_far_out(q3):
     g = torch.tensor([[-1e4, -90.0, -88.0, -1.0, 0.0, 1.0, 88.0, 1e4]], device="cuda").repeat_interleave(5, 1)
     x = torch.cat([g, torch.full_like(g, 0.5)], 1)

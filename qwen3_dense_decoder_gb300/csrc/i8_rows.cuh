@@ -85,14 +85,15 @@ Q3_DEV void store8(X* p, int tid, int n, int i, int K, const float (&v)[8], bool
 // e^-b = 2^t (1 + r ln 2) with t the rounded product b log2(1/e) and r what that
 // leaves: 2^-22 of the value or less, by ex2.approx.  Below -64 e^-64 is taken out
 // and multiplied into z first, so that FP32 holds every step as long as it holds
-// the result.  IEEE expf and division take 35.6 us where this takes 30.7 (2,048
-// rows of 9,728 fp16).
+// the result.  From 200 on e is 0, and b goes no further: its product with HI
+// would leave FP32 (|z| above 2.35e38) and what it leaves be infinite.  IEEE expf
+// and division take 35.6 us where this takes 30.7 (2,048 rows of 9,728 fp16).
 Q3_DEV float silu(float z)
 {
     constexpr double LOG2E = 1.44269504088896340736;
     constexpr float HI = (float)LOG2E, LO = (float)(LOG2E - (double)HI);
     const bool far = z < -64.f;
-    const float b = fabsf(z) - (far ? 64.f : 0.f), t = -HI * b;
+    const float b = fminf(fabsf(z) - (far ? 64.f : 0.f), 200.f), t = -HI * b;
     float e = fast_ex2(t);
     e = fmaf(e, fmaf(-LO, b, fmaf(-HI, b, -t)) * 0.69314718f, e);
     const float top = z < 0.f ? (far ? z * 1.60381089e-28f : z) * e : z;

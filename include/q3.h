@@ -586,17 +586,20 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
  * multiplied by x_scale, then by w_scale, and rounded to out_type (f32, fp16 or
  * bf16).  x_dev: T rows of K codes, w_dev: M rows (1 <= M), as above; any int8 is
  * a code here, -128 among them.  out_dev: rows out_stride elements apart (>= M).
- * workspace_dev: q3_i8_matmul_workspace bytes, 256-byte aligned, needing no
- * preparation (NULL where that is 0); calls that may overlap on the GPU take one
- * each.  Status: Q3_STATUS_F16_RANGE (a result in fp16 is not a finite fp16
+ * workspace_dev: q3_i8_matmul_workspace bytes of these sizes or larger ones,
+ * 256-byte aligned, needing no preparation (NULL where that is 0); calls that may
+ * overlap on the GPU take one each.  Status: Q3_STATUS_F16_RANGE (a result in fp16 is not a finite fp16
  * number), Q3_STATUS_TIMEOUT.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,
                     const float* w_scales_dev, int T, int M, int K, void* out_dev, int out_type, int64_t out_stride,
                     void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* stream);
-/* Bytes of workspace for these sizes: 0 for few tokens, else an fp16 copy of x (T
- * rows of round_up(K, 16)) and 4 bytes for each 1,024 of its codes.  Host only.
- * Errors: Q3_ERR_INVALID_ARG. */
+/* Bytes of workspace that serve these sizes and all smaller ones (T, M or K): 0 for
+ * few tokens or few inputs, else an fp16 copy of x (T rows of round_up(K, 16)) and 4
+ * bytes for each 1,024 of its codes.  Host only.  Errors: Q3_ERR_INVALID_ARG. */
 int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes);
+/* What q3_op_i8_matmul asks for with exactly these sizes: that, or 0 where the way it
+ * takes uses none; it may fall as T grows.  For callers that allocate for each call. */
+int q3_i8_matmul_workspace_used(int T, int M, int K, int64_t* bytes);
 
 /* Split-K matmul that allocates nothing (the Kipp pages have no counterpart;
  * this entry point serves callers that cannot call cudaMalloc where they need

@@ -118,7 +118,7 @@ def lib():
         L.q3_op_i8_norm.argtypes = [vp, i, i64, vp, i, i64, vp, i64, vp, f, i, i, vp, i64, vp, vp, i, vp, vp]
         L.q3_op_i8_swiglu.argtypes = [vp, i, i64, i, i, vp, i64, vp, vp, i, vp, vp]
         L.q3_op_i8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i, i, i, vp, i, i64, vp, i64, vp, vp]
-        L.q3_i8_matmul_workspace.argtypes = [i, i, i, C.POINTER(i64)]
+        L.q3_i8_matmul_workspace.argtypes = L.q3_i8_matmul_workspace_used.argtypes = [i, i, i, C.POINTER(i64)]
         _lib = L
     return _lib
 
@@ -332,7 +332,7 @@ def _op(name: str):
         address = [C.cast(f, C.c_void_p).value for f in (L.q3_op_kv4_append, L.q3_op_kv4_decode_attention,
                                                          L.q3_op_kv4_prefill_attention, L.q3_kv4_prefill_workspace,
                                                          L.q3_op_token_logprobs, L.q3_op_i8_quantize, L.q3_op_i8_norm,
-                                                         L.q3_op_i8_swiglu, L.q3_op_i8_matmul, L.q3_i8_matmul_workspace)]
+                                                         L.q3_op_i8_swiglu, L.q3_op_i8_matmul, L.q3_i8_matmul_workspace_used)]
         _ops.init(_check, *address)
         _native = _ops
     return getattr(_native, name)
@@ -464,12 +464,14 @@ def op_i8_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sca
     """out[t][m] = (sum_k x[t][k] w[m][k]) x_scales[t] w_scales[m] over int8 codes
     x [T, K] and w [M, K], the sum a whole number: [T, M] in dtype (f32, fp16 or
     bf16; fp16 unless out says otherwise).  The rows of out may be strided.
-    workspace: uint8, i8_matmul_workspace bytes (default: allocated here)."""
+    workspace: uint8, i8_matmul_workspace bytes of these sizes or larger ones
+    (default: what the call uses, allocated here)."""
     return _op("i8_matmul")(x, x_scales, w, w_scales, out, dtype, workspace, status, stream)
 
 
 def i8_matmul_workspace(T: int, M: int, K: int) -> int:
-    """Bytes of workspace op_i8_matmul needs for T tokens, M channels and K inputs.  Host only (no GPU)."""
+    """Bytes of workspace that serve op_i8_matmul for T tokens, M channels and K inputs and for
+    all smaller sizes.  Host only (no GPU)."""
     n = C.c_int64()
     _check(lib().q3_i8_matmul_workspace(T, M, K, C.byref(n)))
     return n.value

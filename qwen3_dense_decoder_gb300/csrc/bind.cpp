@@ -38,7 +38,7 @@ decltype(&q3_op_i8_quantize) p_i8_quantize;
 decltype(&q3_op_i8_norm) p_i8_norm;
 decltype(&q3_op_i8_swiglu) p_i8_swiglu;
 decltype(&q3_op_i8_matmul) p_i8_matmul;
-decltype(&q3_i8_matmul_workspace) p_i8_workspace;
+decltype(&q3_i8_matmul_workspace_used) p_i8_workspace;
 PyObject* g_check;
 
 struct Refusal { std::string what; };        // becomes a ValueError

@@ -653,6 +653,23 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
 
 }  // namespace
 
+namespace {
+bool few_rows(int T, int M, int K) { return T <= 16 || (T <= I8_FEW_ROWS && (int64_t)M * K <= 16 << 20); }
+// Whether pairs can be the quicker by i8_plan's times.  They are not where one wave of
+// single CTAs takes at most six stages: 7.8 us and 0.64 a stage against 10 and 0.29.
+// Once true it stays so for larger sizes, as a workspace's bound has to.
+bool may_pair(int T, int M, int K)
+{
+    const int64_t kt = (K + STAGE_K - 1) / STAGE_K, tiles = (M + 127ll) / 128 * ((T + 127) / 128);
+    return !few_rows(T, M, K) && (kt > 6 || tiles > I8_SMS);
+}
+int64_t pair_workspace(int T, int K) { return i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int); }
+}  // namespace
+
+// What a pair keeps outside the SM: x's copy and sum |x|
+int64_t i8_workspace(const I8Plan& q, int T, int K) { return q.cg == 2 ? pair_workspace(T, K) : 0; }
+int64_t i8_workspace_bound(int T, int M, int K) { return may_pair(T, M, K) ? pair_workspace(T, K) : 0; }
+
 // How a product is shared out: the quickest by what was measured (us, device time;
 // 2,048 x 1,024 to 19,456 x 2,560 and 5,120 x 17,408, 32 to 2,048 tokens, within 15 %):
 //  - a wave of tiles takes its stages, 0.56 us and 0.6 ns a token each for one CTA,
@@ -665,7 +682,7 @@ cudaError_t launch_cg(const Launch& L, const CUtensorMap& tw, const CUtensorMap&
 I8Plan i8_plan(int T, int M, int K)
 {
     I8Plan q{};
-    if (T <= 16 || (T <= I8_FEW_ROWS && (int64_t)M * K <= 16 << 20)) return q;
+    if (few_rows(T, M, K)) return q;
     const int64_t kt = (K + STAGE_K - 1) / STAGE_K, m_tiles = (M + 127ll) / 128, m_pairs = (M + 255ll) / 256;
     double best = 1e30;
     auto take = [&](double us, int cg, int bn, int splits) {
@@ -673,7 +690,7 @@ I8Plan i8_plan(int T, int M, int K)
         best = us;
         q.cg = cg; q.bn = bn; q.splits = splits;
     };
-    for (int bn = 32; bn <= 192; bn += 32) {
+    for (int bn = 32; bn <= 192 && may_pair(T, M, K); bn += 32) {
         const int64_t waves = (m_pairs * ((T + bn - 1) / bn) + I8_SMS / 2 - 1) / (I8_SMS / 2);
         const double stage = bn <= 128 ? 0.28 + 0.0004 * bn : 0.33 + 0.002 * (bn - 128);
         take(10 + 7.5e-7 * T * K + waves * kt * stage, 2, bn, 1);

@@ -472,6 +472,9 @@ cudaError_t launch_i8_few(const Launch& L, const I8MatmulArgs& a);
 // in boxes of bn / 2 rows by 64.
 struct I8Plan { int cg, bn, splits, ns, nb; };
 I8Plan i8_plan(int T, int M, int K);
+// Bytes of workspace that a plan takes, and that serve every plan of at most these sizes
+int64_t i8_workspace(const I8Plan& q, int T, int K);
+int64_t i8_workspace_bound(int T, int M, int K);
 // A pair's workspace: x's copy, then sum |x| of every 1,024 inputs of a token, [..][T]
 inline int64_t i8_copy_row(int K) { return (K + 15ll) / 16 * 16; }
 inline int64_t i8_copy_bytes(int T, int K) { return (T * i8_copy_row(K) * 2 + 255) / 256 * 256; }

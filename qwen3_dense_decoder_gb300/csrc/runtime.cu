@@ -2619,18 +2619,26 @@ int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, i
 }
 
 namespace {
-int64_t i8_workspace(const I8Plan& q, int T, int K)
+int i8_sizes(const char* name, int T, int M, int K, const int64_t* bytes)
 {
-    return q.cg == 2 ? i8_copy_bytes(T, K) + (K + 1023ll) / 1024 * T * (int64_t)sizeof(int) : 0;
+    if (!bytes || T < 0 || T > I8_MAX_ROWS || M < 1 || M > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
+        return fail(Q3_ERR_INVALID_ARG, "%s: bad argument", name);
+    return Q3_OK;
 }
 }  // namespace
 
 int q3_i8_matmul_workspace(int T, int M, int K, int64_t* bytes)
 {
-    if (!bytes || T < 0 || T > I8_MAX_ROWS || M < 1 || M > I8_MAX_ROWS || K < 1 || K > I8_MAX_K)
-        return fail(Q3_ERR_INVALID_ARG, "i8_matmul_workspace: bad argument");
-    *bytes = T ? i8_workspace(i8_plan(T, M, K), T, K) : 0;
-    return Q3_OK;
+    const int rc = i8_sizes("i8_matmul_workspace", T, M, K, bytes);
+    if (rc == Q3_OK) *bytes = T ? i8_workspace_bound(T, M, K) : 0;
+    return rc;
+}
+
+int q3_i8_matmul_workspace_used(int T, int M, int K, int64_t* bytes)
+{
+    const int rc = i8_sizes("i8_matmul_workspace_used", T, M, K, bytes);
+    if (rc == Q3_OK) *bytes = T ? i8_workspace(i8_plan(T, M, K), T, K) : 0;
+    return rc;
 }
 
 int q3_op_i8_matmul(const int8_t* x_dev, int64_t x_stride, const float* x_scales_dev, const int8_t* w_dev, int64_t w_stride,

@@ -83,6 +83,39 @@ constexpr size_t smem_bytes(int cg, int bn, int ns, int nb) {
 // expanding waits for the products, with three (160) it does not
 constexpr __host__ __device__ int a_stages(int bn) { return bn > 160 ? 2 : bn > 128 ? 3 : MAX_NA; }
 
+// Stages of the rings: as many as shared memory takes
+struct Rings { int ns, nb; };
+constexpr Rings rings(int cg, int bn) {
+    Rings r{3, 3};
+    for (bool more = true; more;) {
+        more = false;
+        if (cg == 2 && r.nb < MAX_NS && smem_bytes(cg, bn, r.ns, r.nb + 1) <= MAX_SMEM) ++r.nb, more = true;
+        if (r.ns < MAX_NS && smem_bytes(cg, bn, r.ns + 1, r.nb) <= MAX_SMEM) ++r.ns, more = true;
+    }
+    return r;
+}
+
+// Whether a wait on raw_full tells a stage from the one before it in its slot, ns
+// stages earlier: a parity alone does not, so that the group that waits has to know
+// of the earlier one's copy.  The groups take every other stage: with an even ns it
+// was the group's own.  Else the group knows by its last stage, two earlier, which
+// began with a place of A (and, not for pairs, of B) free: the products that many
+// stages before that were done, and so every copy up to there.
+constexpr bool copies_in_order(int cg, int bn, int ns, int nb) {
+    const int na = a_stages(bn), places = cg == 1 && nb < na ? nb : na;
+    return ns % 2 == 0 || ns >= places + 2;
+}
+constexpr bool all_in_order() {
+    for (int cg = 1; cg <= 2; ++cg)
+        for (int bn = 16 * cg; bn <= (cg == 2 ? 192 : 128); bn += 16 * cg) {
+            const Rings r = rings(cg, bn);
+            if (smem_bytes(cg, bn, r.ns, r.nb) > MAX_SMEM || !copies_in_order(cg, bn, r.ns, r.nb)) return false;
+        }
+    return true;
+}
+static_assert(all_in_order(), "a width whose rings leave the order of copies open");
+static_assert(!copies_in_order(1, 64, 3, 3) && !copies_in_order(2, 96, 5, 5), "rings that leave it open");
+
 template <int R> Q3_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(R)); }
 template <int R> Q3_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(R)); }
 
@@ -708,12 +741,8 @@ I8Plan i8_plan(int T, int M, int K)
             take(6.5 + 0.01 * bn + waves * ((kt + splits - 1) / splits) * (0.56 + 0.0006 * bn) + (splits > 1 ? 1.5 + 0.012 * bn : 0), 1, bn, splits);
         }
     }
-    q.ns = q.nb = 3;
-    for (bool more = true; more;) {
-        more = false;
-        if (q.cg == 2 && q.nb < MAX_NS && smem_bytes(q.cg, q.bn, q.ns, q.nb + 1) <= MAX_SMEM) ++q.nb, more = true;
-        if (q.ns < MAX_NS && smem_bytes(q.cg, q.bn, q.ns + 1, q.nb) <= MAX_SMEM) ++q.ns, more = true;
-    }
+    const Rings r = rings(q.cg, q.bn);
+    q.ns = r.ns; q.nb = r.nb;
     return q;
 }
 
@@ -738,6 +767,7 @@ cudaError_t launch_i8_gemm(const Launch& L, const CUtensorMap& tw, const CUtenso
 {
     // what tcgen05.mma takes: 16 k tokens for 128 channels, 32 k for a pair's 256
     if (q.bn % (16 * q.cg) || q.bn < 16 * q.cg || q.bn > (q.cg == 2 ? 192 : 128)) return cudaErrorInvalidValue;
+    if (!copies_in_order(q.cg, q.bn, q.ns, q.nb)) return cudaErrorInvalidValue;
     I8GemmArgs p{};
     p.a = a;
     if (q.cg == 2) p.l1 = i8_sums(workspace, a.T, a.K);

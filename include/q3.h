@@ -557,7 +557,8 @@ int q3_op_token_logprobs(const void* logits_dev, int type, int64_t stride, int N
  * multiple of 16, at least K), 16-byte aligned; bytes between K and the next row
  * are not written and have no effect.
  * scales_dev: f32 [T].  values_dev: [T][K] of values_type (f32, fp16 or bf16),
- * or NULL, receives scale * code.  Inputs: f32, fp16 or bf16 rows, stride
+ * or NULL, receives scale * code; a value that is no finite number of that type
+ * (fp16: 65,520 or more) is an infinity and sets Q3_STATUS_F16_RANGE.  Inputs: f32, fp16 or bf16 rows, stride
  * elements apart, of any alignment of the type (rows that begin on 16-byte
  * boundaries are read faster).
  *

@@ -435,7 +435,8 @@ def op_i8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: t
     """Rows x [T, K] (f32, fp16 or bf16; rows may be strided) as 8-bit integers:
     (codes int8 [T, K], scales f32 [T]).  The tokens of an activation, or the
     output channels of a weight matrix.  values: f32, fp16 or bf16 [T, K], if
-    given, receives the values that the codes stand for."""
+    given, receives the values that the codes stand for (infinities where that
+    type does not hold them, which status reports)."""
     return _op("i8_quantize")(x, codes, scales, values, status, stream)
 
 

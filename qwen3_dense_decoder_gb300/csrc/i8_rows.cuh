@@ -233,6 +233,17 @@ Q3_DEV void store_codes(const I8RowArgs& a, int64_t r, int tid, int n, int i, co
 template <bool VEC>
 Q3_DEV void gains(const I8RowArgs& a, int tid, int n, int i, float (&g)[8]) { load8<__nv_bfloat16, VEC>(a.gain, tid, n, i, a.K, g); }
 
+// A row's scale, by one thread.  Its largest code is 127 (or the scale 0 or NaN), so
+// that one comparison tells whether every value is a finite number of its type: below
+// the half between that type's largest and the next power of two.
+Q3_DEV void put_scale(const I8RowArgs& a, int64_t r, float scale)
+{
+    a.scales[r] = scale;
+    if (!a.values || !a.status) return;
+    const float limit = a.values_type == Q3_TYPE_F32 ? INFINITY : a.values_type == Q3_TYPE_F16 ? 65520.f : __uint_as_float(0x7f7f8000u);
+    if (!(127.0f * scale < limit)) set_status(a.status, Q3_STATUS_F16_RANGE);
+}
+
 // A row whose steps leave FP32's range, in 64 bits; or one with what is no
 // number, or zeros alone.  Out of line and reading the row again: the FP64 unit
 // is slow, and its code beside the common path's took that one from 131 to 717 us
@@ -258,7 +269,7 @@ __device__ __noinline__ void rare_row(const I8RowArgs& a, int64_t r, int tid, in
     const bool bad = !(scale < INFINITY);
     if (bad) scale = __uint_as_float(0x7fffffffu);
     if (tid == 0) {
-        a.scales[r] = scale;
+        put_scale(a, r, scale);
         if (bad && a.status) set_status(a.status, Q3_STATUS_F16_RANGE);
     }
     const bool zero = bad || scale == 0.f;
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(V ? 640 : 1024) i8_rows_any_kernel(const I8Row
         rare_row<X, OP, VEC>(a, r, tid, n);
         return;
     }
-    if (tid == 0) a.scales[r] = scale;
+    if (tid == 0) put_scale(a, r, scale);
     const float top = __uint_as_float(m);
 #pragma unroll
     for (int i = 0; i < chunks; ++i) {
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(640) i8_rows_kernel(const I8RowArgs a)
         parity ^= 1;
         float scale;
         if (row_scale<OP>(a, m, ss, scale)) {
-            if (tid == 0) a.scales[r] = scale;
+            if (tid == 0) put_scale(a, r, scale);
             const float top = __uint_as_float(m);
 #pragma unroll
             for (int i = 0; i < V; ++i) emit<OP, true, true>(a, r, tid, n, i, y[i], top, scale);

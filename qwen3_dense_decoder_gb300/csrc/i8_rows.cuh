@@ -318,14 +318,12 @@ Q3_DEV bool row_scale(const I8RowArgs& a, uint32_t m, float ss, float& scale)
     return plain;
 }
 
-template <int OP>
 Q3_DEV void max_of(const float (&y)[8], uint32_t& m)
 {
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7fffffffu);
 }
 
-template <int OP>
 Q3_DEV void times_gain(float (&y)[8], const float (&g)[8], float& ss)
 {
 #pragma unroll
@@ -351,12 +349,12 @@ __global__ void __launch_bounds__(V ? 640 : 1024) i8_rows_any_kernel(const I8Row
         float g[8];
         if (OP == NORM) gains<VEC>(a, tid, n, i, g);
         row_values<X, OP, VEC>(a, r, tid, n, i, again, v);
-        if (OP == NORM) times_gain<OP>(v, g, ss);
+        if (OP == NORM) times_gain(v, g, ss);
     };
 #pragma unroll
     for (int i = 0; i < chunks; ++i) {
         values(i, false, y[V ? i : 0]);
-        max_of<OP>(y[V ? i : 0], m);
+        max_of(y[V ? i : 0], m);
     }
     block_join<OP == NORM>(m, ss, 0);
     float scale;
@@ -476,9 +474,9 @@ __global__ void __launch_bounds__(640) i8_rows_kernel(const I8RowArgs a)
             if (OP == NORM) {
                 float g[8];
                 raw_values(gain[i], Q3_TYPE_BF16, g);
-                times_gain<OP>(y[i], g, ss);
+                times_gain(y[i], g, ss);
             }
-            max_of<OP>(y[i], m);
+            max_of(y[i], m);
         }
         const int64_t next = r + gridDim.x;
         if (next < a.T) request(next);

@@ -431,10 +431,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ C
                 plan_at.next();
             }
             // the first chunk as the FP32 that it is, whole numbers from the second on
+            // (every share has a stage, so that there is a first)
             int acc[ACC];
-            if (chunks == 0)
-#pragma unroll
-                for (int j = 0; j < ACC; ++j) acc[j] = 0;
             for (int c = 0; c < chunks && ok; ++c, acc_at.next()) {
                 const uint32_t d = acc_at.slot;
                 if (!(ok = wait_warp(&b.acc_full[d], acc_at.phase, b, status))) break;

@@ -577,7 +577,9 @@ int q3_op_i8_norm(const void* x_dev, int type, int64_t stride, const void* delta
                   int64_t code_stride, float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
 
 /* q3_op_i8_swiglu: y[f] = silu(x[f]) * x[F + f] of rows of 2 F values (gate, then
- * up), silu(z) = z / (1 + e^-z).  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
+ * up), silu(z) = z / (1 + e^-z).  silu and y are FP32 values: below its smallest
+ * normal number they have fewer digits, and a y beyond its range is an infinity.
+ * Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_i8_swiglu(const void* x_dev, int type, int64_t stride, int T, int F, int8_t* codes_dev, int64_t code_stride,
                     float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
 

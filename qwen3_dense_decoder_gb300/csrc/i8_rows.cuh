@@ -17,7 +17,10 @@
 // The maximum is taken over the bits of |y|, where infinities and NaN rank
 // above every number: a row with one of them has scale NaN and zero codes.
 // Rows whose squares, products or reciprocals leave FP32's range take the same
-// steps in 64 bits.
+// steps in 64 bits, and so do rows of zeros, whose maximum has no reciprocal: one
+// of 2,560 values takes 10 to 12 us where another takes 2, one of 17,408 40 to 52
+// where another takes 3 to 4, and 2,048 rows of 5,120 of which half are zeros 108
+// to 176 us where others take 8 to 15 (a batch's padding costs as much).
 #pragma once
 
 #include <type_traits>
@@ -87,7 +90,7 @@ Q3_DEV void store8(X* p, int tid, int n, int i, int K, const float (&v)[8], bool
 // and multiplied into z first, so that FP32 holds every step as long as it holds
 // the result.  From 200 on e is 0, and b goes no further: its product with HI
 // would leave FP32 (|z| above 2.35e38) and what it leaves be infinite.  IEEE expf
-// and division take 35.6 us where this takes 30.7 (2,048 rows of 9,728 fp16).
+// and division take 35.9 us where this takes 30.9 (2,048 rows of 9,728 fp16).
 Q3_DEV float silu(float z)
 {
     constexpr double LOG2E = 1.44269504088896340736;
@@ -297,7 +300,7 @@ Q3_DEV void emit(const I8RowArgs& a, int64_t r, int tid, int n, int i, const flo
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float q = y[e] * inv;
-        // (SwiGLU's y lie nowhere in particular: 30.7 us without, 32.7 with, 2,048 rows of 9,728)
+        // (SwiGLU's y lie nowhere in particular: 30.9 us without, 32.7 with, 2,048 rows of 9,728)
         const float c = (OP == SWIGLU ? q : fmaf(fmaf(-q, top, 127.0f * y[e]), one, q)) + MAGIC;
         bits[e] = __float_as_uint(c);
         code[e] = c - MAGIC;
@@ -517,8 +520,8 @@ cudaError_t launch_one(const Launch& L, K kernel, const I8RowArgs& a, int grid, 
 int threads_for(int K, int V) { return ((K + 8 * V - 1) / (8 * V) + 31) / 32 * 32; }
 
 // One wave of CTAs, 640 threads an SM: what 96 registers a thread let reside
-// (two waves' worth: the norm of 2,048 rows of 5,120 20.8 us, one 19.2; SwiGLU of
-// 2,048 of 9,728 31.8 and 30.6; 34,816 rows of 5,120 quantised 139 and 141).
+// (two waves' worth: the norm of 2,048 rows of 5,120 20.7 us, one 19.1; SwiGLU of
+// 2,048 of 9,728 32.1 and 30.9; 34,816 rows of 5,120 quantised 139 and 140).
 template <typename X, int OP, int V, int DELTA>
 cudaError_t launch_v(const Launch& L, const I8RowArgs& a)
 {
@@ -530,9 +533,9 @@ cudaError_t launch_v(const Launch& L, const I8RowArgs& a)
 
 // Eights a thread: fewer threads a row leave more rows' bytes under way between
 // barriers (34,816 bf16 rows of 5,120: 151 us with two, 141 with four), but the
-// norm's two operands and gains then fill the registers (2,048 rows of 5,120: 19.2 us
-// with two, 22.7 with four; one row of 2,560: 2.5 and 4.6).  SwiGLU differs less (32
-// rows of 9,728: 3.1 and 3.5; 2,048: 30.7 and 29.9).
+// norm's two operands and gains then fill the registers (2,048 rows of 5,120: 19.1 us
+// with two, 22.8 with four; one row of 2,560: 2.5 and 4.4).  SwiGLU differs less (32
+// rows of 9,728: 3.2 and 3.5; 2,048: 30.9 and 30.7).
 template <typename X, int OP, int DELTA>
 cudaError_t launch_rows(const Launch& L, const I8RowArgs& a)
 {

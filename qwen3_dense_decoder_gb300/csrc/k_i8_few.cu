@@ -188,9 +188,11 @@ cudaError_t launch_few(const Launch& L, const I8MatmulArgs& a, int kw)
 
 }  // namespace
 
-// Warps that share a channel's inputs: eight, or four where that leaves four CTAs an
-// SM (19,456 channels of 2,560, one token: 12.8 us with eight, 11.1 with four), and no
-// more than there are steps.  More channels a warp or more steps under way cost
+// Warps that share a channel's inputs: eight, or four where eight, at 16 channels a
+// CTA, would need more than the four CTAs an SM that reside (one token, channels of
+// 2,560: 9,728 of them 7.1 us with eight and 7.7 with four, 9,800 9.7 and 7.9, 19,456
+// 12.6 and 10.8), and no more than there are steps.  Long inputs of many channels
+// lose by it (24,576 of 5,120: 24.9 and 27.5; 16 tokens by 19,456 of 5,120: 25.6 and 30.4).  More channels a warp or more steps under way cost
 // resident warps and more time (13.5 us and 11.8).
 cudaError_t launch_i8_few(const Launch& L, const I8MatmulArgs& a)
 {

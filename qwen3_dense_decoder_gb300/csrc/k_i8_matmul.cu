@@ -6,8 +6,9 @@
 // 128.  So kind::f16 sums chunks of 1,024 inputs in tensor memory, and the
 // epilogue's warps add the chunks as 32-bit integers in registers: the exact
 // whole number, at the 16-bit rate, from 8-bit operands in memory.  Reading a chunk
-// slows the products beside it (2,048 rows by 19,456 x 2,560: 147 us with three
-// chunks a tile, 115 with one), so pairs sum longer ones where the tokens allow it:
+// slows the products beside it (2,048 rows by 19,456 x 2,560: 134 us with codes
+// spread evenly over their range, which take two chunks a tile, 118 with those of
+// normal values, which take one), so pairs sum longer ones where the tokens allow it:
 // no partial sum exceeds 128 sum |x|, known for every token and 1,024 inputs.
 //
 // A CTA (or with CG == 2 a pair of CTAs, each with its own 128 channels and half
@@ -701,15 +702,17 @@ int64_t pair_workspace(int T, int K) { return i8_copy_bytes(T, K) + (K + 1023ll)
 int64_t i8_workspace(const I8Plan& q, int T, int K) { return q.cg == 2 ? pair_workspace(T, K) : 0; }
 int64_t i8_workspace_bound(int T, int M, int K) { return may_pair(T, M, K) ? pair_workspace(T, K) : 0; }
 
-// How a product is shared out: the quickest by what was measured (us, device time;
-// 2,048 x 1,024 to 19,456 x 2,560 and 5,120 x 17,408, 32 to 2,048 tokens, within 15 %):
+// How a product is shared out: the quickest by a model of what was measured (us, device
+// time; of 132 products, 17 to 2,048 tokens by 1,024 x 2,048 to 34,816 x 5,120, nine in
+// ten lie within 15 % of it, the others between 0.79 and 1.24 times):
 //  - a wave of tiles takes its stages, 0.56 us and 0.6 ns a token each for one CTA,
 //    0.28 us and 0.4 ns for a pair, or 0.33 and 2 ns for the tokens beyond 128;
 //  - setting up takes 6.5 us and 10 ns a token, joining a cluster's sums 1.5 us and
 //    12 ns a token more; a pair 9 us, and the expansion before it 1 us and its bytes.
 // Few tokens take launch_i8_few's: 2.5 us and up, but its expansion of x, a warp's own,
-// grows with the tokens (32 by 19,456 x 2,560: 23.8 us, by 2,560 x 4,096 8.6; in pairs
-// or a cluster 18 and 10).
+// grows with the tokens (32 by 19,456 x 2,560: 23.8 us, by 2,560 x 4,096 8.3 to 9.2; in
+// pairs or a cluster 18 and 10).  Above 16 Mi codes the step from 16 to 17 tokens costs
+// up to 11 us (7,168 x 5,120: 10.1 to 20.2; 5,120 x 17,408: 24.3 to 34.5).
 I8Plan i8_plan(int T, int M, int K)
 {
     I8Plan q{};

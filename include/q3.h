@@ -568,9 +568,9 @@ int q3_op_i8_quantize(const void* x_dev, int type, int64_t stride, int T, int K,
                       float* scales_dev, void* values_dev, int values_type, int32_t* status_dev, void* stream);
 
 /* q3_op_i8_norm: y = s / sqrt(mean s^2 + eps) * gain with s = x, or with
- * delta_dev the rounding of x + delta to x's type, which goes to sum_dev (rows
- * sum_stride elements apart; sum_dev may be x_dev, with its stride).  Without
- * delta_dev sum_dev is NULL.  delta has a type of its own.  gain_dev: bf16 [K];
+ * delta_dev x + delta, added in FP32 and rounded to x's type, which goes to sum_dev
+ * (rows sum_stride elements apart; sum_dev may be x_dev, with its stride, and else
+ * overlaps no input).  Without delta_dev sum_dev is NULL.  delta has a type of its own.  gain_dev: bf16 [K];
  * eps finite and at least 0.  Errors: Q3_ERR_INVALID_ARG, Q3_ERR_CUDA. */
 int q3_op_i8_norm(const void* x_dev, int type, int64_t stride, const void* delta_dev, int delta_type, int64_t delta_stride,
                   void* sum_dev, int64_t sum_stride, const void* gain_dev, float eps, int T, int K, int8_t* codes_dev,
